@@ -349,7 +349,118 @@ nf4_status nf4_matmul_ws(const nf4_layer* w, int64_t rows, int64_t cols, nf4_for
                          int32_t backward, const void* x, int64_t m, void* out,
                          int32_t out_fp32, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- the adapted layer ----
+ *
+ * QLoRA keeps the weight frozen in NF4 and trains low-rank adapters on top of
+ * it ("QLoRA" paper summary page, How It Works).  The calls below are one such
+ * layer, forward and backward, around nf4_matmul's product:
+ *   h   = s drop(x) A^T                          nf4_lora_project
+ *   z   = x W^T + h B^T + bias                   nf4_linear, forward
+ *   out = act(z) + residual                        (z kept as preact)
+ *   dz  = dout act'(z), dbias = sum of dz        nf4_act_grad
+ *   dh  = s dz B                                 nf4_lora_project, backward
+ *   dB  = dz^T h,  dA = dh^T drop(x)             nf4_lora_grad
+ *   dx  = dz W + drop(dh A) + residual           nf4_linear, backward
+ * with A [rank x cols], B [rows x rank] and x [m x cols], all row-major.  1 <=
+ * rank <= 128.  16-bit operands are bf16 or fp16, products and sums fp32, each
+ * 16-bit result rounded once (nearest even).  Every result is the same from
+ * run to run; sums over a split axis are added in a fixed order.  Nothing is
+ * kept between calls: calls that share no buffer may overlap, and every call
+ * can be captured into a graph (rng is read on the device, so that a replay
+ * draws a new mask when the program has changed it).
+ *
+ * Dropout.  drop(x) = keep ? x / (1 - p) : 0, the mask a function of (seed,
+ * offset, element index) that is recomputed and never stored, so that the
+ * forward, the gradient and a standalone nf4_dropout agree.  Element e (flat,
+ * row-major, in the [m x cols] tensor) takes 16-bit lane e % 8 (low half
+ * first) of the four words of Philox4x32 with 7 rounds (Salmon, Moraes, Dror
+ * and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) at counter
+ * (e / 8, offset), 64 bits each with the low word first, and key seed; it is
+ * kept iff that lane >= t, t = p in units of 2^-16 (nearest).  1 - p is taken
+ * as (65536 - t) / 65536, so that the mean is kept.  A dropped element is 0
+ * whatever x holds. */
+typedef struct {
+    const uint64_t* rng;   /* device {seed, offset}, 8-byte aligned, read in stream order; unused when p is 0 */
+    float           p;     /* drop probability, 0 <= p <= 65535/65536                                         */
+} nf4_drop;
+
+typedef enum {
+    NF4_ACT_NONE = 0,
+    NF4_ACT_RELU = 1,
+    NF4_ACT_SILU = 2,        /* z / (1 + exp(-z))                                  */
+    NF4_ACT_GELU = 3,        /* z P(z), P the normal distribution function         */
+    NF4_ACT_GELU_TANH = 4    /* its approximation by a tanh                        */
+} nf4_act;
+
+/* What nf4_linear adds to the product; a NULL pointer leaves its term out. */
+typedef struct {
+    const void* u;         /* device [m x rank]; with v, or neither                                   */
+    const void* v;         /* device, forward B [rows x rank], backward A [rank x cols]               */
+    int32_t     rank;      /* 1 .. 128, 0 without u and v                                             */
+    int32_t     act;       /* nf4_act; backward: none                                                 */
+    nf4_drop    drop;      /* of u v, backward only; p = 0: none                                      */
+    const void* bias;      /* device [rows] of fmt.dtype, forward only                                */
+    const void* residual;  /* device, shape and type of out; may be out itself                        */
+    void*       preact;    /* device [m x rows] of fmt.dtype, written with z, forward only; not out   */
+} nf4_epilogue;
+
+/* nf4_matmul_ws with an epilogue: the same operands, kernels, splits and
+ * workspace (nf4_matmul_workspace_bytes), and
+ *   backward 0:  z = x W^T + u v^T + bias;  preact = z;  out = act(z) + residual
+ *   backward 1:  out = x W + drop(u v) + residual
+ * in fp32 before the one rounding of out (and of preact).  All pointers of the
+ * epilogue 16-byte aligned.  epi is host memory, read before the call returns.
+ * act, bias or preact backward, or dropout forward: NF4_E_UNSUPPORTED. */
+nf4_status nf4_linear(const nf4_layer* w, int64_t rows, int64_t cols, nf4_format fmt,
+                      int32_t backward, const void* x, int64_t m, const nf4_epilogue* epi,
+                      void* out, int32_t out_fp32, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* The gradient of that epilogue: dz = dy act'(preact) and, with dbias, the sum
+ * of dz over the m tokens (from the unrounded products).
+ *   dy, preact, dz  device [m x n] of dtype, 16-byte aligned; dz may be dy
+ *   dbias           device fp32 [n], 16-byte aligned, or NULL
+ * NF4_ACT_NONE: preact is not read and may be NULL, and so may dz (dbias
+ * alone).  n a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25.  ws:
+ * nf4_act_grad_workspace_bytes(m, n) with dbias, else unused. */
+nf4_status nf4_act_grad(const void* dy, const void* preact, int32_t act, int64_t m, int64_t n,
+                        int32_t dtype, void* dz, float* dbias, void* ws, size_t ws_bytes,
+                        hipStream_t stream);
+
+/* out = drop(x) over n elements of dtype, rounded once.  x and out 16-byte
+ * aligned; out may be x.  Its own gradient is the same call on the gradient.
+ * 1 <= n < 2^36. */
+nf4_status nf4_dropout(const void* x, int64_t n, int32_t dtype, nf4_drop drop, void* out,
+                       hipStream_t stream);
+
+/* The adapter's down product and its gradient's counterpart, rounded once:
+ *   backward 0: h[m x rank] = scale drop(x) w^T, x [m x k], w [rank x k]  (h = s drop(x) A^T)
+ *   backward 1: h[m x rank] = scale x w,         x [m x k], w [k x rank]  (dh = s dz B)
+ * k a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25; device buffers
+ * of dtype, 16-byte aligned.  Dropout with backward 1: NF4_E_UNSUPPORTED. */
+nf4_status nf4_lora_project(const void* x, int64_t m, int64_t k, const void* w, int32_t rank,
+                            int32_t dtype, int32_t backward, float scale, nf4_drop drop, void* h,
+                            hipStream_t stream);
+
+typedef enum { NF4_LORA_A = 0, NF4_LORA_B = 1 } nf4_lora_side;
+
+/* The adapter's weight gradients, fp32:
+ *   side NF4_LORA_A: grad[rank x n] = u^T drop(x)   (dA, u = dh, x the layer's input)
+ *   side NF4_LORA_B: grad[n x rank] = x^T u         (dB, u = h, x = dz)
+ * u [m x rank] and x [m x n] of dtype, grad fp32, all 16-byte aligned; n a
+ * multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25.  Dropout on side B:
+ * NF4_E_UNSUPPORTED.  ws: nf4_lora_grad_workspace_bytes(m, n, rank), may be
+ * NULL when that is 0. */
+nf4_status nf4_lora_grad(const void* u, const void* x, int64_t m, int64_t n, int32_t rank,
+                         int32_t dtype, int32_t side, nf4_drop drop, float* grad, void* ws,
+                         size_t ws_bytes, hipStream_t stream);
+
 /* ---- host-only helpers (pure; no HIP calls) ---- */
+
+/* Workspaces of nf4_act_grad (fp32 partial column sums, one row per block of
+ * tokens) and nf4_lora_grad (one fp32 partial gradient per split of the
+ * tokens); 0 when one block or split does it, or on bad input. */
+size_t      nf4_act_grad_workspace_bytes(int64_t m, int64_t n);
+size_t      nf4_lora_grad_workspace_bytes(int64_t m, int64_t n, int32_t rank);
 
 /* Workspace of nf4_matmul_ws for this shape: parts * m * (rows | cols) fp32
  * partials when the whole reduction is split, parts * leftover tiles * 256 *

@@ -8,6 +8,9 @@ missing library raises instead of falling back.
 
     nf4_quantize, nf4_double_quant, nf4_dequantize, nf4_dequantize_masked,
     nf4_layer_error, aqlora_select_topk     -- enqueue on the current stream
+    nf4_linear, nf4_act_grad, nf4_dropout, nf4_lora_project, nf4_lora_grad
+                                            -- one adapted layer, on the
+                                               tensors' device
     nf4_workspace_bytes, aqlora_workspace_bytes, nf4_storage_bytes,
     aqlora_promote_cost, nf4_levels, nf4_thresholds, nf4_abi_version
                                             -- host-only helpers
@@ -55,6 +58,21 @@ class nf4_variant(ctypes.Structure):
 NF4_DQ_NONE, NF4_DQ_INT8, NF4_DQ_INT8_MEAN, NF4_DQ_E4M3_MEAN = range(4)
 
 
+NF4_ACT_NONE, NF4_ACT_RELU, NF4_ACT_SILU, NF4_ACT_GELU, NF4_ACT_GELU_TANH = range(5)
+NF4_LORA_A, NF4_LORA_B = 0, 1
+LORA_MAX_RANK = 128
+
+
+class nf4_drop(ctypes.Structure):
+    _fields_ = [("rng", ctypes.c_void_p), ("p", ctypes.c_float)]
+
+
+class nf4_epilogue(ctypes.Structure):
+    _fields_ = [("u", ctypes.c_void_p), ("v", ctypes.c_void_p), ("rank", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("drop", nf4_drop), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("preact", ctypes.c_void_p)]
+
+
 class nf4_layer(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("w", ctypes.c_void_p), ("codes", ctypes.c_void_p),
                 ("absmax", ctypes.c_void_p), ("qabsmax", ctypes.c_void_p),
@@ -99,6 +117,23 @@ EXPORTS = {
                                      ctypes.c_size_t, ctypes.c_void_p]),
     "nf4_matmul_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
                                                      ctypes.c_int64]),
+    "nf4_linear": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, nf4_format,
+                                  ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+                                  ctypes.c_void_p]),
+    "nf4_act_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+                                    ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "nf4_dropout": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, nf4_drop,
+                                   ctypes.c_void_p, ctypes.c_void_p]),
+    "nf4_lora_project": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                        nf4_drop, ctypes.c_void_p, ctypes.c_void_p]),
+    "nf4_lora_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                     ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, nf4_drop,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "nf4_act_grad_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
+    "nf4_lora_grad_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32]),
     "nf4_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_void_p, nf4_format]),
     "nf4_layer_error_variant": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, nf4_variant,
                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
@@ -305,6 +340,179 @@ def nf4_workspace_bytes_variant(ns, v: nf4_variant) -> int:
 
 def nf4_storage_bytes_variant(n: int, v: nf4_variant) -> int:
     return int(lib().nf4_storage_bytes_variant(int(n), v))
+
+
+# ---- the adapted layer ----------------------------------------------------
+#
+# Unlike the codec calls, these take their shapes from the tensors, so they
+# check them: what does not fit raises NF4Error with NF4_E_ARG (or the status
+# the C call returns) and enqueues nothing.  Work goes to the current stream of
+# the tensors' device, or to `stream`, which must be one of that device's.
+
+def _need(cond: bool, where: str, what: str) -> None:
+    if not cond:
+        e = NF4Error(NF4_E_ARG, where)
+        e.args = (f"{e.args[0]}: {what}",)
+        raise e
+
+
+def _dtype16(t, where: str) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return NF4_BF16
+    _need(t.dtype == torch.float16, where, f"bfloat16 or float16 expected, got {t.dtype}")
+    return NF4_FP16
+
+
+def _fits(t, name: str, where: str, shape, dtype, device) -> int:
+    """The address of a tensor that must have this shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        _need(False, where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                            f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rng_arg(p: float, rng, where: str, device) -> nf4_drop:
+    if not p:
+        return nf4_drop(None, 0.0)
+    import torch
+    _need(rng is not None, where, "dropout needs rng")
+    _need(rng.numel() == 2 and rng.dtype in (torch.int64, torch.uint64) and rng.device == device
+          and rng.is_contiguous(), where, f"rng must hold {{seed, offset}} as 64-bit integers on {device}")
+    return nf4_drop(rng.data_ptr(), float(p))
+
+
+def _ws_arg(ws, where: str, device):
+    if ws is None:
+        return None, 0
+    _need(ws.device == device and ws.is_contiguous(), where, f"the workspace must be a contiguous tensor on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _enqueue(fn, where: str, device, stream, *args) -> None:
+    """fn(*args, stream) with the tensors' device current."""
+    import torch
+    _need(device.type == "cuda", where, f"tensors must be on the GPU, got {device}")
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(stream))
+    if st != NF4_OK:
+        raise NF4Error(st, where)
+
+
+def nf4_linear(layer, rows: int, cols: int, f: nf4_format, x, out, ws=None, backward: bool = False, lora=None,
+               bias=None, act: int = NF4_ACT_NONE, preact=None, residual=None, p: float = 0.0, rng=None,
+               stream=None) -> None:
+    """Forward: out = act(z) + residual, z = x W^T + u v^T + bias, preact = z.
+    Backward: out = x W + drop(u v) + residual.  W [rows x cols] in NF4 form
+    (layer: an nf4_layer struct), lora = (u, v): u [m, rank] and v [rows, rank]
+    forward, [rank, cols] backward.  x, u, v, bias, preact in the 16-bit type f
+    names; out that type or float32, residual like out (it may be out).  ws:
+    device tensor of nf4_matmul_workspace_bytes(rows, cols, backward, m) bytes,
+    or None when that is 0."""
+    import torch
+    w = "nf4_linear"
+    dev, t16 = x.device, torch.bfloat16 if f.dtype == NF4_BF16 else torch.float16
+    m = x.shape[0] if x.dim() == 2 else 1
+    kred, ncol = (rows, cols) if backward else (cols, rows)
+    xs = torch.Size((m, kred)) if x.dim() == 2 else torch.Size((kred,))
+    xp = _fits(x, "x", w, xs, t16, dev)
+    os_ = torch.Size((m, ncol)) if out.dim() == 2 else torch.Size((m * ncol,))
+    _need(out.dtype in (t16, torch.float32) and (out.dim() == 2 or m == 1), w, "out must be [m, columns] in f's 16-bit type or float32")
+    op = _fits(out, "out", w, os_, out.dtype, dev)
+    e = nf4_epilogue()
+    if lora is not None:
+        u, v = lora
+        r = u.shape[-1] if u.dim() else 0
+        e.u = _fits(u, "u", w, torch.Size((m, r)) if u.dim() == 2 else torch.Size((m * r,)), t16, dev)
+        e.v = _fits(v, "v", w, torch.Size((r, cols) if backward else (rows, r)), t16, dev)
+        e.rank = r
+    e.act = int(act)
+    e.drop = _rng_arg(p, rng, w, dev)
+    if bias is not None:
+        e.bias = _fits(bias, "bias", w, torch.Size((ncol,)), t16, dev)
+    if preact is not None:
+        e.preact = _fits(preact, "preact", w, os_, t16, dev)
+    if residual is not None:
+        e.residual = _fits(residual, "residual", w, os_, out.dtype, dev)
+    wp, wb = _ws_arg(ws, w, dev)
+    _enqueue(lib().nf4_linear, w, dev, stream, ctypes.byref(layer), int(rows), int(cols), f, int(bool(backward)), xp, m,
+             ctypes.byref(e), op, 1 if out.dtype == torch.float32 else 0, wp, wb)
+
+
+def nf4_act_grad(dy, preact, act: int, dz=None, dbias=None, ws=None, stream=None) -> None:
+    """dz = dy act'(preact) and, with dbias (float32 [n]), its sum over the
+    tokens.  dy, preact, dz: [m, n], bfloat16 or float16; dz may be dy.  With
+    NF4_ACT_NONE preact and dz may be None.  ws: device tensor of
+    nf4_act_grad_workspace_bytes(m, n) bytes with dbias."""
+    import torch
+    w = "nf4_act_grad"
+    dt, dev = _dtype16(dy, w), dy.device
+    _need(dy.dim() == 2, w, "dy must be [m, n]")
+    m, n = dy.shape
+    dp = _fits(dy, "dy", w, dy.shape, dy.dtype, dev)
+    pp = None if preact is None else _fits(preact, "preact", w, dy.shape, dy.dtype, dev)
+    zp = None if dz is None else _fits(dz, "dz", w, dy.shape, dy.dtype, dev)
+    bp = None if dbias is None else _fits(dbias, "dbias", w, torch.Size((n,)), torch.float32, dev)
+    wp, wb = _ws_arg(ws, w, dev)
+    _enqueue(lib().nf4_act_grad, w, dev, stream, dp, pp, int(act), m, n, dt, zp, bp, wp, wb)
+
+
+def nf4_act_grad_workspace_bytes(m: int, n: int) -> int:
+    return int(lib().nf4_act_grad_workspace_bytes(int(m), int(n)))
+
+
+def nf4_dropout(x, out, p: float, rng, stream=None) -> None:
+    """out = drop(x) (bfloat16 or float16, any shape; out may be x): the mask of
+    rng (device int64 {seed, offset}) over the flat elements."""
+    w = "nf4_dropout"
+    dt, dev = _dtype16(x, w), x.device
+    xp = _fits(x, "x", w, x.shape, x.dtype, dev)
+    op = _fits(out, "out", w, x.shape, x.dtype, dev)
+    _enqueue(lib().nf4_dropout, w, dev, stream, xp, x.numel(), dt, _rng_arg(p, rng, w, dev), op)
+
+
+def nf4_lora_project(x, w, h, scale: float = 1.0, backward: bool = False, p: float = 0.0, rng=None,
+                     stream=None) -> None:
+    """h [m, rank] = scale drop(x) w^T (x [m, k], w [rank, k]), or backward
+    scale x w (w [k, rank]); bfloat16 or float16."""
+    import torch
+    fn = "nf4_lora_project"
+    dt, dev = _dtype16(x, fn), x.device
+    _need(x.dim() == 2 and w.dim() == 2, fn, "x and w must have two dimensions")
+    m, k = x.shape
+    r = w.shape[1 if backward else 0]
+    xp = _fits(x, "x", fn, x.shape, x.dtype, dev)
+    wp = _fits(w, "w", fn, torch.Size((k, r) if backward else (r, k)), x.dtype, dev)
+    hp = _fits(h, "h", fn, torch.Size((m, r)), x.dtype, dev)
+    _enqueue(lib().nf4_lora_project, fn, dev, stream, xp, m, k, wp, r, dt, int(bool(backward)), float(scale),
+             _rng_arg(p, rng, fn, dev), hp)
+
+
+def nf4_lora_grad(u, x, grad, ws=None, side: str = "A", p: float = 0.0, rng=None, stream=None) -> None:
+    """side "A": grad [rank, n] = u^T drop(x); side "B": grad [n, rank] =
+    x^T u.  u [m, rank], x [m, n] bfloat16 or float16, grad float32.  ws:
+    device tensor of nf4_lora_grad_workspace_bytes(m, n, rank) bytes, or None
+    when that is 0."""
+    import torch
+    fn = "nf4_lora_grad"
+    dt, dev = _dtype16(x, fn), x.device
+    _need(x.dim() == 2 and u.dim() == 2, fn, "u and x must have two dimensions")
+    _need(side in ("A", "B"), fn, "side must be 'A' or 'B'")
+    m, n = x.shape
+    r = u.shape[1]
+    xp = _fits(x, "x", fn, x.shape, x.dtype, dev)
+    up = _fits(u, "u", fn, torch.Size((m, r)), x.dtype, dev)
+    gp = _fits(grad, "grad", fn, torch.Size((r, n) if side == "A" else (n, r)), torch.float32, dev)
+    wp, wb = _ws_arg(ws, fn, dev)
+    _enqueue(lib().nf4_lora_grad, fn, dev, stream, up, xp, m, n, r, dt, NF4_LORA_A if side == "A" else NF4_LORA_B,
+             _rng_arg(p, rng, fn, dev), gp, wp, wb)
+
+
+def nf4_lora_grad_workspace_bytes(m: int, n: int, rank: int) -> int:
+    return int(lib().nf4_lora_grad_workspace_bytes(int(m), int(n), int(rank)))
 
 
 # ---- host helpers ---------------------------------------------------------

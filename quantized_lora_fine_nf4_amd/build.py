@@ -1,6 +1,7 @@
 """Compile the HIP library ``libnf4.so`` for gfx950, in-tree.
 
-hipcc cross-compiles without a GPU.  Flags: no fast-math and no FMA
+hipcc cross-compiles without a GPU, one process per source (the matmul files
+take about a minute each).  Flags: no fast-math and no FMA
 contraction (the codec's fp32 steps are specified as separately rounded
 operations), packed fp32 instructions off, fp32 denormals kept (the default).
 """
@@ -9,6 +10,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,18 +19,22 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_PATH = os.path.join(PKG, "libnf4.so")
 CPU_LIB_PATH = os.path.join(PKG, "libnf4cpu.so")
 CPU_SOURCES = [os.path.join("cpu", "nf4_cpu.cpp")]
-SOURCES = ["k_codec.hip", "k_select.hip", "k_gemm.hip", "k_variants.hip", "nf4_scratch.hip",
-           "nf4_api.cpp"]
+SOURCES = ["k_gemm.hip", "k_linear.hip", "k_codec.hip", "k_select.hip", "k_lora.hip", "k_variants.hip",
+           "nf4_scratch.hip", "nf4_api.cpp"]
 ARCH = os.environ.get("NF4_OFFLOAD_ARCH", "gfx950")
 
 
-def command(out: str = LIB_PATH) -> list:
-    return ["hipcc", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+def compile_command(source: str, out: str) -> list:
+    return ["hipcc", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
             "-ffp-contract=off", "-fno-fast-math",
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-Wall", "-Wno-unused-command-line-argument",
             "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-            "-o", out, *[os.path.join(CSRC, s) for s in SOURCES]]
+            "-c", "-o", out, os.path.join(CSRC, source)]
+
+
+def link_command(objects: list, out: str = LIB_PATH) -> list:
+    return ["hipcc", f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", out, *objects]
 
 
 def cpu_command(out: str = CPU_LIB_PATH) -> list:
@@ -51,9 +58,7 @@ def build_cpu(verbose: bool = False) -> str:
     return CPU_LIB_PATH
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB_PATH + ".tmp"
-    cmd = command(tmp)
+def _hipcc(cmd: list, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -64,6 +69,16 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{err}")
     if err and verbose:
         print(err, file=sys.stderr)
+
+
+def build(verbose: bool = False) -> str:
+    tmp = LIB_PATH + ".tmp"
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, s + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            for f in [pool.submit(_hipcc, compile_command(s, o), verbose) for s, o in zip(SOURCES, objects)]:
+                f.result()
+        _hipcc(link_command(objects, tmp), verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

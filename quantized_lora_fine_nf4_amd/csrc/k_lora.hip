@@ -1,0 +1,613 @@
+// k_lora.hip -- the small operators of an adapted NF4 layer on gfx950: dropout
+// from a counter-based mask, the gradient of the matmul's epilogue, and the
+// low-rank adapter's products ("QLoRA" paper summary page, How It Works: the
+// 4-bit weight stays frozen and low-rank adapters are trained on top of it).
+//
+//   dropout   y = keep ? c x : 0
+//   act_grad  dz = dy act'(z), dbias = sum over tokens of dz
+//   project   h = s c (keep . x) A^T      (forward;  x m x k, A rank x k)
+//             h = s x B                   (backward; x m x k, B k x rank)
+//   grad      dA = c u^T (keep . x), dB = x^T u   (x m x n, u m x rank)
+//
+// All sums are fp32, in an order fixed by the shape, so every result is bitwise
+// reproducible; 16-bit results are rounded once, at the store.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "nf4_act.h"
+#include "nf4_launch.h"
+#include "nf4_philox.h"
+
+namespace nf4k {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+#define GLOBAL __attribute__((address_space(1)))
+
+template <int DT> struct Frag { typedef bf16x8 T; };
+template <> struct Frag<1> { typedef f16x8 T; };
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c)
+{
+    typedef typename Frag<DT>::T F;
+    if constexpr (DT == 0)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(F, a), __builtin_bit_cast(F, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(F, a), __builtin_bit_cast(F, b), c, 0, 0, 0);
+}
+
+// Two packed 16-bit values to fp32 and back (nearest, ties to even).
+template <int DT>
+__device__ __forceinline__ f32x2 unpack2(uint32_t v)
+{
+    if constexpr (DT == 0)
+        return f32x2{__builtin_bit_cast(float, v << 16), __builtin_bit_cast(float, v & 0xffff0000u)};
+    else return __builtin_convertvector(__builtin_bit_cast(f16x2, v), f32x2);
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const f32x2 in = {a, b};
+    if constexpr (DT == 0) return __builtin_bit_cast(uint32_t, __builtin_convertvector(in, bf16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(in, f16x2));
+}
+
+template <int DT>
+__device__ __forceinline__ uint16_t pack1(float a) { return (uint16_t)pack2<DT>(a, 0.0f); }
+
+// ---- dropout
+//
+// Memory-bound: 4 bytes per element, one mask group (eight elements, 16 bytes)
+// per thread and step.
+constexpr int kDropGroups = 4;   // groups per thread
+
+template <int DT>
+__device__ __forceinline__ u32x4 drop8(const u32x4& x, const Bits128& b, uint32_t thr, float keep)
+{
+    u32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const f32x2 v = unpack2<DT>(x[j]);
+        r[j] = pack2<DT>(v.x * keep, v.y * keep) & keep_mask2(b.w[j], thr);
+    }
+    return r;
+}
+
+// DROP false (probability 0, no rng): a copy.
+template <int DT, bool DROP>
+__global__ __launch_bounds__(256) void k_dropout(const uint16_t* x, int64_t n, DropArgs d, uint16_t* out)
+{
+    PhiloxKey key = {};
+    if constexpr (DROP) key = philox_key(d.rng);
+    const int64_t groups = n >> 3, g0 = (int64_t)blockIdx.x * (256 * kDropGroups) + threadIdx.x;
+    u32x4 v[kDropGroups];
+#pragma unroll
+    for (int i = 0; i < kDropGroups; ++i) {
+        const int64_t g = g0 + 256 * i;
+        if (g < groups) v[i] = ((const GLOBAL u32x4*)x)[g];
+    }
+#pragma unroll
+    for (int i = 0; i < kDropGroups; ++i) {
+        const int64_t g = g0 + 256 * i;
+        if (g >= groups) continue;
+        if constexpr (DROP) v[i] = drop8<DT>(v[i], philox7(key, (uint64_t)g), d.thr, d.keep);
+        ((GLOBAL u32x4*)out)[g] = v[i];
+    }
+    // the last partial group, element by element
+    if (blockIdx.x == 0 && threadIdx.x == 0 && (n & 7)) {
+        uint32_t bits = 255;
+        if constexpr (DROP) bits = keep_bits8(philox7(key, (uint64_t)groups), d.thr);
+        for (int i = 0; i < (int)(n & 7); ++i) {
+            const f32x2 v1 = unpack2<DT>(x[8 * groups + i]);
+            out[8 * groups + i] = (bits >> i & 1) ? pack1<DT>(v1.x * d.keep) : (uint16_t)0;
+        }
+    }
+}
+
+template <int DT>
+hipError_t dropout_go(const uint16_t* x, int64_t n, DropArgs d, uint16_t* out, unsigned blocks, hipStream_t s)
+{
+    if (d.thr) hipLaunchKernelGGL((k_dropout<DT, true>), dim3(blocks), dim3(256), 0, s, x, n, d, out);
+    else hipLaunchKernelGGL((k_dropout<DT, false>), dim3(blocks), dim3(256), 0, s, x, n, d, out);
+    return hipGetLastError();
+}
+
+// ---- gradient of the epilogue
+//
+// Memory-bound: 6 bytes per element.  A workgroup takes 8 L columns (L lanes
+// of eight, a power of two up to 64) and `rows` rows per lane; the column
+// sums are kept per lane over its rows, added over the workgroup's rows in
+// LDS and stored as one partial row per row block, added in block order by
+// k_sum_parts.
+
+struct ActArgs {
+    const uint16_t* dy;
+    const uint16_t* z;
+    uint16_t* dz;      // null: no dz (activation none)
+    float* part;       // fp32 partials [row blocks][n], or dbias itself with one block; null: no bias gradient
+    int64_t m, n;
+    int act, lshift;   // L = 1 << lshift
+    int64_t rows;      // rows per lane
+};
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_act_grad(ActArgs g)
+{
+    __shared__ __attribute__((aligned(16))) float s_sum[256 * 8];
+    const int t = threadIdx.x, L = 1 << g.lshift, lane = t & (L - 1), row0 = t >> g.lshift, nrow = 256 >> g.lshift;
+    const int64_t col = ((int64_t)blockIdx.y * L + lane) * 8;
+    const int64_t m0 = (int64_t)blockIdx.x * nrow * g.rows + row0;
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+    if (col < g.n) {
+        for (int64_t r = 0; r < g.rows; ++r) {
+            const int64_t row = m0 + r * nrow;
+            if (row >= g.m) break;
+            const int64_t at = row * g.n + col;
+            const u32x4 dy = *(const GLOBAL u32x4*)(g.dy + at);
+            u32x4 zv = {0, 0, 0, 0};
+            if (g.act != ACT_NONE) zv = *(const GLOBAL u32x4*)(g.z + at);
+            u32x4 o;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f32x2 v = unpack2<DT>(dy[j]);
+                const f32x2 z = unpack2<DT>(zv[j]);
+                v.x *= act_slope(z.x, g.act);
+                v.y *= act_slope(z.y, g.act);
+                sum[2 * j] += v.x;
+                sum[2 * j + 1] += v.y;
+                o[j] = pack2<DT>(v.x, v.y);
+            }
+            if (g.dz) *(GLOBAL u32x4*)(g.dz + at) = o;
+        }
+    }
+    if (!g.part) return;   // uniform
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_sum[t * 8 + i] = sum[i];
+    __syncthreads();
+    // column c of the workgroup: the rows' sums in row order
+    for (int c = t; c < 8 * L; c += 256) {
+        float a = 0.0f;
+        for (int r = 0; r < nrow; ++r) a += s_sum[(r << g.lshift) * 8 + c];
+        const int64_t cc = (int64_t)blockIdx.y * L * 8 + c;
+        if (cc < g.n) ((GLOBAL float*)g.part)[(int64_t)blockIdx.x * g.n + cc] = a;
+    }
+}
+
+// out[i] = scale * (part[0][i] + part[1][i] + ...), in part order; n a multiple of 4.
+__global__ __launch_bounds__(256) void k_sum_parts(const float* part, int nparts, int64_t n, float scale, float* out)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    f32x4 a = *(const GLOBAL f32x4*)(part + i);
+    for (int p = 1; p < nparts; ++p) a += *(const GLOBAL f32x4*)(part + (int64_t)p * n + i);
+    *(GLOBAL f32x4*)(out + i) = a * scale;
+}
+
+// ---- the adapter's down product
+//
+// h[m x rank] = alpha (keep . x) W, reduction over k.  A workgroup takes
+// 16 MB rows of x and 16 RT ranks; its waves share the reduction in chunks of
+// 128 k (four 16 x 16 x 32 MFMA steps; lane l holds x row l % 16, k 8 (l / 16)
+// .. + 7 of a step), and their sums are added pairwise in LDS.
+struct ProjArgs {
+    const uint16_t* x;    // [m x k]
+    const uint16_t* w;    // forward [rank x k], backward [k x rank]
+    uint16_t* h;          // [m x rank]
+    int64_t m, k;
+    int rank;
+    float alpha;          // scale (times the dropout factor)
+    DropArgs drop;
+};
+
+template <int DT, bool BWD, bool DROP, int MB, int RT>
+__global__ __launch_bounds__(1024) void k_lora_project(ProjArgs g)
+{
+    extern __shared__ __attribute__((aligned(16))) float s_acc[];   // [waves / 2][64 lanes][4 MB RT]
+    const int t = threadIdx.x, lane = t & 63, wv = t >> 6, nw = blockDim.x >> 6;
+    const int q = lane & 15, kg = lane >> 4;
+    const int64_t m0 = (int64_t)blockIdx.x * (16 * MB);
+    const int r0 = blockIdx.y * (16 * RT);
+    PhiloxKey key = {};
+    if constexpr (DROP) key = philox_key(g.drop.rng);
+    int64_t xrow[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        const int64_t r = m0 + 16 * b + q;
+        xrow[b] = (r < g.m ? r : g.m - 1) * g.k;
+    }
+    int rk[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+        const int r = r0 + 16 * j + q;
+        rk[j] = r < g.rank ? r : g.rank - 1;
+    }
+    f32x4 acc[MB][RT];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t k0 = (int64_t)wv * 128; k0 < g.k; k0 += (int64_t)nw * 128) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int64_t kk = k0 + 32 * s + 8 * kg;
+            const bool in = kk < g.k;
+            const int64_t kc = in ? kk : g.k - 8;
+            u32x4 a[MB];
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                a[b] = *(const GLOBAL u32x4*)(g.x + xrow[b] + kc);
+                if constexpr (DROP) {
+                    const Bits128 bits = philox7(key, (uint64_t)(xrow[b] + kc) >> 3);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[b][j] &= keep_mask2(bits.w[j], g.drop.thr);
+                }
+                if (!in) a[b] = u32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                u32x4 w;
+                if constexpr (!BWD) {
+                    w = *(const GLOBAL u32x4*)(g.w + (int64_t)rk[j] * g.k + kc);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const GLOBAL uint16_t* p = (const GLOBAL uint16_t*)g.w + (kc + 2 * e) * g.rank + rk[j];
+                        w[e] = (uint32_t)p[0] | ((uint32_t)p[g.rank] << 16);
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < MB; ++b) acc[b][j] = mfma<DT>(a[b], w, acc[b][j]);
+            }
+        }
+    }
+    // pairwise over the waves (a power of two of them)
+    for (int half = nw >> 1; half > 0; half >>= 1) {
+        if (wv >= half && wv < 2 * half) {
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+#pragma unroll
+                for (int j = 0; j < RT; ++j)
+                    *(f32x4*)(s_acc + (((wv - half) * MB * RT + b * RT + j) * 64 + lane) * 4) = acc[b][j];
+        }
+        __syncthreads();
+        if (wv < half) {
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+#pragma unroll
+                for (int j = 0; j < RT; ++j)
+                    acc[b][j] += *(const f32x4*)(s_acc + ((wv * MB * RT + b * RT + j) * 64 + lane) * 4);
+        }
+        __syncthreads();
+    }
+    if (wv != 0) return;
+    // lane l, value i: row 4 (l / 16) + i, rank l % 16
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = m0 + 16 * b + 4 * kg + i;
+                const int r = r0 + 16 * j + q;
+                if (row < g.m && r < g.rank)
+                    ((GLOBAL uint16_t*)g.h)[row * g.rank + r] = pack1<DT>(acc[b][j][i] * g.alpha);
+            }
+}
+
+// ---- the adapter's gradients
+//
+// G[rank x n] = u^T (keep . x), reduction over the m tokens, which are the
+// slow index of both operands.  Lane l loads eight consecutive columns
+// n0 + 8 (l % 16) of the eight rows m0 + 8 (l / 16) + i (16 bytes each) and
+// transposes the 8 x 8 block in registers with byte permutes: column c of the
+// block is the lane's fragment of MFMA c (16 x 16 x 32), whose 16 columns are
+// n0 + 8 q + c, q = 0 .. 15.  A wave covers 128 columns and 16 RT ranks, the
+// waves of a workgroup share its rows, and their sums are added in LDS.
+struct GradArgs {
+    const uint16_t* u;     // [m x rank]
+    const uint16_t* x;     // [m x n]
+    float* out;            // the result, or fp32 partials [splits][result]
+    int64_t m, n;
+    int rank;
+    bool by_col;           // result layout: [n x rank] instead of [rank x n]
+    int64_t rows_split;    // rows per split, a multiple of 32
+    float scale;           // applied here when there is one split
+    DropArgs drop;
+};
+
+constexpr int kGradWaves = 4;
+
+template <int DT, bool DROP, int RT>
+__global__ __launch_bounds__(64 * kGradWaves) void k_lora_grad(GradArgs g)
+{
+    __shared__ __attribute__((aligned(16))) f32x4 s_acc[(kGradWaves / 2) * 8 * RT * 64];
+    const int t = threadIdx.x, lane = t & 63, wv = t >> 6, q = lane & 15, mg = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 128 + 8 * q;
+    const int64_t nc = n0 < g.n ? n0 : g.n - 8;
+    const int r0 = blockIdx.z * (16 * RT);
+    const int64_t s0 = (int64_t)blockIdx.y * g.rows_split;
+    const int64_t s1 = s0 + g.rows_split < g.m ? s0 + g.rows_split : g.m;
+    PhiloxKey key = {};
+    if constexpr (DROP) key = philox_key(g.drop.rng);
+    int rk[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+        const int r = r0 + 16 * j + q;
+        rk[j] = r < g.rank ? r : g.rank - 1;
+    }
+    f32x4 acc[RT][8];
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[j][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t m0 = s0 + 32 * wv; m0 < s1; m0 += 32 * kGradWaves) {
+        u32x4 x[8];
+        u32x4 a[RT];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t row = m0 + 8 * mg + i;
+            x[i] = *(const GLOBAL u32x4*)(g.x + (row < s1 ? row : s1 - 1) * g.n + nc);
+        }
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = m0 + 8 * mg + 2 * i;
+                const uint32_t lo = ((const GLOBAL uint16_t*)g.u)[(row < s1 ? row : s1 - 1) * g.rank + rk[j]];
+                const uint32_t hi = ((const GLOBAL uint16_t*)g.u)[(row + 1 < s1 ? row + 1 : s1 - 1) * g.rank + rk[j]];
+                a[j][i] = lo | (hi << 16);
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t row = m0 + 8 * mg + i;
+            if constexpr (DROP) {
+                const Bits128 bits = philox7(key, (uint64_t)(row * g.n + nc) >> 3);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[i][j] &= keep_mask2(bits.w[j], g.drop.thr);
+            }
+            if (row >= s1) x[i] = u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
+            u32x4 b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = __builtin_amdgcn_perm(x[2 * i + 1][c >> 1], x[2 * i][c >> 1], sel);
+#pragma unroll
+            for (int j = 0; j < RT; ++j) acc[j][c] = mfma<DT>(a[j], b, acc[j][c]);
+        }
+    }
+#pragma unroll
+    for (int half = kGradWaves / 2; half > 0; half >>= 1) {
+        if (wv >= half && wv < 2 * half) {
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) s_acc[((wv - half) * RT * 8 + j * 8 + c) * 64 + lane] = acc[j][c];
+        }
+        __syncthreads();
+        if (wv < half) {
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) acc[j][c] += s_acc[(wv * RT * 8 + j * 8 + c) * 64 + lane];
+        }
+        __syncthreads();
+    }
+    if (wv != 0 || n0 >= g.n) return;
+    // lane l, value i of acc[j][c]: rank r0 + 16 j + 4 (l / 16) + i, column n0 + c
+    GLOBAL float* out = (GLOBAL float*)g.out + (int64_t)blockIdx.y * g.rank * g.n;
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 16 * j + 4 * mg + i;
+            if (r >= g.rank) continue;
+            if (g.by_col) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) out[(n0 + c) * g.rank + r] = acc[j][c][i] * g.scale;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; c += 4)
+                    *(GLOBAL f32x4*)(out + (int64_t)r * g.n + n0 + c) =
+                        f32x4{acc[j][c][i], acc[j][c + 1][i], acc[j][c + 2][i], acc[j][c + 3][i]} * g.scale;
+            }
+        }
+}
+
+constexpr int64_t kMaxGrid = (int64_t(1) << 32) / 256 - 1;
+
+}  // namespace
+
+hipError_t launch_dropout(int dtype, const void* x, int64_t n, DropArgs d, void* out, hipStream_t s)
+{
+    const int64_t per = 8 * 256 * kDropGroups, blocks = (n + per - 1) / per;
+    if (blocks > kMaxGrid) return hipErrorInvalidValue;
+    const uint16_t* xi = static_cast<const uint16_t*>(x);
+    uint16_t* o = static_cast<uint16_t*>(out);
+    return dtype == 0 ? dropout_go<0>(xi, n, d, o, (unsigned)blocks, s) : dropout_go<1>(xi, n, d, o, (unsigned)blocks, s);
+}
+
+namespace {
+
+// Lanes of eight columns per row: the power of two that covers n, at most 64.
+int act_lshift(int64_t n)
+{
+    int l = 0;
+    while (l < 6 && (int64_t(8) << l) < n) ++l;
+    return l;
+}
+
+// Rows per lane: eight (32 rows and a 4% partial per workgroup at 64 lanes),
+// more where that would make over 4,096 workgroups.
+int64_t act_rows(int64_t m, int64_t n)
+{
+    const int ls = act_lshift(n);
+    const int64_t cols = int64_t(8) << ls, gy = (n + cols - 1) / cols, lrows = (m + (256 >> ls) - 1) / (256 >> ls);
+    const int64_t target = 4096 / gy > 1 ? 4096 / gy : 1, rows = (lrows + target - 1) / target;
+    return rows > 8 ? rows : 8;
+}
+
+}  // namespace
+
+int64_t act_grad_blocks(int64_t m, int64_t n)
+{
+    const int64_t rows = (int64_t)(256 >> act_lshift(n)) * act_rows(m, n);
+    return (m + rows - 1) / rows;
+}
+
+hipError_t launch_act_grad(int dtype, const void* dy, const void* z, int act, int64_t m, int64_t n, void* dz,
+                           float* dbias, float* part, hipStream_t s)
+{
+    const int64_t blocks = act_grad_blocks(m, n);
+    ActArgs g;
+    g.dy = static_cast<const uint16_t*>(dy);
+    g.z = static_cast<const uint16_t*>(z);
+    g.dz = static_cast<uint16_t*>(dz);
+    g.part = dbias ? (blocks > 1 ? part : dbias) : nullptr;
+    g.m = m;
+    g.n = n;
+    g.act = act;
+    g.lshift = act_lshift(n);
+    g.rows = act_rows(m, n);
+    const int64_t cols = int64_t(8) << g.lshift, gy = (n + cols - 1) / cols;
+    if (blocks > kMaxGrid || gy > 65535) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks, (unsigned)gy);
+    if (dtype == 0) hipLaunchKernelGGL((k_act_grad<0>), grid, dim3(256), 0, s, g);
+    else hipLaunchKernelGGL((k_act_grad<1>), grid, dim3(256), 0, s, g);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !dbias || blocks <= 1) return e;
+    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, s, (const float*)part,
+                       (int)blocks, n, 1.0f, dbias);
+    return hipGetLastError();
+}
+
+namespace {
+
+template <int DT, bool BWD, bool DROP, int MB, int RT>
+hipError_t project_go(const ProjArgs& g, int waves, hipStream_t s)
+{
+    const dim3 grid((unsigned)((g.m + 16 * MB - 1) / (16 * MB)), (unsigned)((g.rank + 16 * RT - 1) / (16 * RT)));
+    const unsigned lds = (unsigned)(waves / 2 * MB * RT * 64 * 4 * sizeof(float));
+    hipLaunchKernelGGL((k_lora_project<DT, BWD, DROP, MB, RT>), grid, dim3(64 * waves), lds, s, g);
+    return hipGetLastError();
+}
+
+template <int DT, bool BWD, bool DROP>
+hipError_t project_shape(const ProjArgs& g, hipStream_t s)
+{
+    // Few rows: one 16-rank tile per workgroup and up to 16 waves on its
+    // reduction; otherwise a workgroup takes all ranks (up to 128), so that x
+    // is read once.
+    int waves = 1;
+    while (waves < 16 && (int64_t)waves * 128 < g.k) waves *= 2;
+    if (g.m <= 1024 || g.rank <= 16) return project_go<DT, BWD, DROP, 1, 1>(g, waves, s);
+    if (waves > 8) waves = 8;
+    if (g.rank <= 32) return project_go<DT, BWD, DROP, 1, 2>(g, waves, s);
+    if (g.rank <= 64) return project_go<DT, BWD, DROP, 1, 4>(g, waves, s);
+    return project_go<DT, BWD, DROP, 1, 8>(g, waves, s);
+}
+
+template <int DT>
+hipError_t project_dt(const ProjArgs& g, bool backward, hipStream_t s)
+{
+    if (backward) return project_shape<DT, true, false>(g, s);
+    return g.drop.thr ? project_shape<DT, false, true>(g, s) : project_shape<DT, false, false>(g, s);
+}
+
+}  // namespace
+
+hipError_t launch_lora_project(int dtype, const void* x, int64_t m, int64_t k, const void* w, int rank, bool backward,
+                               float scale, DropArgs drop, void* h, hipStream_t s)
+{
+    ProjArgs g;
+    g.x = static_cast<const uint16_t*>(x);
+    g.w = static_cast<const uint16_t*>(w);
+    g.h = static_cast<uint16_t*>(h);
+    g.m = m;
+    g.k = k;
+    g.rank = rank;
+    g.alpha = drop.thr ? scale * drop.keep : scale;
+    g.drop = drop;
+    if ((m + 15) / 16 >= kMaxGrid / 4) return hipErrorInvalidValue;   // up to 1,024 threads each
+    return dtype == 0 ? project_dt<0>(g, backward, s) : project_dt<1>(g, backward, s);
+}
+
+namespace {
+
+// Ranks per workgroup in 16-rank tiles.
+int grad_rt(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
+
+}  // namespace
+
+// Splits of the token axis: about 1,024 workgroups, each split at least 128
+// rows and at least eight rows per rank (a split's fp32 partial is written and
+// read back, 8 rank n bytes against the 2 rows n bytes of x that it reads).
+int lora_grad_splits(int64_t m, int64_t n, int rank)
+{
+    const int rt = grad_rt(rank);
+    const int64_t blocks = ((n + 127) / 128) * ((rank + 16 * rt - 1) / (16 * rt));
+    const int64_t least = rank > 16 ? (int64_t)8 * rank : 128;
+    int64_t sp = (1024 + blocks - 1) / blocks;
+    if (sp > m / least) sp = m / least;
+    if (sp < 1) sp = 1;
+    const int64_t rows = ((m + sp - 1) / sp + 31) / 32 * 32;
+    return (int)((m + rows - 1) / rows);
+}
+
+namespace {
+
+template <int DT, bool DROP>
+hipError_t grad_go(const GradArgs& g, int splits, hipStream_t s)
+{
+    const int rt = grad_rt(g.rank);
+    const int64_t gx = (g.n + 127) / 128;
+    if (gx > kMaxGrid || splits > 65535) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)gx, (unsigned)splits, (unsigned)((g.rank + 16 * rt - 1) / (16 * rt)));
+    if (rt == 1) hipLaunchKernelGGL((k_lora_grad<DT, DROP, 1>), grid, dim3(64 * kGradWaves), 0, s, g);
+    else if (rt == 2) hipLaunchKernelGGL((k_lora_grad<DT, DROP, 2>), grid, dim3(64 * kGradWaves), 0, s, g);
+    else hipLaunchKernelGGL((k_lora_grad<DT, DROP, 4>), grid, dim3(64 * kGradWaves), 0, s, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_lora_grad(int dtype, const void* u, const void* x, int64_t m, int64_t n, int rank, bool by_col,
+                            DropArgs drop, float* grad, float* part, hipStream_t s)
+{
+    const int splits = lora_grad_splits(m, n, rank);
+    const float scale = drop.thr ? drop.keep : 1.0f;
+    GradArgs g;
+    g.u = static_cast<const uint16_t*>(u);
+    g.x = static_cast<const uint16_t*>(x);
+    g.out = splits > 1 ? part : grad;
+    g.m = m;
+    g.n = n;
+    g.rank = rank;
+    g.by_col = by_col;
+    g.rows_split = ((m + splits - 1) / splits + 31) / 32 * 32;
+    g.scale = splits > 1 ? 1.0f : scale;
+    g.drop = drop;
+    hipError_t e;
+    if (dtype == 0) e = drop.thr ? grad_go<0, true>(g, splits, s) : grad_go<0, false>(g, splits, s);
+    else e = drop.thr ? grad_go<1, true>(g, splits, s) : grad_go<1, false>(g, splits, s);
+    if (e != hipSuccess || splits == 1) return e;
+    const int64_t total = n * rank, blocks = (total / 4 + 255) / 256;
+    if (blocks > kMaxGrid) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)blocks), dim3(256), 0, s, (const float*)part, splits, total, scale,
+                       grad);
+    return hipGetLastError();
+}
+
+}  // namespace nf4k

@@ -258,6 +258,59 @@ size_t matmul_tail_bytes(int64_t rows, int64_t cols, int32_t backward, int64_t m
     return align256(size_t(ts) * size_t(rem) * size_t(256 * 256) * sizeof(float));
 }
 
+// ---- the adapted layer's operators
+
+constexpr int32_t kMaxLoraRank = 128;
+// tokens of the adapter and epilogue-gradient calls, and elements of a dropout
+// (their grids); columns of theirs are below 2^31
+constexpr int64_t kMaxTokens = int64_t(1) << 25, kMaxDrop = int64_t(1) << 36, kMaxCols = int64_t(1) << 31;
+
+// The drop probability as a 16-bit threshold.  p = 0 (or a p that rounds to
+// it) is no dropout and needs no rng.
+nf4_status check_drop(const nf4_drop& d, nf4k::DropArgs* out)
+{
+    if (!(d.p >= 0.0f && d.p <= 65535.0f / 65536.0f)) return NF4_E_ARG;   // NaN fails too
+    const uint32_t thr = static_cast<uint32_t>(d.p * 65536.0f + 0.5f);
+    *out = nf4k::DropArgs{nullptr, 0, 1.0f};
+    if (thr == 0) return NF4_OK;
+    if (!d.rng) return NF4_E_ARG;
+    if (!aligned(d.rng, 8)) return NF4_E_ALIGN;
+    *out = nf4k::DropArgs{d.rng, thr, 65536.0f / static_cast<float>(65536u - thr)};
+    return NF4_OK;
+}
+
+nf4_status check_epilogue(const nf4_epilogue& e, int32_t backward, const void* out, nf4k::EpiArgs* a)
+{
+    if (e.act < NF4_ACT_NONE || e.act > NF4_ACT_GELU_TANH) return NF4_E_ARG;
+    if (backward && (e.act != NF4_ACT_NONE || e.bias || e.preact)) return NF4_E_UNSUPPORTED;
+    if ((e.u != nullptr) != (e.v != nullptr) || (e.u != nullptr) != (e.rank != 0) || e.rank < 0) return NF4_E_ARG;
+    if (e.rank > kMaxLoraRank) return NF4_E_UNSUPPORTED;
+    nf4k::DropArgs drop;
+    nf4_status st = check_drop(e.drop, &drop);
+    if (st != NF4_OK) return st;
+    if (drop.thr && !e.u) return NF4_E_ARG;
+    if (drop.thr && !backward) return NF4_E_UNSUPPORTED;
+    for (const void* p : {e.u, e.v, e.bias, e.residual, static_cast<const void*>(e.preact)})
+        if (!aligned(p, 16)) return NF4_E_ALIGN;
+    if (e.preact && (e.preact == out || e.preact == e.residual)) return NF4_E_ARG;
+    *a = nf4k::EpiArgs{static_cast<const uint16_t*>(e.u), static_cast<const uint16_t*>(e.v),
+                       static_cast<const uint16_t*>(e.bias), e.residual, static_cast<uint16_t*>(e.preact),
+                       e.rank, e.act, drop};
+    return NF4_OK;
+}
+
+nf4_status check_dtype(int32_t dtype) { return dtype == NF4_BF16 || dtype == NF4_FP16 ? NF4_OK : NF4_E_UNSUPPORTED; }
+
+// Tokens, columns (a multiple of 8) and rank of the adapter calls.
+nf4_status check_lora(int64_t m, int64_t n, int32_t rank, int32_t dtype)
+{
+    nf4_status st = check_dtype(dtype);
+    if (st != NF4_OK) return st;
+    if (m <= 0 || m > kMaxTokens || n <= 0 || n >= kMaxCols || rank <= 0) return NF4_E_ARG;
+    if (n % 8 || rank > kMaxLoraRank) return NF4_E_UNSUPPORTED;
+    return NF4_OK;
+}
+
 // nf4_dequantize, with the device skip mask of nf4_dequantize_masked (or null).
 nf4_status dequantize_impl(const nf4_layer* layers, int32_t nl, nf4_format fmt, const uint8_t* skip,
                            void* ws, size_t ws_bytes, hipStream_t stream)
@@ -539,6 +592,112 @@ nf4_status nf4_matmul_ws(const nf4_layer* w, int64_t rows, int64_t cols, nf4_for
     if (st != NF4_OK) return st;
     return run_matmul(w, rows, cols, fmt, backward, x, m, out, out_fp32, static_cast<float*>(ws), nsplit, 0,
                       stream);
+}
+
+nf4_status nf4_linear(const nf4_layer* w, int64_t rows, int64_t cols, nf4_format fmt, int32_t backward, const void* x,
+                      int64_t m, const nf4_epilogue* epi, void* out, int32_t out_fp32, void* ws, size_t ws_bytes,
+                      hipStream_t stream)
+{
+    nf4_status st = check_matmul(w, rows, cols, fmt, backward, x, m, out, out_fp32);
+    if (st != NF4_OK) return st;
+    if (!epi) return NF4_E_ARG;
+    nf4k::EpiArgs ep;
+    if ((st = check_epilogue(*epi, backward, out, &ep)) != NF4_OK) return st;
+    const size_t need = nf4_matmul_workspace_bytes(rows, cols, backward, m);
+    if (need > 0 && (st = check_ws(ws, ws_bytes, need)) != NF4_OK) return st;
+    float* part = need > 0 ? static_cast<float*>(ws) : nullptr;
+    const bool dq = fmt.dq_group != 0, fwd = backward == 0;
+    const int8_t* qa = dq ? w->qabsmax : nullptr;
+    const float* s2 = dq ? w->scale2 : nullptr;
+    const float* am = dq ? nullptr : w->absmax;
+    const int gv = nf4k::nf4_gemv_parts(rows, cols, fwd, m);
+    hipError_t e;
+    if (gv > 0) {
+        e = nf4k::launch_nf4_linear_gemv(fmt.dtype, w->codes, qa, s2, am, rows, cols, x, m, out, out_fp32 == 1, part,
+                                         gv, ep, stream);
+    } else {
+        const int nsplit = nf4k::nf4_matmul_splits(rows, cols, fwd, m);
+        int tail = 0;
+        if (nsplit <= 1) matmul_tail_bytes(rows, cols, backward, m, &tail);
+        e = nf4k::launch_nf4_linear(fmt.dtype, w->codes, qa, s2, am, rows, cols, fwd, x, m, out, out_fp32 == 1, part,
+                                    nsplit, tail, ep, stream);
+    }
+    return e == hipSuccess ? NF4_OK : hip_fail(e);
+}
+
+nf4_status nf4_dropout(const void* x, int64_t n, int32_t dtype, nf4_drop drop, void* out, hipStream_t stream)
+{
+    nf4_status st = check_dtype(dtype);
+    if (st != NF4_OK) return st;
+    if (!x || !out || n <= 0) return NF4_E_ARG;
+    if (n >= kMaxDrop) return NF4_E_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(out, 16)) return NF4_E_ALIGN;
+    nf4k::DropArgs d;
+    if ((st = check_drop(drop, &d)) != NF4_OK) return st;
+    hipError_t e = nf4k::launch_dropout(dtype, x, n, d, out, stream);
+    return e == hipSuccess ? NF4_OK : hip_fail(e);
+}
+
+size_t nf4_act_grad_workspace_bytes(int64_t m, int64_t n)
+{
+    if (m <= 0 || m > kMaxTokens || n <= 0 || n >= kMaxCols || n % 8) return 0;
+    const int64_t blocks = nf4k::act_grad_blocks(m, n);
+    return blocks > 1 ? align256(size_t(blocks) * size_t(n) * sizeof(float)) : 0;
+}
+
+nf4_status nf4_act_grad(const void* dy, const void* preact, int32_t act, int64_t m, int64_t n, int32_t dtype, void* dz,
+                        float* dbias, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    nf4_status st = check_dtype(dtype);
+    if (st != NF4_OK) return st;
+    if (act < NF4_ACT_NONE || act > NF4_ACT_GELU_TANH) return NF4_E_ARG;
+    if (!dy || m <= 0 || m > kMaxTokens || n <= 0 || n >= kMaxCols) return NF4_E_ARG;
+    if (act == NF4_ACT_NONE ? (!dz && !dbias) : (!preact || !dz)) return NF4_E_ARG;
+    if (n % 8) return NF4_E_UNSUPPORTED;
+    if (!aligned(dy, 16) || !aligned(preact, 16) || !aligned(dz, 16) || !aligned(dbias, 16)) return NF4_E_ALIGN;
+    const size_t need = dbias ? nf4_act_grad_workspace_bytes(m, n) : 0;
+    if (need > 0 && (st = check_ws(ws, ws_bytes, need)) != NF4_OK) return st;
+    hipError_t e = nf4k::launch_act_grad(dtype, dy, act == NF4_ACT_NONE ? nullptr : preact, act, m, n, dz, dbias,
+                                         static_cast<float*>(ws), stream);
+    return e == hipSuccess ? NF4_OK : hip_fail(e);
+}
+
+nf4_status nf4_lora_project(const void* x, int64_t m, int64_t k, const void* w, int32_t rank, int32_t dtype,
+                            int32_t backward, float scale, nf4_drop drop, void* h, hipStream_t stream)
+{
+    nf4_status st = check_lora(m, k, rank, dtype);
+    if (st != NF4_OK) return st;
+    if (!x || !w || !h || (backward != 0 && backward != 1)) return NF4_E_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(h, 16)) return NF4_E_ALIGN;
+    nf4k::DropArgs d;
+    if ((st = check_drop(drop, &d)) != NF4_OK) return st;
+    if (d.thr && backward) return NF4_E_UNSUPPORTED;
+    hipError_t e = nf4k::launch_lora_project(dtype, x, m, k, w, rank, backward == 1, scale, d, h, stream);
+    return e == hipSuccess ? NF4_OK : hip_fail(e);
+}
+
+size_t nf4_lora_grad_workspace_bytes(int64_t m, int64_t n, int32_t rank)
+{
+    if (check_lora(m, n, rank, NF4_BF16) != NF4_OK) return 0;
+    const int sp = nf4k::lora_grad_splits(m, n, rank);
+    return sp > 1 ? align256(size_t(sp) * size_t(n) * size_t(rank) * sizeof(float)) : 0;
+}
+
+nf4_status nf4_lora_grad(const void* u, const void* x, int64_t m, int64_t n, int32_t rank, int32_t dtype, int32_t side,
+                         nf4_drop drop, float* grad, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    nf4_status st = check_lora(m, n, rank, dtype);
+    if (st != NF4_OK) return st;
+    if (!u || !x || !grad || (side != NF4_LORA_A && side != NF4_LORA_B)) return NF4_E_ARG;
+    if (!aligned(u, 16) || !aligned(x, 16) || !aligned(grad, 16)) return NF4_E_ALIGN;
+    nf4k::DropArgs d;
+    if ((st = check_drop(drop, &d)) != NF4_OK) return st;
+    if (d.thr && side == NF4_LORA_B) return NF4_E_UNSUPPORTED;
+    const size_t need = nf4_lora_grad_workspace_bytes(m, n, rank);
+    if (need > 0 && (st = check_ws(ws, ws_bytes, need)) != NF4_OK) return st;
+    hipError_t e = nf4k::launch_lora_grad(dtype, u, x, m, n, rank, side == NF4_LORA_B, d, grad, static_cast<float*>(ws),
+                                          stream);
+    return e == hipSuccess ? NF4_OK : hip_fail(e);
 }
 
 size_t nf4_workspace_bytes_variant(int32_t nl, const int64_t* n_per_layer, nf4_variant v)

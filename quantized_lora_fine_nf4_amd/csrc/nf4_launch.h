@@ -93,4 +93,50 @@ hipError_t launch_select_ex(const double* err, const double* denom, const int64_
                             const int32_t* group_end, int nu, int64_t budget, int kcap, int rule,
                             uint8_t* selected, int32_t* k_out, SelectScratch w, hipStream_t s);
 
+// ---- the adapted layer's operators (k_lora.hip, k_linear.hip)
+
+// Dropout of a launch; thr == 0: none (rng not read).
+struct DropArgs {
+    const uint64_t* rng;   // device {seed, offset}
+    uint32_t thr;          // drop probability in units of 2^-16, 1 .. 65535
+    float keep;            // 65536 / (65536 - thr)
+};
+
+hipError_t launch_dropout(int dtype, const void* x, int64_t n, DropArgs d, void* out, hipStream_t s);
+// Row blocks of the epilogue's gradient: with more than one, fp32 partials
+// [blocks][n] at part.  z: null for activation none; dz: null to skip it;
+// dbias: null to skip it.
+int64_t act_grad_blocks(int64_t m, int64_t n);
+hipError_t launch_act_grad(int dtype, const void* dy, const void* z, int act, int64_t m, int64_t n, void* dz,
+                           float* dbias, float* part, hipStream_t s);
+// h[m x rank] = scale drop(x) W^T with W [rank x k], or scale x W with W
+// [k x rank] when backward (drop.thr must be 0 then).
+hipError_t launch_lora_project(int dtype, const void* x, int64_t m, int64_t k, const void* w, int rank, bool backward,
+                               float scale, DropArgs drop, void* h, hipStream_t s);
+// u^T drop(x) as [rank x n], or as [n x rank] with by_col; with more than one
+// split of the m tokens, fp32 partials [splits][result] at part.
+int lora_grad_splits(int64_t m, int64_t n, int rank);
+hipError_t launch_lora_grad(int dtype, const void* u, const void* x, int64_t m, int64_t n, int rank, bool by_col,
+                            DropArgs drop, float* grad, float* part, hipStream_t s);
+
+// What the matmul's epilogue adds to the product (k_linear.hip).  Forward
+// columns are W's rows, backward W's columns.
+struct EpiArgs {
+    const uint16_t* u;     // [m x rank]; null: no low-rank term
+    const uint16_t* v;     // forward [ncol x rank], backward [rank x ncol]
+    const uint16_t* bias;  // [ncol] or null
+    const void* residual;  // [m x ncol], the output's type, or null
+    uint16_t* preact;      // [m x ncol] or null
+    int rank, act;
+    DropArgs drop;         // of the low-rank term (backward)
+};
+// As launch_nf4_matmul / launch_nf4_gemv, with the epilogue.
+hipError_t launch_nf4_linear(int dtype, const uint8_t* codes, const int8_t* qabsmax, const float* scale2,
+                             const float* absmax, int64_t rows, int64_t cols, bool forward, const void* x, int64_t m,
+                             void* out, bool out_f32, float* part, int nsplit, int tail_split, const EpiArgs& epi,
+                             hipStream_t s);
+hipError_t launch_nf4_linear_gemv(int dtype, const uint8_t* codes, const int8_t* qabsmax, const float* scale2,
+                                  const float* absmax, int64_t rows, int64_t cols, const void* x, int64_t m, void* out,
+                                  bool out_f32, float* part, int parts, const EpiArgs& epi, hipStream_t s);
+
 }  // namespace nf4k
