@@ -184,22 +184,116 @@ __global__ __launch_bounds__(256) void k_act_grad(ActArgs g)
     }
 }
 
-// out[i] = scale * (part[0][i] + part[1][i] + ...), in part order; n a multiple of 4.
-__global__ __launch_bounds__(256) void k_sum_parts(const float* part, int nparts, int64_t n, float scale, float* out)
+// out[i] = scale * (part[0][i] + part[1][i] + ...); n a multiple of 4.  A
+// workgroup takes 256 >> glog columns of four values; its 1 << glog groups of
+// threads add every (1 << glog)-th part, and the groups' sums are added in
+// group order: a fixed order for a given part count.
+__global__ __launch_bounds__(256) void k_sum_parts(const float* part, int nparts, int glog, int64_t n, float scale,
+                                                   float* out)
 {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= n) return;
-    f32x4 a = *(const GLOBAL f32x4*)(part + i);
-    for (int p = 1; p < nparts; ++p) a += *(const GLOBAL f32x4*)(part + (int64_t)p * n + i);
-    *(GLOBAL f32x4*)(out + i) = a * scale;
+    __shared__ __attribute__((aligned(16))) f32x4 s_sum[256];
+    const int t = threadIdx.x, per = 256 >> glog, c = t & (per - 1), g = t >> (8 - glog), ng = 1 << glog;
+    const int64_t i = ((int64_t)blockIdx.x * per + c) * 4;
+    f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (i < n) {
+#pragma unroll 4
+        for (int p = g; p < nparts; p += ng) a += *(const GLOBAL f32x4*)(part + (int64_t)p * n + i);
+    }
+    if (glog > 0) {
+        s_sum[t] = a;
+        __syncthreads();
+        if (g > 0) return;
+        for (int k = 1; k < ng; ++k) a += s_sum[k * per + c];
+    }
+    if (i < n) *(GLOBAL f32x4*)(out + i) = a * scale;
+}
+
+// ---- the adapter's down product
+//
+// ---- 16-rank operand tiles
+//
+// The reduction index of a [k x rank] matrix is its slow index, while an MFMA
+// fragment wants eight consecutive k of one rank.  With the rank a multiple of
+// 8 a wave copies a 32 x 16 RT tile to LDS (16 bytes a lane, rank contiguous)
+// and reads it back with the transposing 64-bit read: in each group of 16
+// lanes, lane i receives element i % 4 of the pieces read by lanes 4 j + i / 4,
+// so lanes reading rows r .. r + 3 at columns C + 4 (i % 4) get column C + i of
+// those rows.  Otherwise each lane gathers its eight values from memory.
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Orders a wave's LDS writes before its lanes' later reads (and the reverse);
+// LDS executes one wave's accesses in order.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Rows k0 .. k0 + 31 (past `rows` the last row again), ranks r0 .. r0 + 16 RT
+// - 1 of p [rows x rank], rank a multiple of 8: 16-byte piece t * 64 + lane.
+template <int RT>
+__device__ __forceinline__ void load_tile(const uint16_t* p, int64_t rows, int rank, int64_t k0, int r0, u32x4 (&d)[RT])
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int item = t * 64 + lane, r = r0 + 8 * (item % (2 * RT));
+        const int64_t k = k0 + item / (2 * RT);
+        d[t] = *(const GLOBAL u32x4*)(p + (k < rows ? k : rows - 1) * rank + (r < rank ? r : rank - 8));
+    }
+}
+
+// Through LDS (32 x 16 RT values of the wave's own) to the fragments of the RT
+// rank tiles.
+template <int RT>
+__device__ __forceinline__ void transpose_tile(const u32x4 (&d)[RT], uint16_t* lds, u32x4 (&f)[RT])
+{
+    const int lane = threadIdx.x & 63, q = lane & 15, kg = lane >> 4;
+    wave_sync();
+#pragma unroll
+    for (int t = 0; t < RT; ++t) *(u32x4*)(lds + (t * 64 + lane) * 8) = d[t];
+    wave_sync();
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+        u32x2 h[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            h[u] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(lds + (8 * kg + 4 * u + (q >> 2)) * (16 * RT) + 16 * j +
+                                                            4 * (q & 3))));
+        f[j] = u32x4{h[0].x, h[0].y, h[1].x, h[1].y};
+    }
+}
+
+// The same fragments gathered from memory, any rank.
+template <int RT>
+__device__ __forceinline__ void gather_tile(const uint16_t* p, int64_t rows, int rank, int64_t k0, int r0, u32x4 (&f)[RT])
+{
+    const int lane = threadIdx.x & 63, q = lane & 15, kg = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+        const int r = r0 + 16 * j + q;
+        const GLOBAL uint16_t* col = (const GLOBAL uint16_t*)p + (r < rank ? r : rank - 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t k = k0 + 8 * kg + 2 * i;
+            const uint32_t lo = col[(k < rows ? k : rows - 1) * rank], hi = col[(k + 1 < rows ? k + 1 : rows - 1) * rank];
+            f[j][i] = lo | (hi << 16);
+        }
+    }
 }
 
 // ---- the adapter's down product
 //
 // h[m x rank] = alpha (keep . x) W, reduction over k.  A workgroup takes
-// 16 MB rows of x and 16 RT ranks; its waves share the reduction in chunks of
-// 128 k (four 16 x 16 x 32 MFMA steps; lane l holds x row l % 16, k 8 (l / 16)
-// .. + 7 of a step), and their sums are added pairwise in LDS.
+// 16 MB rows of x and 16 RT ranks; its W waves share the reduction in chunks of
+// 64 k (two 16 x 16 x 32 MFMA steps; lane l holds x row l % 16, k 8 (l / 16)
+// .. + 7 of a step), the next chunk's x loaded while this one multiplies, and
+// their sums are added pairwise in LDS.
+enum ProjMode { PROJ_FWD, PROJ_DROP, PROJ_BACK, PROJ_BACK_ANY };   // forward, with dropout, backward, any rank
+
 struct ProjArgs {
     const uint16_t* x;    // [m x k]
     const uint16_t* w;    // forward [rank x k], backward [k x rank]
@@ -210,11 +304,14 @@ struct ProjArgs {
     DropArgs drop;
 };
 
-template <int DT, bool BWD, bool DROP, int MB, int RT>
-__global__ __launch_bounds__(1024) void k_lora_project(ProjArgs g)
+template <int DT, int MODE, int MB, int RT, int W>
+__global__ __launch_bounds__(64 * W) void k_lora_project(ProjArgs g)
 {
-    extern __shared__ __attribute__((aligned(16))) float s_acc[];   // [waves / 2][64 lanes][4 MB RT]
-    const int t = threadIdx.x, lane = t & 63, wv = t >> 6, nw = blockDim.x >> 6;
+    constexpr bool DROP = MODE == PROJ_DROP;
+    // the waves' operand tiles, then the sums
+    constexpr int kTile = MODE == PROJ_BACK ? W * RT * 1024 : 0, kSums = W / 2 * MB * RT * 1024;
+    __shared__ __attribute__((aligned(16))) uint8_t s_mem[kTile > kSums ? kTile : kSums > 0 ? kSums : 16];
+    const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
     const int q = lane & 15, kg = lane >> 4;
     const int64_t m0 = (int64_t)blockIdx.x * (16 * MB);
     const int r0 = blockIdx.y * (16 * RT);
@@ -226,53 +323,70 @@ __global__ __launch_bounds__(1024) void k_lora_project(ProjArgs g)
         const int64_t r = m0 + 16 * b + q;
         xrow[b] = (r < g.m ? r : g.m - 1) * g.k;
     }
-    int rk[RT];
+    int64_t wrow[RT];
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
         const int r = r0 + 16 * j + q;
-        rk[j] = r < g.rank ? r : g.rank - 1;
+        wrow[j] = (int64_t)(r < g.rank ? r : g.rank - 1) * g.k;
     }
     f32x4 acc[MB][RT];
 #pragma unroll
     for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t k0 = (int64_t)wv * 128; k0 < g.k; k0 += (int64_t)nw * 128) {
+    // k of step s of the chunk at k0; past the end the last eight again (zeroed below)
+    auto at = [&](int64_t k0, int s) { const int64_t kk = k0 + 32 * s + 8 * kg; return kk < g.k ? kk : g.k - 8; };
+    u32x4 x[MB][2];
+    auto load_x = [&](int64_t k0) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int64_t kk = k0 + 32 * s + 8 * kg;
-            const bool in = kk < g.k;
-            const int64_t kc = in ? kk : g.k - 8;
-            u32x4 a[MB];
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) x[b][s] = *(const GLOBAL u32x4*)(g.x + xrow[b] + at(k0, s));
+    };
+    int64_t k0 = (int64_t)wv * 64;
+    if (k0 < g.k) load_x(k0);
+    for (; k0 < g.k; k0 += 64 * W) {
+        u32x4 a[MB][2], w[2][RT];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if constexpr (MODE == PROJ_BACK) load_tile<RT>(g.w, g.k, g.rank, k0 + 32 * s, r0, w[s]);
+            else if constexpr (MODE == PROJ_BACK_ANY) gather_tile<RT>(g.w, g.k, g.rank, k0 + 32 * s, r0, w[s]);
+            else {
+#pragma unroll
+                for (int j = 0; j < RT; ++j) w[s][j] = *(const GLOBAL u32x4*)(g.w + wrow[j] + at(k0, s));
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) a[b][s] = x[b][s];
+        if (k0 + 64 * W < g.k) load_x(k0 + 64 * W);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if constexpr (MODE == PROJ_BACK) {
+                u32x4 f[RT];
+                transpose_tile<RT>(w[s], (uint16_t*)(s_mem + wv * RT * 1024), f);
+#pragma unroll
+                for (int j = 0; j < RT; ++j) w[s][j] = f[j];
+            }
+            const bool in = k0 + 32 * s + 8 * kg < g.k;
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
-                a[b] = *(const GLOBAL u32x4*)(g.x + xrow[b] + kc);
                 if constexpr (DROP) {
-                    const Bits128 bits = philox7(key, (uint64_t)(xrow[b] + kc) >> 3);
+                    const Bits128 bits = philox7(key, (uint64_t)(xrow[b] + at(k0, s)) >> 3);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) a[b][j] &= keep_mask2(bits.w[j], g.drop.thr);
+                    for (int j = 0; j < 4; ++j) a[b][s][j] &= keep_mask2(bits.w[j], g.drop.thr);
                 }
-                if (!in) a[b] = u32x4{0, 0, 0, 0};
-            }
+                if (!in) a[b][s] = u32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < RT; ++j) {
-                u32x4 w;
-                if constexpr (!BWD) {
-                    w = *(const GLOBAL u32x4*)(g.w + (int64_t)rk[j] * g.k + kc);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const GLOBAL uint16_t* p = (const GLOBAL uint16_t*)g.w + (kc + 2 * e) * g.rank + rk[j];
-                        w[e] = (uint32_t)p[0] | ((uint32_t)p[g.rank] << 16);
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < MB; ++b) acc[b][j] = mfma<DT>(a[b], w, acc[b][j]);
+                for (int j = 0; j < RT; ++j) acc[b][j] = mfma<DT>(a[b][s], w[s][j], acc[b][j]);
             }
         }
     }
-    // pairwise over the waves (a power of two of them)
-    for (int half = nw >> 1; half > 0; half >>= 1) {
+    if constexpr (kTile > 0) __syncthreads();   // every wave done with its tile
+    float* s_acc = (float*)s_mem;
+#pragma unroll
+    for (int half = W / 2; half > 0; half >>= 1) {
         if (wv >= half && wv < 2 * half) {
 #pragma unroll
             for (int b = 0; b < MB; ++b)
@@ -313,7 +427,7 @@ __global__ __launch_bounds__(1024) void k_lora_project(ProjArgs g)
 // transposes the 8 x 8 block in registers with byte permutes: column c of the
 // block is the lane's fragment of MFMA c (16 x 16 x 32), whose 16 columns are
 // n0 + 8 q + c, q = 0 .. 15.  A wave covers 128 columns and 16 RT ranks, the
-// waves of a workgroup share its rows, and their sums are added in LDS.
+// W waves of a workgroup share its rows, and their sums are added in LDS.
 struct GradArgs {
     const uint16_t* u;     // [m x rank]
     const uint16_t* x;     // [m x n]
@@ -326,12 +440,17 @@ struct GradArgs {
     DropArgs drop;
 };
 
-constexpr int kGradWaves = 4;
+// Waves of a workgroup: as many as the accumulators (32 RT registers) leave
+// room for on a CU.
+template <int RT> constexpr int kGradWaves = RT == 1 ? 16 : 8;
 
-template <int DT, bool DROP, int RT>
-__global__ __launch_bounds__(64 * kGradWaves) void k_lora_grad(GradArgs g)
+template <int DT, bool DROP, bool VEC, int RT>
+__global__ __launch_bounds__(64 * kGradWaves<RT>) void k_lora_grad(GradArgs g)
 {
-    __shared__ __attribute__((aligned(16))) f32x4 s_acc[(kGradWaves / 2) * 8 * RT * 64];
+    constexpr int W = kGradWaves<RT>;
+    // the waves' tiles of u, then the sums
+    constexpr int kTile = VEC ? W * RT * 1024 : 0, kSums = W / 2 * 8 * RT * 1024;
+    __shared__ __attribute__((aligned(16))) uint8_t s_mem[kTile > kSums ? kTile : kSums];
     const int t = threadIdx.x, lane = t & 63, wv = t >> 6, q = lane & 15, mg = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 128 + 8 * q;
     const int64_t nc = n0 < g.n ? n0 : g.n - 8;
@@ -340,34 +459,25 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_lora_grad(GradArgs g)
     const int64_t s1 = s0 + g.rows_split < g.m ? s0 + g.rows_split : g.m;
     PhiloxKey key = {};
     if constexpr (DROP) key = philox_key(g.drop.rng);
-    int rk[RT];
-#pragma unroll
-    for (int j = 0; j < RT; ++j) {
-        const int r = r0 + 16 * j + q;
-        rk[j] = r < g.rank ? r : g.rank - 1;
-    }
     f32x4 acc[RT][8];
 #pragma unroll
     for (int j = 0; j < RT; ++j)
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[j][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t m0 = s0 + 32 * wv; m0 < s1; m0 += 32 * kGradWaves) {
-        u32x4 x[8];
-        u32x4 a[RT];
+    for (int64_t m0 = s0 + 32 * wv; m0 < s1; m0 += 32 * W) {
+        u32x4 x[8], a[RT];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t row = m0 + 8 * mg + i;
             x[i] = *(const GLOBAL u32x4*)(g.x + (row < s1 ? row : s1 - 1) * g.n + nc);
         }
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t row = m0 + 8 * mg + 2 * i;
-                const uint32_t lo = ((const GLOBAL uint16_t*)g.u)[(row < s1 ? row : s1 - 1) * g.rank + rk[j]];
-                const uint32_t hi = ((const GLOBAL uint16_t*)g.u)[(row + 1 < s1 ? row + 1 : s1 - 1) * g.rank + rk[j]];
-                a[j][i] = lo | (hi << 16);
-            }
+        if constexpr (VEC) {
+            u32x4 d[RT];
+            load_tile<RT>(g.u, s1, g.rank, m0, r0, d);
+            transpose_tile<RT>(d, (uint16_t*)(s_mem + wv * RT * 1024), a);
+        } else {
+            gather_tile<RT>(g.u, s1, g.rank, m0, r0, a);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t row = m0 + 8 * mg + i;
@@ -388,8 +498,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_lora_grad(GradArgs g)
             for (int j = 0; j < RT; ++j) acc[j][c] = mfma<DT>(a[j], b, acc[j][c]);
         }
     }
+    if constexpr (kTile > 0) __syncthreads();   // every wave done with its tile
+    f32x4* s_acc = (f32x4*)s_mem;
 #pragma unroll
-    for (int half = kGradWaves / 2; half > 0; half >>= 1) {
+    for (int half = W / 2; half > 0; half >>= 1) {
         if (wv >= half && wv < 2 * half) {
 #pragma unroll
             for (int j = 0; j < RT; ++j)
@@ -409,10 +521,18 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_lora_grad(GradArgs g)
     // lane l, value i of acc[j][c]: rank r0 + 16 j + 4 (l / 16) + i, column n0 + c
     GLOBAL float* out = (GLOBAL float*)g.out + (int64_t)blockIdx.y * g.rank * g.n;
 #pragma unroll
-    for (int j = 0; j < RT; ++j)
+    for (int j = 0; j < RT; ++j) {
+        const int rb = r0 + 16 * j + 4 * mg;
+        if (g.by_col && (g.rank & 3) == 0) {
+            if (rb < g.rank) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) *(GLOBAL f32x4*)(out + (n0 + c) * g.rank + rb) = acc[j][c] * g.scale;
+            }
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = r0 + 16 * j + 4 * mg + i;
+            const int r = rb + i;
             if (r >= g.rank) continue;
             if (g.by_col) {
 #pragma unroll
@@ -424,9 +544,19 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_lora_grad(GradArgs g)
                         f32x4{acc[j][c][i], acc[j][c + 1][i], acc[j][c + 2][i], acc[j][c + 3][i]} * g.scale;
             }
         }
+    }
 }
 
 constexpr int64_t kMaxGrid = (int64_t(1) << 32) / 256 - 1;
+
+hipError_t sum_parts(const float* part, int nparts, int64_t n, float scale, float* out, hipStream_t s)
+{
+    const int glog = nparts >= 16 ? 4 : nparts >= 4 ? 2 : 0;
+    const int64_t per = (256 >> glog) * 4, blocks = (n + per - 1) / per;
+    if (blocks > kMaxGrid) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)blocks), dim3(256), 0, s, part, nparts, glog, n, scale, out);
+    return hipGetLastError();
+}
 
 }  // namespace
 
@@ -488,42 +618,37 @@ hipError_t launch_act_grad(int dtype, const void* dy, const void* z, int act, in
     else hipLaunchKernelGGL((k_act_grad<1>), grid, dim3(256), 0, s, g);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !dbias || blocks <= 1) return e;
-    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, s, (const float*)part,
-                       (int)blocks, n, 1.0f, dbias);
-    return hipGetLastError();
+    return sum_parts(part, (int)blocks, n, 1.0f, dbias, s);
 }
 
 namespace {
 
-template <int DT, bool BWD, bool DROP, int MB, int RT>
-hipError_t project_go(const ProjArgs& g, int waves, hipStream_t s)
+template <int DT, int MODE, int MB, int RT, int W>
+hipError_t project_go(const ProjArgs& g, hipStream_t s)
 {
     const dim3 grid((unsigned)((g.m + 16 * MB - 1) / (16 * MB)), (unsigned)((g.rank + 16 * RT - 1) / (16 * RT)));
-    const unsigned lds = (unsigned)(waves / 2 * MB * RT * 64 * 4 * sizeof(float));
-    hipLaunchKernelGGL((k_lora_project<DT, BWD, DROP, MB, RT>), grid, dim3(64 * waves), lds, s, g);
+    hipLaunchKernelGGL((k_lora_project<DT, MODE, MB, RT, W>), grid, dim3(64 * W), 0, s, g);
     return hipGetLastError();
 }
 
-template <int DT, bool BWD, bool DROP>
+// Few rows: one 16-rank tile per workgroup, so that there are more of them;
+// otherwise a workgroup takes all ranks, so that x is read (and its mask
+// computed) once, and 32 rows where those still make a workgroup per CU.
+template <int DT, int MODE>
 hipError_t project_shape(const ProjArgs& g, hipStream_t s)
 {
-    // Few rows: one 16-rank tile per workgroup and up to 16 waves on its
-    // reduction; otherwise a workgroup takes all ranks (up to 128), so that x
-    // is read once.
-    int waves = 1;
-    while (waves < 16 && (int64_t)waves * 128 < g.k) waves *= 2;
-    if (g.m <= 1024 || g.rank <= 16) return project_go<DT, BWD, DROP, 1, 1>(g, waves, s);
-    if (waves > 8) waves = 8;
-    if (g.rank <= 32) return project_go<DT, BWD, DROP, 1, 2>(g, waves, s);
-    if (g.rank <= 64) return project_go<DT, BWD, DROP, 1, 4>(g, waves, s);
-    return project_go<DT, BWD, DROP, 1, 8>(g, waves, s);
+    if (g.m <= 1024 || g.rank <= 16) return project_go<DT, MODE, 1, 1, 16>(g, s);
+    const bool two = g.m >= 32 * 256;
+    if (g.rank <= 32) return two ? project_go<DT, MODE, 2, 2, 16>(g, s) : project_go<DT, MODE, 1, 2, 16>(g, s);
+    if (g.rank <= 64) return two ? project_go<DT, MODE, 2, 4, 16>(g, s) : project_go<DT, MODE, 1, 4, 16>(g, s);
+    return two ? project_go<DT, MODE, 2, 8, 8>(g, s) : project_go<DT, MODE, 1, 8, 8>(g, s);
 }
 
 template <int DT>
 hipError_t project_dt(const ProjArgs& g, bool backward, hipStream_t s)
 {
-    if (backward) return project_shape<DT, true, false>(g, s);
-    return g.drop.thr ? project_shape<DT, false, true>(g, s) : project_shape<DT, false, false>(g, s);
+    if (backward) return g.rank % 8 == 0 ? project_shape<DT, PROJ_BACK>(g, s) : project_shape<DT, PROJ_BACK_ANY>(g, s);
+    return g.drop.thr ? project_shape<DT, PROJ_DROP>(g, s) : project_shape<DT, PROJ_FWD>(g, s);
 }
 
 }  // namespace
@@ -551,15 +676,15 @@ int grad_rt(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
 
 }  // namespace
 
-// Splits of the token axis: about 1,024 workgroups, each split at least 128
-// rows and at least eight rows per rank (a split's fp32 partial is written and
-// read back, 8 rank n bytes against the 2 rows n bytes of x that it reads).
+// Splits of the token axis: a workgroup per CU, each split at least 128 rows
+// and at least eight rows per rank (a split's fp32 partial is written and read
+// back, 8 rank n bytes against the 2 rows n bytes of x that it reads).
 int lora_grad_splits(int64_t m, int64_t n, int rank)
 {
     const int rt = grad_rt(rank);
     const int64_t blocks = ((n + 127) / 128) * ((rank + 16 * rt - 1) / (16 * rt));
     const int64_t least = rank > 16 ? (int64_t)8 * rank : 128;
-    int64_t sp = (1024 + blocks - 1) / blocks;
+    int64_t sp = 256 / blocks;
     if (sp > m / least) sp = m / least;
     if (sp < 1) sp = 1;
     const int64_t rows = ((m + sp - 1) / sp + 31) / 32 * 32;
@@ -568,17 +693,25 @@ int lora_grad_splits(int64_t m, int64_t n, int rank)
 
 namespace {
 
-template <int DT, bool DROP>
+template <int DT, bool DROP, bool VEC>
 hipError_t grad_go(const GradArgs& g, int splits, hipStream_t s)
 {
     const int rt = grad_rt(g.rank);
     const int64_t gx = (g.n + 127) / 128;
     if (gx > kMaxGrid || splits > 65535) return hipErrorInvalidValue;
     const dim3 grid((unsigned)gx, (unsigned)splits, (unsigned)((g.rank + 16 * rt - 1) / (16 * rt)));
-    if (rt == 1) hipLaunchKernelGGL((k_lora_grad<DT, DROP, 1>), grid, dim3(64 * kGradWaves), 0, s, g);
-    else if (rt == 2) hipLaunchKernelGGL((k_lora_grad<DT, DROP, 2>), grid, dim3(64 * kGradWaves), 0, s, g);
-    else hipLaunchKernelGGL((k_lora_grad<DT, DROP, 4>), grid, dim3(64 * kGradWaves), 0, s, g);
+    if (rt == 1) hipLaunchKernelGGL((k_lora_grad<DT, DROP, VEC, 1>), grid, dim3(64 * kGradWaves<1>), 0, s, g);
+    else if (rt == 2) hipLaunchKernelGGL((k_lora_grad<DT, DROP, VEC, 2>), grid, dim3(64 * kGradWaves<2>), 0, s, g);
+    else hipLaunchKernelGGL((k_lora_grad<DT, DROP, VEC, 4>), grid, dim3(64 * kGradWaves<4>), 0, s, g);
     return hipGetLastError();
+}
+
+template <int DT>
+hipError_t grad_dt(const GradArgs& g, int splits, hipStream_t s)
+{
+    const bool vec = g.rank % 8 == 0;
+    if (g.drop.thr) return vec ? grad_go<DT, true, true>(g, splits, s) : grad_go<DT, true, false>(g, splits, s);
+    return vec ? grad_go<DT, false, true>(g, splits, s) : grad_go<DT, false, false>(g, splits, s);
 }
 
 }  // namespace
@@ -599,15 +732,9 @@ hipError_t launch_lora_grad(int dtype, const void* u, const void* x, int64_t m, 
     g.rows_split = ((m + splits - 1) / splits + 31) / 32 * 32;
     g.scale = splits > 1 ? 1.0f : scale;
     g.drop = drop;
-    hipError_t e;
-    if (dtype == 0) e = drop.thr ? grad_go<0, true>(g, splits, s) : grad_go<0, false>(g, splits, s);
-    else e = drop.thr ? grad_go<1, true>(g, splits, s) : grad_go<1, false>(g, splits, s);
+    const hipError_t e = dtype == 0 ? grad_dt<0>(g, splits, s) : grad_dt<1>(g, splits, s);
     if (e != hipSuccess || splits == 1) return e;
-    const int64_t total = n * rank, blocks = (total / 4 + 255) / 256;
-    if (blocks > kMaxGrid) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)blocks), dim3(256), 0, s, (const float*)part, splits, total, scale,
-                       grad);
-    return hipGetLastError();
+    return sum_parts(part, splits, n * rank, scale, grad, s);
 }
 
 }  // namespace nf4k
