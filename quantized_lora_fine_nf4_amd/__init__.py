@@ -349,57 +349,68 @@ def nf4_storage_bytes_variant(n: int, v: nf4_variant) -> int:
 # the C call returns) and enqueues nothing.  Work goes to the current stream of
 # the tensors' device, or to `stream`, which must be one of that device's.
 
-def _need(cond: bool, where: str, what: str) -> None:
-    if not cond:
-        e = NF4Error(NF4_E_ARG, where)
-        e.args = (f"{e.args[0]}: {what}",)
-        raise e
+def _misfit(where: str, what: str):
+    e = NF4Error(NF4_E_ARG, where)
+    e.args = (f"{e.args[0]}: {what}",)
+    raise e
 
 
 def _dtype16(t, where: str) -> int:
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return NF4_BF16
-    _need(t.dtype == torch.float16, where, f"bfloat16 or float16 expected, got {t.dtype}")
+    if t.dtype is not torch.float16:
+        _misfit(where, f"bfloat16 or float16 expected, got {t.dtype}")
     return NF4_FP16
 
 
-def _fits(t, name: str, where: str, shape, dtype, device) -> int:
-    """The address of a tensor that must have this shape, type and device."""
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        _need(False, where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                            f"{t.dtype} {tuple(t.shape)} on {t.device}")
+def _fits(t, name: str, where: str, shape: tuple, dtype, dev: int) -> int:
+    """The address of a tensor that must have this shape, type and device index."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _misfit(where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {dev}, got "
+                       f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rng_arg(p: float, rng, where: str, device) -> nf4_drop:
+_NO_DROP = nf4_drop(None, 0.0)
+
+
+def _rng_arg(p: float, rng, where: str, dev: int) -> nf4_drop:
     if not p:
-        return nf4_drop(None, 0.0)
-    import torch
-    _need(rng is not None, where, "dropout needs rng")
-    _need(rng.numel() == 2 and rng.dtype in (torch.int64, torch.uint64) and rng.device == device
-          and rng.is_contiguous(), where, f"rng must hold {{seed, offset}} as 64-bit integers on {device}")
-    return nf4_drop(rng.data_ptr(), float(p))
+        return _NO_DROP
+    if rng is None:
+        _misfit(where, "dropout needs rng")
+    if (rng.numel() != 2 or rng.element_size() != 8 or rng.is_floating_point() or rng.get_device() != dev
+            or not rng.is_contiguous()):
+        _misfit(where, f"rng must hold {{seed, offset}} as 64-bit integers on device {dev}")
+    return nf4_drop(rng.data_ptr(), p)
 
 
-def _ws_arg(ws, where: str, device):
+def _ws_arg(ws, where: str, dev: int):
     if ws is None:
         return None, 0
-    _need(ws.device == device and ws.is_contiguous(), where, f"the workspace must be a contiguous tensor on {device}")
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _misfit(where, f"the workspace must be a contiguous tensor on device {dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _enqueue(fn, where: str, device, stream, *args) -> None:
-    """fn(*args, stream) with the tensors' device current."""
+def _enqueue(name: str, dev: int, stream, *args) -> None:
+    """The C call `name` with these arguments and the stream, the tensors' device current."""
     import torch
-    _need(device.type == "cuda", where, f"tensors must be on the GPU, got {device}")
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(stream))
+    if dev < 0:
+        _misfit(name, "tensors must be on the GPU")
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev) without the Stream object
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(stream))
+        s = _stream(stream)
+    fn = getattr(_lib or lib(), name)
+    if dev == torch.cuda.current_device():
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
     if st != NF4_OK:
-        raise NF4Error(st, where)
+        raise NF4Error(st, name)
 
 
 def nf4_linear(layer, rows: int, cols: int, f: nf4_format, x, out, ws=None, backward: bool = False, lora=None,
@@ -414,32 +425,36 @@ def nf4_linear(layer, rows: int, cols: int, f: nf4_format, x, out, ws=None, back
     or None when that is 0."""
     import torch
     w = "nf4_linear"
-    dev, t16 = x.device, torch.bfloat16 if f.dtype == NF4_BF16 else torch.float16
-    m = x.shape[0] if x.dim() == 2 else 1
+    dev, t16 = x.get_device(), torch.bfloat16 if f.dtype == NF4_BF16 else torch.float16
     kred, ncol = (rows, cols) if backward else (cols, rows)
-    xs = torch.Size((m, kred)) if x.dim() == 2 else torch.Size((kred,))
+    if x.dim() == 2:
+        m, xs, os_ = x.shape[0], (x.shape[0], kred), (x.shape[0], ncol)
+    else:
+        m, xs, os_ = 1, (kred,), (ncol,)
     xp = _fits(x, "x", w, xs, t16, dev)
-    os_ = torch.Size((m, ncol)) if out.dim() == 2 else torch.Size((m * ncol,))
-    _need(out.dtype in (t16, torch.float32) and (out.dim() == 2 or m == 1), w, "out must be [m, columns] in f's 16-bit type or float32")
-    op = _fits(out, "out", w, os_, out.dtype, dev)
+    f32 = out.dtype is torch.float32
+    if out.dim() == 1 and m == 1:
+        os_ = (ncol,)
+    op = _fits(out, "out", w, os_, torch.float32 if f32 else t16, dev)
     e = nf4_epilogue()
     if lora is not None:
         u, v = lora
-        r = u.shape[-1] if u.dim() else 0
-        e.u = _fits(u, "u", w, torch.Size((m, r)) if u.dim() == 2 else torch.Size((m * r,)), t16, dev)
-        e.v = _fits(v, "v", w, torch.Size((r, cols) if backward else (rows, r)), t16, dev)
+        r = u.shape[-1]
+        e.u = _fits(u, "u", w, (m, r) if u.dim() == 2 or m > 1 else (r,), t16, dev)
+        e.v = _fits(v, "v", w, (r, cols) if backward else (rows, r), t16, dev)
         e.rank = r
-    e.act = int(act)
-    e.drop = _rng_arg(p, rng, w, dev)
+    e.act = act
+    if p:
+        e.drop = _rng_arg(p, rng, w, dev)
     if bias is not None:
-        e.bias = _fits(bias, "bias", w, torch.Size((ncol,)), t16, dev)
+        e.bias = _fits(bias, "bias", w, (ncol,), t16, dev)
     if preact is not None:
         e.preact = _fits(preact, "preact", w, os_, t16, dev)
     if residual is not None:
         e.residual = _fits(residual, "residual", w, os_, out.dtype, dev)
     wp, wb = _ws_arg(ws, w, dev)
-    _enqueue(lib().nf4_linear, w, dev, stream, ctypes.byref(layer), int(rows), int(cols), f, int(bool(backward)), xp, m,
-             ctypes.byref(e), op, 1 if out.dtype == torch.float32 else 0, wp, wb)
+    _enqueue(w, dev, stream, ctypes.byref(layer), rows, cols, f, 1 if backward else 0, xp, m, ctypes.byref(e), op,
+             1 if f32 else 0, wp, wb)
 
 
 def nf4_act_grad(dy, preact, act: int, dz=None, dbias=None, ws=None, stream=None) -> None:
@@ -449,15 +464,16 @@ def nf4_act_grad(dy, preact, act: int, dz=None, dbias=None, ws=None, stream=None
     nf4_act_grad_workspace_bytes(m, n) bytes with dbias."""
     import torch
     w = "nf4_act_grad"
-    dt, dev = _dtype16(dy, w), dy.device
-    _need(dy.dim() == 2, w, "dy must be [m, n]")
-    m, n = dy.shape
-    dp = _fits(dy, "dy", w, dy.shape, dy.dtype, dev)
-    pp = None if preact is None else _fits(preact, "preact", w, dy.shape, dy.dtype, dev)
-    zp = None if dz is None else _fits(dz, "dz", w, dy.shape, dy.dtype, dev)
-    bp = None if dbias is None else _fits(dbias, "dbias", w, torch.Size((n,)), torch.float32, dev)
+    dt, dev = _dtype16(dy, w), dy.get_device()
+    if dy.dim() != 2:
+        _misfit(w, "dy must be [m, n]")
+    m, n = shape = dy.shape
+    dp = _fits(dy, "dy", w, shape, dy.dtype, dev)
+    pp = None if preact is None else _fits(preact, "preact", w, shape, dy.dtype, dev)
+    zp = None if dz is None else _fits(dz, "dz", w, shape, dy.dtype, dev)
+    bp = None if dbias is None else _fits(dbias, "dbias", w, (n,), torch.float32, dev)
     wp, wb = _ws_arg(ws, w, dev)
-    _enqueue(lib().nf4_act_grad, w, dev, stream, dp, pp, int(act), m, n, dt, zp, bp, wp, wb)
+    _enqueue(w, dev, stream, dp, pp, act, m, n, dt, zp, bp, wp, wb)
 
 
 def nf4_act_grad_workspace_bytes(m: int, n: int) -> int:
@@ -468,27 +484,26 @@ def nf4_dropout(x, out, p: float, rng, stream=None) -> None:
     """out = drop(x) (bfloat16 or float16, any shape; out may be x): the mask of
     rng (device int64 {seed, offset}) over the flat elements."""
     w = "nf4_dropout"
-    dt, dev = _dtype16(x, w), x.device
+    dt, dev = _dtype16(x, w), x.get_device()
     xp = _fits(x, "x", w, x.shape, x.dtype, dev)
     op = _fits(out, "out", w, x.shape, x.dtype, dev)
-    _enqueue(lib().nf4_dropout, w, dev, stream, xp, x.numel(), dt, _rng_arg(p, rng, w, dev), op)
+    _enqueue(w, dev, stream, xp, x.numel(), dt, _rng_arg(p, rng, w, dev), op)
 
 
 def nf4_lora_project(x, w, h, scale: float = 1.0, backward: bool = False, p: float = 0.0, rng=None,
                      stream=None) -> None:
     """h [m, rank] = scale drop(x) w^T (x [m, k], w [rank, k]), or backward
     scale x w (w [k, rank]); bfloat16 or float16."""
-    import torch
     fn = "nf4_lora_project"
-    dt, dev = _dtype16(x, fn), x.device
-    _need(x.dim() == 2 and w.dim() == 2, fn, "x and w must have two dimensions")
+    dt, dev, t16 = _dtype16(x, fn), x.get_device(), x.dtype
+    if x.dim() != 2 or w.dim() != 2:
+        _misfit(fn, "x and w must have two dimensions")
     m, k = x.shape
     r = w.shape[1 if backward else 0]
-    xp = _fits(x, "x", fn, x.shape, x.dtype, dev)
-    wp = _fits(w, "w", fn, torch.Size((k, r) if backward else (r, k)), x.dtype, dev)
-    hp = _fits(h, "h", fn, torch.Size((m, r)), x.dtype, dev)
-    _enqueue(lib().nf4_lora_project, fn, dev, stream, xp, m, k, wp, r, dt, int(bool(backward)), float(scale),
-             _rng_arg(p, rng, fn, dev), hp)
+    xp = _fits(x, "x", fn, (m, k), t16, dev)
+    wp = _fits(w, "w", fn, (k, r) if backward else (r, k), t16, dev)
+    hp = _fits(h, "h", fn, (m, r), t16, dev)
+    _enqueue(fn, dev, stream, xp, m, k, wp, r, dt, 1 if backward else 0, scale, _rng_arg(p, rng, fn, dev), hp)
 
 
 def nf4_lora_grad(u, x, grad, ws=None, side: str = "A", p: float = 0.0, rng=None, stream=None) -> None:
@@ -498,16 +513,18 @@ def nf4_lora_grad(u, x, grad, ws=None, side: str = "A", p: float = 0.0, rng=None
     when that is 0."""
     import torch
     fn = "nf4_lora_grad"
-    dt, dev = _dtype16(x, fn), x.device
-    _need(x.dim() == 2 and u.dim() == 2, fn, "u and x must have two dimensions")
-    _need(side in ("A", "B"), fn, "side must be 'A' or 'B'")
+    dt, dev, t16 = _dtype16(x, fn), x.get_device(), x.dtype
+    if x.dim() != 2 or u.dim() != 2:
+        _misfit(fn, "u and x must have two dimensions")
+    if side != "A" and side != "B":
+        _misfit(fn, "side must be 'A' or 'B'")
     m, n = x.shape
     r = u.shape[1]
-    xp = _fits(x, "x", fn, x.shape, x.dtype, dev)
-    up = _fits(u, "u", fn, torch.Size((m, r)), x.dtype, dev)
-    gp = _fits(grad, "grad", fn, torch.Size((r, n) if side == "A" else (n, r)), torch.float32, dev)
+    xp = _fits(x, "x", fn, (m, n), t16, dev)
+    up = _fits(u, "u", fn, (m, r), t16, dev)
+    gp = _fits(grad, "grad", fn, (r, n) if side == "A" else (n, r), torch.float32, dev)
     wp, wb = _ws_arg(ws, fn, dev)
-    _enqueue(lib().nf4_lora_grad, fn, dev, stream, up, xp, m, n, r, dt, NF4_LORA_A if side == "A" else NF4_LORA_B,
+    _enqueue(fn, dev, stream, up, xp, m, n, r, dt, NF4_LORA_A if side == "A" else NF4_LORA_B,
              _rng_arg(p, rng, fn, dev), gp, wp, wb)
 
 
