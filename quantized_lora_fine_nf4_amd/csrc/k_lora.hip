@@ -77,7 +77,7 @@ __device__ __forceinline__ u32x4 drop8(const u32x4& x, const Bits128& b, uint32_
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const f32x2 v = unpack2<DT>(x[j]);
-        r[j] = pack2<DT>(v.x * keep, v.y * keep) & keep_mask2(b.w[j], thr);
+        r[j] = keep2(pack2<DT>(v.x * keep, v.y * keep), b.w[j], thr);
     }
     return r;
 }
@@ -317,71 +317,96 @@ __global__ __launch_bounds__(64 * W) void k_lora_project(ProjArgs g)
     const int r0 = blockIdx.y * (16 * RT);
     PhiloxKey key = {};
     if constexpr (DROP) key = philox_key(g.drop.rng);
-    int64_t xrow[MB];
+    // Loads address a uniform base, advanced per chunk, plus a 32-bit lane
+    // offset (k is below 2^27).  Rows and ranks past the end repeat the last
+    // one: they feed only results that are not stored.
+    uint32_t xo[MB], wo[RT];
+    const uint16_t* wb[RT];
+    uint64_t grp[MB];   // mask group of this lane's k in the row, chunk at 0
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
-        const int64_t r = m0 + 16 * b + q;
-        xrow[b] = (r < g.m ? r : g.m - 1) * g.k;
+        const int64_t left = g.m - 1 - m0;
+        const uint32_t r = 16 * b + q < left ? 16 * b + q : (uint32_t)left;
+        xo[b] = (uint32_t)(r * g.k + 8 * kg) * 2;
+        if constexpr (DROP) grp[b] = (uint64_t)((m0 + r) * g.k + 8 * kg) >> 3;
     }
-    int64_t wrow[RT];
+    if constexpr (MODE == PROJ_FWD || MODE == PROJ_DROP) {
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-        const int r = r0 + 16 * j + q;
-        wrow[j] = (int64_t)(r < g.rank ? r : g.rank - 1) * g.k;
+        for (int j = 0; j < RT; ++j) {
+            const int rb = r0 + 16 * j < g.rank ? r0 + 16 * j : r0, left = g.rank - 1 - rb;
+            wb[j] = g.w + (int64_t)rb * g.k;
+            wo[j] = (uint32_t)((int64_t)(q < left ? q : left) * g.k + 8 * kg) * 2;
+        }
     }
     f32x4 acc[MB][RT];
 #pragma unroll
     for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // k of step s of the chunk at k0; past the end the last eight again (zeroed below)
-    auto at = [&](int64_t k0, int s) { const int64_t kk = k0 + 32 * s + 8 * kg; return kk < g.k ? kk : g.k - 8; };
-    u32x4 x[MB][2];
+    const uint16_t* xb = g.x + m0 * g.k;
+    auto ld = [](const uint16_t* base, uint32_t off) {
+        return *(const GLOBAL u32x4*)((const GLOBAL uint8_t*)base + off);
+    };
+    // operand tiles of the step at k = ks; off: the lane's byte shift (0 in whole steps)
+    auto load_w = [&](int64_t ks, int32_t off, u32x4 (&w)[RT]) {
+        if constexpr (MODE == PROJ_BACK) load_tile<RT>(g.w, g.k, g.rank, ks, r0, w);
+        else if constexpr (MODE == PROJ_BACK_ANY) gather_tile<RT>(g.w, g.k, g.rank, ks, r0, w);
+        else {
+#pragma unroll
+            for (int j = 0; j < RT; ++j) w[j] = ld(wb[j] + ks, wo[j] + off);
+        }
+    };
+    auto step = [&](int64_t ks, bool in, u32x4 (&a)[MB], u32x4 (&w)[RT]) {
+        u32x4 f[RT];
+        if constexpr (MODE == PROJ_BACK) transpose_tile<RT>(w, (uint16_t*)(s_mem + wv * RT * 1024), f);
+        else {
+#pragma unroll
+            for (int j = 0; j < RT; ++j) f[j] = w[j];
+        }
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+            if constexpr (DROP) {
+                const Bits128 bits = philox7(key, grp[b] + (uint64_t)(ks >> 3));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[b][j] = keep2(a[b][j], bits.w[j], g.drop.thr);
+            }
+            if (!in) a[b] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < RT; ++j) acc[b][j] = mfma<DT>(a[b], f[j], acc[b][j]);
+        }
+    };
+    // whole chunks, the next one's x in flight (at the end the same one again, unused)
+    u32x4 x[2][MB];
     auto load_x = [&](int64_t k0) {
 #pragma unroll
-        for (int b = 0; b < MB; ++b)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) x[b][s] = *(const GLOBAL u32x4*)(g.x + xrow[b] + at(k0, s));
+            for (int b = 0; b < MB; ++b) x[s][b] = ld(xb + k0 + 32 * s, xo[b]);
     };
     int64_t k0 = (int64_t)wv * 64;
-    if (k0 < g.k) load_x(k0);
-    for (; k0 < g.k; k0 += 64 * W) {
-        u32x4 a[MB][2], w[2][RT];
+    if (k0 + 64 <= g.k) load_x(k0);
+    for (; k0 + 64 <= g.k; k0 += 64 * W) {
+        u32x4 a[2][MB], w[2][RT];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            if constexpr (MODE == PROJ_BACK) load_tile<RT>(g.w, g.k, g.rank, k0 + 32 * s, r0, w[s]);
-            else if constexpr (MODE == PROJ_BACK_ANY) gather_tile<RT>(g.w, g.k, g.rank, k0 + 32 * s, r0, w[s]);
-            else {
+            load_w(k0 + 32 * s, 0, w[s]);
 #pragma unroll
-                for (int j = 0; j < RT; ++j) w[s][j] = *(const GLOBAL u32x4*)(g.w + wrow[j] + at(k0, s));
-            }
+            for (int b = 0; b < MB; ++b) a[s][b] = x[s][b];
         }
+        load_x(k0 + 64 * W + 64 <= g.k ? k0 + 64 * W : k0);
 #pragma unroll
-        for (int b = 0; b < MB; ++b)
+        for (int s = 0; s < 2; ++s) step(k0 + 32 * s, true, a[s], w[s]);
+    }
+    // the last partial chunk (of one wave): lanes past the end load the last eight k and count as zero
+    for (int s = 0; s < 2; ++s) {
+        const int64_t ks = k0 + 32 * s, over = ks + 8 * kg + 8 - g.k;
+        if (ks >= g.k) break;
+        const int32_t off = over > 0 ? (int32_t)(-2 * over) : 0;
+        u32x4 a[MB], w[RT];
+        load_w(ks, off, w);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) a[b][s] = x[b][s];
-        if (k0 + 64 * W < g.k) load_x(k0 + 64 * W);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if constexpr (MODE == PROJ_BACK) {
-                u32x4 f[RT];
-                transpose_tile<RT>(w[s], (uint16_t*)(s_mem + wv * RT * 1024), f);
-#pragma unroll
-                for (int j = 0; j < RT; ++j) w[s][j] = f[j];
-            }
-            const bool in = k0 + 32 * s + 8 * kg < g.k;
-#pragma unroll
-            for (int b = 0; b < MB; ++b) {
-                if constexpr (DROP) {
-                    const Bits128 bits = philox7(key, (uint64_t)(xrow[b] + at(k0, s)) >> 3);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) a[b][s][j] &= keep_mask2(bits.w[j], g.drop.thr);
-                }
-                if (!in) a[b][s] = u32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < RT; ++j) acc[b][j] = mfma<DT>(a[b][s], w[s][j], acc[b][j]);
-            }
-        }
+        for (int b = 0; b < MB; ++b) a[b] = ld(xb + ks, xo[b] + off);
+        step(ks, over <= 0, a, w);
     }
     if constexpr (kTile > 0) __syncthreads();   // every wave done with its tile
     float* s_acc = (float*)s_mem;
@@ -484,7 +509,7 @@ __global__ __launch_bounds__(64 * kGradWaves<RT>) void k_lora_grad(GradArgs g)
             if constexpr (DROP) {
                 const Bits128 bits = philox7(key, (uint64_t)(row * g.n + nc) >> 3);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[i][j] &= keep_mask2(bits.w[j], g.drop.thr);
+                for (int j = 0; j < 4; ++j) x[i][j] = keep2(x[i][j], bits.w[j], g.drop.thr);
             }
             if (row >= s1) x[i] = u32x4{0, 0, 0, 0};
         }

@@ -38,9 +38,10 @@ __device__ __forceinline__ Bits128 philox7(const PhiloxKey& key, uint64_t group)
 #pragma unroll
     for (int i = 0; i < 7; ++i) {
         const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
-        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+        // the three-input exclusive or in one instruction (truth table 0x96)
+        c0 = __builtin_amdgcn_bitop3_b32((uint32_t)(p1 >> 32), c1, k0, 0x96);
         c1 = (uint32_t)p1;
-        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+        c2 = __builtin_amdgcn_bitop3_b32((uint32_t)(p0 >> 32), c3, k1, 0x96);
         c3 = (uint32_t)p0;
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
@@ -48,12 +49,15 @@ __device__ __forceinline__ Bits128 philox7(const PhiloxKey& key, uint64_t group)
     return Bits128{{c0, c1, c2, c3}};
 }
 
-// Two 16-bit lanes as a mask: each half all ones iff that lane >= thr (thr >= 1).
-__device__ __forceinline__ uint32_t keep_mask2(uint32_t w, uint32_t thr)
+// x with the half whose 16-bit lane of w is below thr (thr >= 1) set to zero:
+// the lanes as signed values around thr (both less 2^15), their saturated
+// difference, its sign spread over the half.
+__device__ __forceinline__ uint32_t keep2(uint32_t x, uint32_t w, uint32_t thr)
 {
-    const uint32_t lo = (w & 0xffffu) >= thr ? 0x0000ffffu : 0u;
-    const uint32_t hi = (w >> 16) >= thr ? 0xffff0000u : 0u;
-    return lo | hi;
+    typedef int16_t s16x2 __attribute__((ext_vector_type(2)));
+    const int16_t t = (int16_t)(thr ^ 0x8000u);
+    const s16x2 d = __builtin_elementwise_sub_sat(__builtin_bit_cast(s16x2, w ^ 0x80008000u), s16x2{t, t});
+    return x & ~__builtin_bit_cast(uint32_t, d >> 15);
 }
 
 // Bit i set iff element i of the group is kept.
