@@ -231,17 +231,23 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_wave_barrier();
 }
 
+__device__ __forceinline__ u32x4 ld16(const uint16_t* base, uint32_t off)
+{
+    return *(const GLOBAL u32x4*)((const GLOBAL uint8_t*)base + off);
+}
+
 // Rows k0 .. k0 + 31 (past `rows` the last row again), ranks r0 .. r0 + 16 RT
 // - 1 of p [rows x rank], rank a multiple of 8: 16-byte piece t * 64 + lane.
 template <int RT>
 __device__ __forceinline__ void load_tile(const uint16_t* p, int64_t rows, int rank, int64_t k0, int r0, u32x4 (&d)[RT])
 {
     const int lane = threadIdx.x & 63;
+    const uint16_t* base = p + k0 * rank;
+    const int left = k0 + 32 <= rows ? 31 : (int)(rows - 1 - k0);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        const int item = t * 64 + lane, r = r0 + 8 * (item % (2 * RT));
-        const int64_t k = k0 + item / (2 * RT);
-        d[t] = *(const GLOBAL u32x4*)(p + (k < rows ? k : rows - 1) * rank + (r < rank ? r : rank - 8));
+        const int item = t * 64 + lane, r = r0 + 8 * (item % (2 * RT)), k = item / (2 * RT);
+        d[t] = ld16(base, (uint32_t)((k < left ? k : left) * rank + (r < rank ? r : rank - 8)) * 2);
     }
 }
 
@@ -288,10 +294,14 @@ __device__ __forceinline__ void gather_tile(const uint16_t* p, int64_t rows, int
 // ---- the adapter's down product
 //
 // h[m x rank] = alpha (keep . x) W, reduction over k.  A workgroup takes
-// 16 MB rows of x and 16 RT ranks; its W waves share the reduction in chunks of
+// 16 MB rows of x and 16 RT ranks; its waves share the reduction in chunks of
 // 64 k (two 16 x 16 x 32 MFMA steps; lane l holds x row l % 16, k 8 (l / 16)
-// .. + 7 of a step), the next chunk's x loaded while this one multiplies, and
-// their sums are added pairwise in LDS.
+// .. + 7 of a step), the next chunk loaded while this one multiplies, and their
+// sums are added pairwise in LDS.  x goes straight to fragments; W goes through
+// LDS, so that memory is read in whole 128-byte lines (fragments read straight
+// from its rows, 64 bytes each, took 1.5 times as long at rank 64).  Bound by
+// x's bytes at rank 16 (4096 x 5120 in 9.3 us, 4.5 TB/s; 4096 x 13824 backward
+// in 26 us), by the reads of W from the L2 above: every 16 or 32 rows read all of it.
 enum ProjMode { PROJ_FWD, PROJ_DROP, PROJ_BACK, PROJ_BACK_ANY };   // forward, with dropout, backward, any rank
 
 struct ProjArgs {
@@ -304,12 +314,18 @@ struct ProjArgs {
     DropArgs drop;
 };
 
-template <int DT, int MODE, int MB, int RT, int W>
-__global__ __launch_bounds__(64 * W) void k_lora_project(ProjArgs g)
+constexpr int kProjWaves = 8;    // 256 registers a wave: the next chunk of x and W fits (16 waves: 10-15% slower)
+constexpr int kProjPitch = 72;   // staged W row of 64 k (144 B: conflict-free 16-byte reads)
+
+template <int DT, int MODE, int MB, int RT>
+__global__ __launch_bounds__(64 * kProjWaves) void k_lora_project(ProjArgs g)
 {
+    constexpr int W = kProjWaves;
     constexpr bool DROP = MODE == PROJ_DROP;
     // the waves' operand tiles, then the sums
-    constexpr int kTile = MODE == PROJ_BACK ? W * RT * 1024 : 0, kSums = W / 2 * MB * RT * 1024;
+    constexpr bool FWD = MODE == PROJ_FWD || MODE == PROJ_DROP;
+    constexpr int kWave = FWD ? 16 * RT * kProjPitch * 2 : MODE == PROJ_BACK ? RT * 1024 : 0;
+    constexpr int kTile = W * kWave, kSums = W / 2 * MB * RT * 1024;
     __shared__ __attribute__((aligned(16))) uint8_t s_mem[kTile > kSums ? kTile : kSums > 0 ? kSums : 16];
     const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
     const int q = lane & 15, kg = lane >> 4;
@@ -320,8 +336,7 @@ __global__ __launch_bounds__(64 * W) void k_lora_project(ProjArgs g)
     // Loads address a uniform base, advanced per chunk, plus a 32-bit lane
     // offset (k is below 2^27).  Rows and ranks past the end repeat the last
     // one: they feed only results that are not stored.
-    uint32_t xo[MB], wo[RT];
-    const uint16_t* wb[RT];
+    uint32_t xo[MB];
     uint64_t grp[MB];   // mask group of this lane's k in the row, chunk at 0
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
@@ -330,83 +345,106 @@ __global__ __launch_bounds__(64 * W) void k_lora_project(ProjArgs g)
         xo[b] = (uint32_t)(r * g.k + 8 * kg) * 2;
         if constexpr (DROP) grp[b] = (uint64_t)((m0 + r) * g.k + 8 * kg) >> 3;
     }
-    if constexpr (MODE == PROJ_FWD || MODE == PROJ_DROP) {
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            const int rb = r0 + 16 * j < g.rank ? r0 + 16 * j : r0, left = g.rank - 1 - rb;
-            wb[j] = g.w + (int64_t)rb * g.k;
-            wo[j] = (uint32_t)((int64_t)(q < left ? q : left) * g.k + 8 * kg) * 2;
-        }
-    }
     f32x4 acc[MB][RT];
 #pragma unroll
     for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const uint16_t* xb = g.x + m0 * g.k;
-    auto ld = [](const uint16_t* base, uint32_t off) {
-        return *(const GLOBAL u32x4*)((const GLOBAL uint8_t*)base + off);
-    };
-    // operand tiles of the step at k = ks; off: the lane's byte shift (0 in whole steps)
-    auto load_w = [&](int64_t ks, int32_t off, u32x4 (&w)[RT]) {
-        if constexpr (MODE == PROJ_BACK) load_tile<RT>(g.w, g.k, g.rank, ks, r0, w);
-        else if constexpr (MODE == PROJ_BACK_ANY) gather_tile<RT>(g.w, g.k, g.rank, ks, r0, w);
-        else {
+    uint16_t* tile = (uint16_t*)(s_mem + wv * kWave);
+    // W of the 64 k at k0 (over: how far they run past the end): forward rows 8 t
+    // + lane / 8 of the rank tile, 16-byte piece lane % 8; backward one 32-row
+    // tile or fragment set per step
+    auto load_w = [&](int64_t k0, int over, u32x4 (&w)[2 * RT]) {
+        if constexpr (FWD) {
+            const int piece = lane & 7, last = 7 - over / 8;
 #pragma unroll
-            for (int j = 0; j < RT; ++j) w[j] = ld(wb[j] + ks, wo[j] + off);
-        }
-    };
-    auto step = [&](int64_t ks, bool in, u32x4 (&a)[MB], u32x4 (&w)[RT]) {
-        u32x4 f[RT];
-        if constexpr (MODE == PROJ_BACK) transpose_tile<RT>(w, (uint16_t*)(s_mem + wv * RT * 1024), f);
-        else {
-#pragma unroll
-            for (int j = 0; j < RT; ++j) f[j] = w[j];
-        }
-#pragma unroll
-        for (int b = 0; b < MB; ++b) {
-            if constexpr (DROP) {
-                const Bits128 bits = philox7(key, grp[b] + (uint64_t)(ks >> 3));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) a[b][j] = keep2(a[b][j], bits.w[j], g.drop.thr);
+            for (int t = 0; t < 2 * RT; ++t) {
+                const int rb = r0 + 8 * t < g.rank ? r0 + 8 * t : r0, left = g.rank - 1 - rb, r = lane >> 3;
+                w[t] = ld16(g.w + rb * g.k + k0, (uint32_t)((r < left ? r : left) * g.k + 8 * (piece < last ? piece : last)) * 2);
             }
-            if (!in) a[b] = u32x4{0, 0, 0, 0};
+        } else {
 #pragma unroll
-            for (int j = 0; j < RT; ++j) acc[b][j] = mfma<DT>(a[b], f[j], acc[b][j]);
+            for (int s = 0; s < 2; ++s) {
+                if (32 * s >= 64 - over) break;   // no step there (uniform)
+                u32x4 d[RT];
+                if constexpr (MODE == PROJ_BACK) load_tile<RT>(g.w, g.k, g.rank, k0 + 32 * s, r0, d);
+                else gather_tile<RT>(g.w, g.k, g.rank, k0 + 32 * s, r0, d);
+#pragma unroll
+                for (int j = 0; j < RT; ++j) w[s * RT + j] = d[j];
+            }
         }
     };
-    // whole chunks, the next one's x in flight (at the end the same one again, unused)
-    u32x4 x[2][MB];
-    auto load_x = [&](int64_t k0) {
+    auto load_x = [&](int64_t k0, int over, u32x4 (&x)[2][MB]) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (over && 32 * s >= 64 - over) break;   // no step there (uniform)
+            // lanes past the end load the step's last eight k (past <= 8 kg: never before the row)
+            const int past = 32 * s + 8 * kg + 8 - (64 - over);
+            const int32_t back = over && past > 0 ? -2 * past : 0;
+#pragma unroll
+            for (int b = 0; b < MB; ++b) x[s][b] = ld16(xb + k0 + 32 * s, xo[b] + back);
+        }
+    };
+    auto multiply = [&](int64_t k0, int over, u32x4 (&x)[2][MB], u32x4 (&w)[2 * RT]) {
+        if constexpr (FWD) {
+            wave_sync();
+#pragma unroll
+            for (int t = 0; t < 2 * RT; ++t) *(u32x4*)(tile + (8 * t + (lane >> 3)) * kProjPitch + 8 * (lane & 7)) = w[t];
+            wave_sync();
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (over && 32 * s >= 64 - over) break;
+            u32x4 f[RT];
+            if constexpr (FWD) {
+#pragma unroll
+                for (int j = 0; j < RT; ++j) f[j] = *(const u32x4*)(tile + (16 * j + q) * kProjPitch + 32 * s + 8 * kg);
+            } else {
+                u32x4 d[RT];
+#pragma unroll
+                for (int j = 0; j < RT; ++j) d[j] = f[j] = w[s * RT + j];
+                if constexpr (MODE == PROJ_BACK) transpose_tile<RT>(d, tile, f);
+            }
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                u32x4 a = x[s][b];
+                if constexpr (DROP) {
+                    const Bits128 bits = philox7(key, grp[b] + (uint64_t)((k0 + 32 * s) >> 3));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[j] = keep2(a[j], bits.w[j], g.drop.thr);
+                }
+                if (over && 32 * s + 8 * kg >= 64 - over) a = u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < RT; ++j) acc[b][j] = mfma<DT>(a, f[j], acc[b][j]);
+            }
+        }
+    };
+    // whole chunks, the next one in flight (at the end the same one again, unused)
+    u32x4 x[2][MB], w[2 * RT];
+    int64_t k0 = (int64_t)wv * 64;
+    if (k0 + 64 <= g.k) {
+        load_x(k0, 0, x);
+        load_w(k0, 0, w);
+    }
+    for (; k0 + 64 <= g.k; k0 += 64 * W) {
+        const int64_t kn = k0 + 64 * W + 64 <= g.k ? k0 + 64 * W : k0;
+        u32x4 xc[2][MB], wc[2 * RT];
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int b = 0; b < MB; ++b) x[s][b] = ld(xb + k0 + 32 * s, xo[b]);
-    };
-    int64_t k0 = (int64_t)wv * 64;
-    if (k0 + 64 <= g.k) load_x(k0);
-    for (; k0 + 64 <= g.k; k0 += 64 * W) {
-        u32x4 a[2][MB], w[2][RT];
+            for (int b = 0; b < MB; ++b) xc[s][b] = x[s][b];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            load_w(k0 + 32 * s, 0, w[s]);
-#pragma unroll
-            for (int b = 0; b < MB; ++b) a[s][b] = x[s][b];
-        }
-        load_x(k0 + 64 * W + 64 <= g.k ? k0 + 64 * W : k0);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) step(k0 + 32 * s, true, a[s], w[s]);
+        for (int t = 0; t < 2 * RT; ++t) wc[t] = w[t];
+        load_x(kn, 0, x);
+        load_w(kn, 0, w);
+        multiply(k0, 0, xc, wc);
     }
-    // the last partial chunk (of one wave): lanes past the end load the last eight k and count as zero
-    for (int s = 0; s < 2; ++s) {
-        const int64_t ks = k0 + 32 * s, over = ks + 8 * kg + 8 - g.k;
-        if (ks >= g.k) break;
-        const int32_t off = over > 0 ? (int32_t)(-2 * over) : 0;
-        u32x4 a[MB], w[RT];
-        load_w(ks, off, w);
-#pragma unroll
-        for (int b = 0; b < MB; ++b) a[b] = ld(xb + ks, xo[b] + off);
-        step(ks, over <= 0, a, w);
+    if (k0 < g.k) {   // the last partial chunk, of one wave
+        const int over = (int)(k0 + 64 - g.k);
+        load_x(k0, over, x);
+        load_w(k0, over, w);
+        multiply(k0, over, x, w);
     }
     if constexpr (kTile > 0) __syncthreads();   // every wave done with its tile
     float* s_acc = (float*)s_mem;
@@ -648,25 +686,33 @@ hipError_t launch_act_grad(int dtype, const void* dy, const void* z, int act, in
 
 namespace {
 
-template <int DT, int MODE, int MB, int RT, int W>
+template <int DT, int MODE, int MB, int RT>
 hipError_t project_go(const ProjArgs& g, hipStream_t s)
 {
     const dim3 grid((unsigned)((g.m + 16 * MB - 1) / (16 * MB)), (unsigned)((g.rank + 16 * RT - 1) / (16 * RT)));
-    hipLaunchKernelGGL((k_lora_project<DT, MODE, MB, RT, W>), grid, dim3(64 * W), 0, s, g);
+    hipLaunchKernelGGL((k_lora_project<DT, MODE, MB, RT>), grid, dim3(64 * kProjWaves), 0, s, g);
     return hipGetLastError();
 }
 
-// Few rows: one 16-rank tile per workgroup, so that there are more of them;
-// otherwise a workgroup takes all ranks, so that x is read (and its mask
-// computed) once, and 32 rows where those still make a workgroup per CU.
+// The fewest ranks per workgroup (16, 32, 64) that still make one round of the
+// 256 CUs: few rows get a workgroup per rank tile, many rows read x (and compute
+// its mask) once; past one round 32 rows at a time, so that W is read half as
+// often.  At 5120 k, rank 64 with 16 / 32 / 64 ranks at a time: 1000 rows 9.6 /
+// 10.7 / 15.0 us, 2048 rows 16.1 / 11.1 / 15.4, 3000 rows 23.1 / 20.4 / 15.8;
+// 64 ranks and 16 / 32 rows at a time: 6000 rows 32.2 / 26.1, 8192 rows 39.3 /
+// 28.5.
 template <int DT, int MODE>
 hipError_t project_shape(const ProjArgs& g, hipStream_t s)
 {
-    if (g.m <= 1024 || g.rank <= 16) return project_go<DT, MODE, 1, 1, 16>(g, s);
-    const bool two = g.m >= 32 * 256;
-    if (g.rank <= 32) return two ? project_go<DT, MODE, 2, 2, 16>(g, s) : project_go<DT, MODE, 1, 2, 16>(g, s);
-    if (g.rank <= 64) return two ? project_go<DT, MODE, 2, 4, 16>(g, s) : project_go<DT, MODE, 1, 4, 16>(g, s);
-    return two ? project_go<DT, MODE, 2, 8, 8>(g, s) : project_go<DT, MODE, 1, 8, 8>(g, s);
+    const int64_t tiles = (g.m + 15) / 16;
+    const int cover = g.rank <= 16 ? 1 : g.rank <= 32 ? 2 : 4;
+    auto groups = [&](int rt) { return tiles * ((g.rank + 16 * rt - 1) / (16 * rt)); };
+    int rt = 1;
+    while (rt < cover && groups(rt) > 256) rt *= 2;
+    const bool two = groups(rt) > 256;
+    if (rt == 1) return two ? project_go<DT, MODE, 2, 1>(g, s) : project_go<DT, MODE, 1, 1>(g, s);
+    if (rt == 2) return two ? project_go<DT, MODE, 2, 2>(g, s) : project_go<DT, MODE, 1, 2>(g, s);
+    return two ? project_go<DT, MODE, 2, 4>(g, s) : project_go<DT, MODE, 1, 4>(g, s);
 }
 
 template <int DT>
