@@ -21,6 +21,7 @@ hipError_t launch_nf4_linear(int dtype, const uint8_t* codes, const int8_t* qabs
 {
     const GemmArgs g = gemm_args(codes, qabsmax, scale2, absmax, rows, cols, forward, x, m, out, part, nsplit,
                                  tail_split);
+    if (epi.drop.thr) return gemm_any(dtype, forward, qabsmax != nullptr, out_f32, g, WithDrop{epi}, s);
     return gemm_any(dtype, forward, qabsmax != nullptr, out_f32, g, WithEpi{epi}, s);
 }
 

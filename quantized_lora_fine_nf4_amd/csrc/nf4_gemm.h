@@ -301,18 +301,22 @@ __device__ __forceinline__ void group_coords(int64_t tile, int64_t mtiles, int64
 // u and v staged in LDS by each wave for its own rows and columns: on the same
 // accumulators, or under dropout on accumulators of their own, 32 rows at a
 // time, whose kept values are added where the sums are stored.  The mask comes
-// from one generator call per group of eight elements, kept in LDS as one byte
-// per group (the accumulators hold one column per lane, so a lane's own
-// elements would each cost a call).  With a split reduction the first split
+// from one generator call per group of eight elements, where a lane holds eight
+// consecutive columns of a row: after the accumulators (one column per lane)
+// have gone through LDS, or (128 x 128 kernel) kept there as one byte a group.  With a split reduction the first split
 // adds the low-rank term.  The rest is applied where the final value is stored:
 // from the accumulators through LDS, so that a lane handles eight consecutive
 // columns and every access is 16 bytes, or in the kernel that adds the splits.
 // All of it is private to a wave: no barrier.
 struct NoEpi {
-    static constexpr bool kOn = false;
+    static constexpr bool kOn = false, kDrop = false;
 };
 struct WithEpi {
-    static constexpr bool kOn = true;
+    static constexpr bool kOn = true, kDrop = false;
+    EpiArgs a;
+};
+struct WithDrop {   // backward, the low-rank term under dropout
+    static constexpr bool kOn = true, kDrop = true;
     EpiArgs a;
 };
 
@@ -320,12 +324,23 @@ constexpr int kEpiPitch = 68;                              // fp32 values per st
 constexpr int kEpiWave = 128 * kEpiPitch * 4;              // bytes per wave, 256 x 256 kernels: 128 rows
 constexpr int kEpiWaveSmall = (kBM + kBN) * kLdp * 2 / 4;  // 128 x 128 kernel: 9,216
 constexpr int kEpiRanks = 32, kEpiRanksSmall = 16;         // ranks of u and v staged at a time
-constexpr int kMaxRank = 128;                              // under dropout, ranks of v staged at a time (256 x 256)
-constexpr int kEpiMask = 256 * 8;                          // mask bytes of 256 rows
+constexpr int kMaxRank = 128;                              // under dropout, all of v (256 x 256)
 constexpr int kEpiRow = 32 * kEpiPitch * 4;                // staged output of 32 rows
 static_assert((64 + 256) * (kEpiRanks + 8) * 2 <= kEpiWave, "staged v and u");
-static_assert(64 * (kMaxRank + 8) * 2 + kEpiMask + kEpiRow <= kEpiWave, "staged v, mask and output rows");
+static_assert(64 * kMaxRank * 2 + 2 * kEpiRow <= kEpiWave, "staged v, products and low-rank terms");
 static_assert((64 + kWM) * (kEpiRanksSmall + 8) * 2 <= kEpiWaveSmall && kEpiRow <= kEpiWaveSmall, "128 x 128 kernel");
+
+// Keeps the accumulators in accumulation registers up to here: without it the
+// epilogue's other uses of them drew some of them into vector registers, and the
+// main loop moved 32 to 128 of them forth and back each step.
+template <int MT>
+__device__ __forceinline__ void pin_acc(f32x16 (&acc)[MT][2])
+{
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) __asm__ volatile("" : "+a"(acc[i][j]));
+}
 
 // Orders a wave's LDS writes before its own lanes' later reads (and the
 // reverse); LDS executes one wave's accesses in order.
@@ -335,31 +350,61 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_wave_barrier();
 }
 
-// Values k .. k + 7 of a row of R 16-bit values with the given element stride;
-// zero from R on.
-__device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t stride, int k, int R)
+// Values k .. k + 7 of a row of R 16-bit values; zero from R on.
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, int k, int R)
 {
     u32x4 d = {0u, 0u, 0u, 0u};
     if (k >= R) return d;
-    if (stride == 1 && (R & 7) == 0) return *(const GLOBAL u32x4*)(row + k);
+    if ((R & 7) == 0) return *(const GLOBAL u32x4*)(row + k);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-        const uint32_t v = k + t < R ? ((const GLOBAL uint16_t*)row)[(k + t) * stride] : (uint16_t)0;
-        d[t >> 1] |= v << (16 * (t & 1));
+        const uint32_t v = ((const GLOBAL uint16_t*)row)[k + t < R ? k + t : R - 1];
+        d[t >> 1] |= (k + t < R ? v : 0u) << (16 * (t & 1));
     }
     return d;
 }
 
-// The wave's 64 columns of v, ranks k0 .. k0 + n - 1 (n a multiple of 8), to
-// LDS with the rank contiguous.
+// The wave's 64 columns of v, ranks k0 .. k0 + n - 1 (n a multiple of 16; zero
+// from the rank on), to LDS: forward [64][pitch], the rank contiguous as in
+// memory; backward [n][64], read back transposed.
 template <bool FWD>
 __device__ __forceinline__ void stage_v(const EpiArgs& e, int64_t ncol, int64_t c0, int k0, int n, int pitch, uint16_t* vs)
 {
     const int lane = threadIdx.x & 63;
-    const uint16_t* src = FWD ? e.v + (c0 + lane) * e.rank : e.v + c0 + lane;
-#pragma unroll 1
-    for (int g = 0; g < n; g += 8)
-        *(u32x4*)(vs + lane * pitch + g) = load8(src, FWD ? 1 : ncol, k0 + g, e.rank);
+    if constexpr (FWD) {
+        const uint16_t* src = e.v + (c0 + lane) * e.rank;
+#pragma unroll 2
+        for (int g = 0; g < n; g += 8) *(u32x4*)(vs + lane * pitch + g) = load8(src, k0 + g, e.rank);
+    } else {
+        const int cg = lane & 7;
+#pragma unroll 4
+        for (int g = lane >> 3; g < n; g += 8) {   // rank k0 + g, columns 8 cg .. + 7
+            const int k = k0 + g < e.rank ? k0 + g : e.rank - 1;
+            u32x4 d = *(const GLOBAL u32x4*)(e.v + k * ncol + c0 + 8 * cg);
+            if (k0 + g >= e.rank) d = u32x4{0u, 0u, 0u, 0u};
+            *(u32x4*)(vs + g * 64 + 8 * cg) = d;
+        }
+    }
+}
+
+// Fragment of columns 32 j .. + 31, ranks k .. k + 15 of the staged v.
+template <int DT, bool FWD>
+__device__ __forceinline__ typename Frag8<DT>::T frag_v(const uint16_t* vs, int pitch, int j, int k)
+{
+    typedef typename Frag8<DT>::T F;
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5;
+    if constexpr (FWD) {
+        return *(const F*)(vs + (32 * j + q) * pitch + k + 8 * h);
+    } else {
+        u32x2 d[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            d[t] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(vs + (k + 8 * h + 4 * t + ((lane & 15) >> 2)) * 64 + 32 * j +
+                                                            16 * ((lane >> 4) & 1) + 4 * (lane & 3))));
+        return __builtin_bit_cast(F, u32x4{d[0].x, d[0].y, d[1].x, d[1].y});
+    }
 }
 
 // acc += the low-rank term of rows m0 .. m0 + 32 MT - 1, columns c0 .. c0 + 63
@@ -378,18 +423,18 @@ __device__ __forceinline__ void add_lowrank(const EpiArgs& e, int64_t M, int64_t
     for (int k0 = 0; k0 < R; k0 += CH) {
         wave_sync();
         stage_v<FWD>(e, ncol, c0, k0, CH, P, vs);
-#pragma unroll 1
+#pragma unroll 4
         for (int t = lane; t < 32 * MT * G; t += 64) {
             const int64_t row = m0 + t / G;
             *(u32x4*)(us + (t / G) * P + 8 * (t % G)) =
-                load8(e.u + (row < M ? row : M - 1) * R, 1, k0 + 8 * (t % G), R);
+                load8(e.u + (row < M ? row : M - 1) * R, k0 + 8 * (t % G), R);
         }
         wave_sync();
         F b[CH / 16][2];
 #pragma unroll
         for (int s = 0; s < CH / 16; ++s)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) b[s][j] = *(const F*)(vs + (32 * j + q) * P + 16 * s + 8 * h);
+            for (int j = 0; j < 2; ++j) b[s][j] = frag_v<DT, FWD>(vs, P, j, 16 * s);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -436,35 +481,60 @@ __device__ __forceinline__ void store16(uint16_t* p, const float (&v)[N])
     else *(GLOBAL u32x2*)p = u32x2{pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3])};
 }
 
+// The residual of N consecutive columns at element `at` (zero without one).
+template <int DT, bool OUT_F32, int N>
+__device__ __forceinline__ void load_residual(const EpiArgs& e, int64_t at, float (&r)[N])
+{
+    typedef float f4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = 0.0f;
+    if (!e.residual) return;
+    if constexpr (OUT_F32) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const f4 v = *(const GLOBAL f4*)((const float*)e.residual + at + i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[i + k] = v[k];
+        }
+    } else {
+        load16<DT, N>((const uint16_t*)e.residual + at, r);
+    }
+}
+
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float (&z)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = act_value(z[i], ACT);
+}
+
 // The epilogue of N consecutive columns at element `at` of the output; z holds
-// the product with its low-rank term.
+// the product with its low-rank term, res the residual (unused without one).
 template <int DT, bool FWD, bool OUT_F32, int N>
-__device__ __forceinline__ void finish(const EpiArgs& e, float (&z)[N], const float (&bias)[N], int64_t at, void* out)
+__device__ __forceinline__ void finish(const EpiArgs& e, float (&z)[N], const float (&bias)[N], const float (&res)[N],
+                                       int64_t at, void* out)
 {
     typedef float f4 __attribute__((ext_vector_type(4)));
     if constexpr (FWD) {
 #pragma unroll
         for (int i = 0; i < N; ++i) z[i] += bias[i];
         if (e.preact) store16<DT, N>(e.preact + at, z);
-        if (e.act != ACT_NONE) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = act_value(z[i], e.act);
+        switch (e.act) {
+            case ACT_RELU: act_all<ACT_RELU>(z); break;
+            case ACT_SILU: act_all<ACT_SILU>(z); break;
+            case ACT_GELU: act_all<ACT_GELU>(z); break;
+            case ACT_GELU_TANH: act_all<ACT_GELU_TANH>(z); break;
+            default: break;
         }
+    }
+    if (e.residual) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] += res[i];
     }
     if constexpr (OUT_F32) {
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            f4 o = {z[i], z[i + 1], z[i + 2], z[i + 3]};
-            if (e.residual) o += *(const GLOBAL f4*)((const float*)e.residual + at + i);
-            *(GLOBAL f4*)((float*)out + at + i) = o;
-        }
+        for (int i = 0; i < N; i += 4) *(GLOBAL f4*)((float*)out + at + i) = f4{z[i], z[i + 1], z[i + 2], z[i + 3]};
     } else {
-        if (e.residual) {
-            float r[N];
-            load16<DT, N>((const uint16_t*)e.residual + at, r);
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] += r[i];
-        }
         store16<DT, N>((uint16_t*)out + at, z);
     }
 }
@@ -477,14 +547,36 @@ __device__ __forceinline__ void load_bias(const EpiArgs& e, int64_t col, float (
     if (e.bias) load16<DT, N>(e.bias + col, b);
 }
 
+// Eight columns of row rl of a staged 32-row block.
+__device__ __forceinline__ void staged8(const float* s, int rl, int cc, float (&z)[8])
+{
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    const f4 a = *(const f4*)(s + rl * kEpiPitch + cc), b = *(const f4*)(s + rl * kEpiPitch + cc + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        z[i] = a[i];
+        z[4 + i] = b[i];
+    }
+}
+
+// A 32-row accumulator block to its staged rows.
+__device__ __forceinline__ void stage_block(float* s, const f32x16 (&a)[2])
+{
+    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[(8 * (r >> 2) + 4 * h + (r & 3)) * kEpiPitch + 32 * j + q] = a[j][r];
+}
+
 // The accumulators of rows m0 .. m0 + 32 MT - 1, columns c0 .. c0 + 63 through
-// the wave's LDS region (GI 32-row blocks at a time) to the output.
+// the wave's LDS region (GI 32-row blocks at a time) to the output; a block's
+// residual is loaded before its rows are read back.
 template <int DT, bool FWD, bool OUT_F32, int MT, int GI>
 __device__ __forceinline__ void store_epi(const EpiArgs& e, void* out, int64_t M, int64_t ncol, int64_t m0, int64_t c0,
                                           uint8_t* reg, const f32x16 (&acc)[MT][2])
 {
-    typedef float f4 __attribute__((ext_vector_type(4)));
-    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5, cc = 8 * (lane & 7);
+    const int lane = threadIdx.x & 63, cc = 8 * (lane & 7);
     float* s = (float*)reg;
     float bias[8];
     load_bias<DT, 8>(e, c0 + cc, bias);
@@ -492,66 +584,144 @@ __device__ __forceinline__ void store_epi(const EpiArgs& e, void* out, int64_t M
     for (int i0 = 0; i0 < MT; i0 += GI) {
         wave_sync();
 #pragma unroll
-        for (int i = 0; i < GI; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[(32 * i + 8 * (r >> 2) + 4 * h + (r & 3)) * kEpiPitch + 32 * j + q] = acc[i0 + i][j][r];
+        for (int i = 0; i < GI; ++i) stage_block(s + 32 * i * kEpiPitch, acc[i0 + i]);
         wave_sync();
 #pragma unroll 1
-        for (int p = 0; p < 4 * GI; ++p) {
-            const int rl = 8 * p + (lane >> 3);
-            const int64_t row = m0 + 32 * i0 + rl;
-            if (row < M) {
-                const f4 a = *(const f4*)(s + rl * kEpiPitch + cc), b = *(const f4*)(s + rl * kEpiPitch + cc + 4);
-                float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                finish<DT, FWD, OUT_F32, 8>(e, z, bias, row * ncol + c0 + cc, out);
+        for (int b = 0; b < GI; ++b) {
+            const int64_t row = m0 + 32 * (i0 + b) + (lane >> 3);
+            float res[4][8];
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (row + 8 * p < M) load_residual<DT, OUT_F32, 8>(e, (row + 8 * p) * ncol + c0 + cc, res[p]);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                if (row + 8 * p < M) {
+                    float z[8];
+                    staged8(s, 32 * b + 8 * p + (lane >> 3), cc, z);
+                    finish<DT, FWD, OUT_F32, 8>(e, z, bias, res[p], (row + 8 * p) * ncol + c0 + cc, out);
+                }
             }
         }
     }
 }
 
-// The backward store under dropout: acc + keep . (u v) / (1 - p), 32 rows at a
-// time, as the final value (out) or as the split's fp32 partial (element (row,
-// col) at part[row * ldp + col]).  SMALL: the 128 x 128 kernel's LDS (16 ranks
-// of v at a time, restaged for each 32 rows; the staged output replaces them).
-template <int DT, bool OUT_F32, bool PART, int MT, bool SMALL>
+// The 256 x 256 kernel's backward store under dropout: acc + keep . (u v) /
+// (1 - p), 32 rows at a time, as the final value (out) or as the split's fp32
+// partial (element (row, col) at part[row * ldp + col]; without `add` as for
+// rank 0).
+// Both terms go through LDS.
+template <int DT, bool OUT_F32, bool PART, int MT>
 __device__ __forceinline__ void store_drop(const EpiArgs& e, void* out, float* part, int64_t ldp, int64_t M,
-                                           int64_t ncol, int64_t m0, int64_t c0, uint8_t* reg, uint8_t* mask,
+                                           int64_t ncol, int64_t m0, int64_t c0, uint8_t* reg, bool add,
                                            const f32x16 (&acc)[MT][2])
 {
-    constexpr int CH = SMALL ? kEpiRanksSmall : kMaxRank, P = CH + 8;
     typedef typename Frag8<DT>::T F;
-    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5, R = e.rank, rr = (R + 15) & ~15;
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    constexpr int kAhead = 4;   // 16-rank steps of u loaded one block ahead
+    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5, R = add ? e.rank : 0, rr = (R + 15) & ~15;
+    const int cc = 8 * (lane & 7);
     uint16_t* vs = (uint16_t*)reg;
-    uint8_t* stage = SMALL ? reg : reg + 64 * P * 2 + kEpiMask;
+    float* s = (float*)(reg + 64 * kMaxRank * 2);
+    float* sl = s + kEpiRow / 4;
     const PhiloxKey key = philox_key(e.drop.rng);
-#pragma unroll 1
-    for (int g = lane; g < 32 * MT * 8; g += 64) {   // row g / 8, columns 8 (g % 8) .. + 7
-        const uint64_t at = (uint64_t)((m0 + (g >> 3)) * ncol + c0 + 8 * (g & 7));
-        mask[g] = (uint8_t)keep_bits8(philox7(key, at >> 3), e.drop.thr);
-    }
-    if (!SMALL) stage_v<false>(e, ncol, c0, 0, rr, P, vs);
+    auto urow = [&](int i) {
+        const int64_t r = m0 + 32 * i + q;
+        return e.u + (r < M ? r : M - 1) * R;
+    };
+    u32x4 un[kAhead];
+    auto ahead = [&](int i) {
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t)
+            if (16 * t < R) un[t] = load8(urow(i), 16 * t + 8 * h, R);
+    };
+    ahead(0);
+    stage_v<false>(e, ncol, c0, 0, rr, 0, vs);
     wave_sync();
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
+        const int64_t row = m0 + 32 * i + (lane >> 3);
+        float res[4][8];
+        if constexpr (!PART) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (row + 8 * p < M) load_residual<DT, OUT_F32, 8>(e, (row + 8 * p) * ncol + c0 + cc, res[p]);
+        }
+        wave_sync();
+        stage_block(s, acc[i]);
+        f32x16 lr[2];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) lr[0][r] = lr[1][r] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t)
+            if (16 * t < R) {
+                const F a = __builtin_bit_cast(F, un[t]);
+                lr[0] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 0, 16 * t), lr[0]);
+                lr[1] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 1, 16 * t), lr[1]);
+            }
+#pragma unroll 1
+        for (int k = 16 * kAhead; k < R; k += 16) {
+            const F a = __builtin_bit_cast(F, load8(urow(i), k + 8 * h, R));
+            lr[0] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 0, k), lr[0]);
+            lr[1] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 1, k), lr[1]);
+        }
+        if (i + 1 < MT) ahead(i + 1);
+        stage_block(sl, lr);
+        wave_sync();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            if (row + 8 * p >= M) continue;
+            const int64_t at = (row + 8 * p) * ncol + c0 + cc;
+            uint32_t bits = 0;
+            if (R) bits = keep_bits8(philox7(key, (uint64_t)at >> 3), e.drop.thr);
+            float z[8], l[8];
+            staged8(s, 8 * p + (lane >> 3), cc, z);
+            staged8(sl, 8 * p + (lane >> 3), cc, l);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) z[t] += (bits >> t & 1) ? l[t] * e.drop.keep : 0.0f;
+            if constexpr (PART) {
+                GLOBAL float* o = (GLOBAL float*)part + (row + 8 * p) * ldp + c0 + cc;
+                *(GLOBAL f4*)o = f4{z[0], z[1], z[2], z[3]};
+                *(GLOBAL f4*)(o + 4) = f4{z[4], z[5], z[6], z[7]};
+            } else {
+                const float none[8] = {};
+                finish<DT, false, OUT_F32, 8>(e, z, none, res[p], at, out);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);   // one 32-row block at a time
+    }
+}
+
+// The same in the 128 x 128 kernel's LDS: 16 ranks of v at a time, restaged for
+// each 32 rows (the staged output replaces them), the mask as bytes of groups.
+template <int DT, bool OUT_F32, bool PART>
+__device__ __forceinline__ void store_drop_small(const EpiArgs& e, void* out, float* part, int64_t ldp, int64_t M,
+                                                 int64_t ncol, int64_t m0, int64_t c0, uint8_t* reg, uint8_t* mask,
+                                                 const f32x16 (&acc)[kTM][2])
+{
+    typedef typename Frag8<DT>::T F;
+    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5, R = e.rank;
+    uint16_t* vs = (uint16_t*)reg;
+    const PhiloxKey key = philox_key(e.drop.rng);
+#pragma unroll 1
+    for (int g = lane; g < 32 * kTM * 8; g += 64) {   // row g / 8, columns 8 (g % 8) .. + 7
+        const uint64_t at = (uint64_t)((m0 + (g >> 3)) * ncol + c0 + 8 * (g & 7));
+        mask[g] = (uint8_t)keep_bits8(philox7(key, at >> 3), e.drop.thr);
+    }
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
         const int64_t urow = m0 + 32 * i + q;
         const uint16_t* up = e.u + (urow < M ? urow : M - 1) * R;
         f32x16 lr[1][2];
 #pragma unroll
         for (int r = 0; r < 16; ++r) lr[0][0][r] = lr[0][1][r] = 0.0f;
 #pragma unroll 1
-        for (int k = 0; k < rr; k += 16) {
-            const F a = __builtin_bit_cast(F, load8(up, 1, k + 8 * h, R));
-            if (SMALL) {
-                wave_sync();
-                stage_v<false>(e, ncol, c0, k, 16, P, vs);
-                wave_sync();
-            }
-            const uint16_t* vk = vs + (SMALL ? 0 : k) + 8 * h;
-            lr[0][0] = mfma32<DT>(a, *(const F*)(vk + q * P), lr[0][0]);
-            lr[0][1] = mfma32<DT>(a, *(const F*)(vk + (32 + q) * P), lr[0][1]);
+        for (int k = 0; k < R; k += 16) {
+            const F a = __builtin_bit_cast(F, load8(up, k + 8 * h, R));
+            wave_sync();
+            stage_v<false>(e, ncol, c0, k, 16, 0, vs);
+            wave_sync();
+            lr[0][0] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 0, 0), lr[0][0]);
+            lr[0][1] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 1, 0), lr[0][1]);
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
@@ -569,9 +739,8 @@ __device__ __forceinline__ void store_drop(const EpiArgs& e, void* out, float* p
                 }
             }
         } else {
-            store_epi<DT, false, OUT_F32, 1, 1>(e, out, M, ncol, m0 + 32 * i, c0, stage, lr);
+            store_epi<DT, false, OUT_F32, 1, 1>(e, out, M, ncol, m0 + 32 * i, c0, reg, lr);
         }
-        __builtin_amdgcn_sched_barrier(0);   // one 32-row block at a time
     }
 }
 
@@ -653,14 +822,16 @@ __global__ __launch_bounds__(kGThreads, 3) void k_nf4_matmul(GemmArgs g, E e)
         // mask bits in the level table
         uint8_t* reg = (uint8_t*)(wv < 2 ? s_a : s_w) + (wv & 1) * kEpiWaveSmall;
         const int64_t mw = m0 + kWM * wm, cw = c0 + kWN * wn;
-        if constexpr (!FWD) {
-            if (e.a.drop.thr && split == 0) {
-                store_drop<DT, OUT_F32, PART, kTM, true>(e.a, g.out, g.part, g.ldo, g.M, g.ncol, mw, cw, reg,
-                                                         (uint8_t*)s_lv + 512 * wv, acc);
+        if constexpr (E::kDrop) {
+            if (split == 0) {
+                store_drop_small<DT, OUT_F32, PART>(e.a, g.out, g.part, g.ldo, g.M, g.ncol, mw, cw, reg,
+                                                    (uint8_t*)s_lv + 512 * wv, acc);
                 return;
             }
         }
-        if (split == 0) add_lowrank<DT, FWD, kTM, kEpiRanksSmall>(e.a, g.M, g.ncol, mw, cw, reg, acc);
+        if constexpr (!E::kDrop) {
+            if (split == 0) add_lowrank<DT, FWD, kTM, kEpiRanksSmall>(e.a, g.M, g.ncol, mw, cw, reg, acc);
+        }
         if constexpr (!PART) {
             store_epi<DT, FWD, OUT_F32, kTM, 1>(e.a, g.out, g.M, g.ncol, mw, cw, reg, acc);
             return;
@@ -922,6 +1093,7 @@ __device__ __forceinline__ void mm_fwd_tile(const GemmArgs& g, const E& e, uint8
     }
 
     if constexpr (E::kOn) {
+        pin_acc(acc);
         uint8_t* reg = s_mem + wv * kEpiWave;   // past the last barrier
         if (split == 0) add_lowrank<DT, true, MT, kEpiRanks>(e.a, g.M, g.ncol, m0, wrow, reg, acc);
         if constexpr (!PART) {
@@ -1027,7 +1199,8 @@ __global__ __launch_bounds__(256, 1) void k_nf4_mm_fwd(GemmArgs g, E e)
     }
     const BigWork w = big_work<PART>(g);
     const int64_t m0 = w.mt * kXM, c0 = w.nt * kXN;
-    if (w.piece < 0) mm_fwd_tile<DT, DQ, OUT_F32, PART, 8>(g, e, s_mem, m0, c0, w.split, w.poff, w.ldp);
+    if constexpr (E::kOn) mm_fwd_tile<DT, DQ, OUT_F32, PART, 8>(g, e, s_mem, m0, c0, w.split, w.poff, w.ldp);
+    else if (w.piece < 0) mm_fwd_tile<DT, DQ, OUT_F32, PART, 8>(g, e, s_mem, m0, c0, w.split, w.poff, w.ldp);
     else if (g.pieces == 2)
         mm_fwd_tile<DT, DQ, OUT_F32, PART, 4>(g, e, s_mem, m0 + 128 * w.piece, c0, w.split, w.poff, w.ldp);
     else mm_fwd_tile<DT, DQ, OUT_F32, PART, 2>(g, e, s_mem, m0 + 64 * w.piece, c0, w.split, w.poff, w.ldp);
@@ -1258,13 +1431,15 @@ __device__ __forceinline__ void mm_bwd_tile(const GemmArgs& g, const E& e, uint8
     }
 
     if constexpr (E::kOn) {
+        pin_acc(acc);
         uint8_t* reg = s_mem + wv * kEpiWave;   // past the last barrier
-        if (e.a.drop.thr && split == 0) {
-            store_drop<DT, OUT_F32, PART, MT, false>(e.a, g.out, g.part + poff, ldp, g.M, g.ncol, m0, cw, reg,
-                                                     reg + 64 * (kMaxRank + 8) * 2, acc);
+        if constexpr (E::kDrop) {
+            store_drop<DT, OUT_F32, PART, MT>(e.a, g.out, g.part + poff, ldp, g.M, g.ncol, m0, cw, reg,
+                                              !PART || split == 0, acc);
             return;
+        } else {
+            if (split == 0) add_lowrank<DT, false, MT, kEpiRanks>(e.a, g.M, g.ncol, m0, cw, reg, acc);
         }
-        if (split == 0) add_lowrank<DT, false, MT, kEpiRanks>(e.a, g.M, g.ncol, m0, cw, reg, acc);
         if constexpr (!PART) {
             store_epi<DT, false, OUT_F32, MT, (MT < 4 ? MT : 4)>(e.a, g.out, g.M, g.ncol, m0, cw, reg, acc);
             return;
@@ -1309,7 +1484,8 @@ __global__ __launch_bounds__(256, 1) void k_nf4_mm_bwd(GemmArgs g, E e)
     // tiles fill one short round.
     const BigWork w = big_work<PART>(g);
     const int64_t m0 = w.mt * kXM, c0 = w.nt * kXN;
-    if (w.piece < 0) mm_bwd_tile<DT, DQ, OUT_F32, PART, 8>(g, e, s_mem, m0, c0, w.split, w.poff, w.ldp);
+    if constexpr (E::kOn) mm_bwd_tile<DT, DQ, OUT_F32, PART, 8>(g, e, s_mem, m0, c0, w.split, w.poff, w.ldp);
+    else if (w.piece < 0) mm_bwd_tile<DT, DQ, OUT_F32, PART, 8>(g, e, s_mem, m0, c0, w.split, w.poff, w.ldp);
     else if (g.pieces == 2)
         mm_bwd_tile<DT, DQ, OUT_F32, PART, 4>(g, e, s_mem, m0 + 128 * w.piece, c0, w.split, w.poff, w.ldp);
     else mm_bwd_tile<DT, DQ, OUT_F32, PART, 2>(g, e, s_mem, m0 + 64 * w.piece, c0, w.split, w.poff, w.ldp);
@@ -1440,11 +1616,11 @@ __global__ __launch_bounds__(256, 4) void k_nf4_gemv16(GemvArgs g, E e)
         // the low-rank term: 32 ranks a step, lane l's at 8 (l / 16)
         if (e.a.u && part == 0) {
             for (int k = 0; k < e.a.rank; k += 32) {
-                const u32x4 v = load8(e.a.v + n * e.a.rank, 1, k + 8 * kg, e.a.rank);
+                const u32x4 v = load8(e.a.v + n * e.a.rank, k + 8 * kg, e.a.rank);
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb) {
                     const int64_t row = 16 * mb + xr;
-                    const u32x4 u = load8(e.a.u + (row < g.m ? row : g.m - 1) * e.a.rank, 1, k + 8 * kg, e.a.rank);
+                    const u32x4 u = load8(e.a.u + (row < g.m ? row : g.m - 1) * e.a.rank, k + 8 * kg, e.a.rank);
                     acc[mb] = mfma16<DT>(__builtin_bit_cast(F, u), __builtin_bit_cast(F, v), acc[mb]);
                 }
             }
@@ -1478,7 +1654,9 @@ __global__ __launch_bounds__(256) void k_splitk_sum(const float* __restrict__ pa
         const uint32_t i4 = (uint32_t)(i >> 2);
         float z[4] = {acc.x, acc.y, acc.z, acc.w}, bias[4];
         load_bias<DT, 4>(e.a, (int64_t)(i4 % (uint32_t)(ncol >> 2)) * 4, bias);
-        finish<DT, true, OUT_F32, 4>(e.a, z, bias, i, out);
+        float res[4];
+        load_residual<DT, OUT_F32, 4>(e.a, i, res);
+        finish<DT, true, OUT_F32, 4>(e.a, z, bias, res, i, out);
     } else if constexpr (OUT_F32) {
         *(GLOBAL f4*)((float*)out + i) = acc;
     } else {
@@ -1508,7 +1686,9 @@ __global__ __launch_bounds__(256) void k_tail_sum(GemmArgs g, E ep)
     if constexpr (E::kOn) {
         float z[4] = {acc.x, acc.y, acc.z, acc.w}, bias[4];
         load_bias<DT, 4>(ep.a, col, bias);
-        finish<DT, true, OUT_F32, 4>(ep.a, z, bias, i, g.out);
+        float res[4];
+        load_residual<DT, OUT_F32, 4>(ep.a, i, res);
+        finish<DT, true, OUT_F32, 4>(ep.a, z, bias, res, i, g.out);
     } else if constexpr (OUT_F32) {
         *(GLOBAL f4*)((float*)g.out + i) = acc;
     } else {
@@ -1680,7 +1860,7 @@ hipError_t mm_fwd_go(GemmArgs g, const E& ep, hipStream_t s)
     g.nhalf = 0;
     g.pieces = 2;
     int64_t full = 0, rem = 0;
-    const int pieces = g.nsplit == 1 ? tail_pieces(total, cu_count(), full, rem) : 0;
+    const int pieces = !E::kOn && g.nsplit == 1 ? tail_pieces(total, cu_count(), full, rem) : 0;
     if (pieces > 0 && full + pieces * rem < kMaxGemmGrid) {
         g.nfull = full;
         g.nhalf = rem;
@@ -1740,7 +1920,7 @@ hipError_t mm_bwd_go(GemmArgs g, const E& ep, hipStream_t s)
         return hipGetLastError();
     }
     int64_t full = 0, rem = 0;
-    const int pieces = tail_pieces(g.ntiles, cu_count(), full, rem);
+    const int pieces = E::kOn ? 0 : tail_pieces(g.ntiles, cu_count(), full, rem);
     if (pieces > 0) {
         g.nfull = full;
         g.nhalf = rem;
@@ -1878,18 +2058,18 @@ inline GemmArgs gemm_args(const uint8_t* codes, const int8_t* qabsmax, const flo
 template <class E>
 hipError_t gemm_any(int dtype, bool forward, bool dq, bool out_f32, const GemmArgs& g, const E& ep, hipStream_t s)
 {
-#define NF4_GEMM(T, F, D, O) return gemm_go<T, F, D, O, E>(g, ep, s)
-#define NF4_GEMM_DT(T)                                                                             \
-    if (forward) {                                                                               \
-        if (dq) { if (out_f32) NF4_GEMM(T, true, true, true); else NF4_GEMM(T, true, true, false); }     \
-        else    { if (out_f32) NF4_GEMM(T, true, false, true); else NF4_GEMM(T, true, false, false); }   \
-    } else {                                                                                     \
-        if (dq) { if (out_f32) NF4_GEMM(T, false, true, true); else NF4_GEMM(T, false, true, false); }   \
-        else    { if (out_f32) NF4_GEMM(T, false, false, true); else NF4_GEMM(T, false, false, false); } \
+#define NF4_GEMM(T, F)                                                                                        \
+    if (dq) return out_f32 ? gemm_go<T, F, true, true, E>(g, ep, s) : gemm_go<T, F, true, false, E>(g, ep, s); \
+    return out_f32 ? gemm_go<T, F, false, true, E>(g, ep, s) : gemm_go<T, F, false, false, E>(g, ep, s)
+    if (forward) {
+        if constexpr (E::kDrop) return hipErrorInvalidValue;   // backward only
+        else {
+            if (dtype == 0) { NF4_GEMM(0, true); }
+            NF4_GEMM(1, true);
+        }
     }
-    if (dtype == 0) { NF4_GEMM_DT(0) }
-    NF4_GEMM_DT(1)
-#undef NF4_GEMM_DT
+    if (dtype == 0) { NF4_GEMM(0, false); }
+    NF4_GEMM(1, false);
 #undef NF4_GEMM
 }
 
