@@ -297,17 +297,18 @@ __device__ __forceinline__ void group_coords(int64_t tile, int64_t mtiles, int64
 // What the call adds to the product before its one rounding:
 //   forward   z = x W^T + u v^T + bias, preact = z, out = act(z) + residual
 //   backward  out = dy W + drop(u v) + residual
-// The low-rank product is a few more MFMA steps (rank padded with zeros), from
-// u and v staged in LDS by each wave for its own rows and columns: on the same
+// The low-rank product is a few more MFMA steps (rank padded with zeros), each
+// wave for its own rows and columns, v through its LDS: on the same
 // accumulators, or under dropout on accumulators of their own, 32 rows at a
 // time, whose kept values are added where the sums are stored.  The mask comes
 // from one generator call per group of eight elements, where a lane holds eight
 // consecutive columns of a row: after the accumulators (one column per lane)
-// have gone through LDS, or (128 x 128 kernel) kept there as one byte a group.  With a split reduction the first split
-// adds the low-rank term.  The rest is applied where the final value is stored:
-// from the accumulators through LDS, so that a lane handles eight consecutive
-// columns and every access is 16 bytes, or in the kernel that adds the splits.
-// All of it is private to a wave: no barrier.
+// have gone through LDS, or (128 x 128 kernel) kept there as one byte a group.
+// With a split reduction the splits share the row blocks of the low-rank term.
+// The rest is applied where the final value is stored: from the accumulators
+// through LDS, so that a lane handles eight consecutive columns and every access
+// is 16 bytes, or in the kernel that adds the splits.  All of it is private to a
+// wave: no barrier.
 struct NoEpi {
     static constexpr bool kOn = false, kDrop = false;
 };
@@ -323,12 +324,11 @@ struct WithDrop {   // backward, the low-rank term under dropout
 constexpr int kEpiPitch = 68;                              // fp32 values per staged output row
 constexpr int kEpiWave = 128 * kEpiPitch * 4;              // bytes per wave, 256 x 256 kernels: 128 rows
 constexpr int kEpiWaveSmall = (kBM + kBN) * kLdp * 2 / 4;  // 128 x 128 kernel: 9,216
-constexpr int kEpiRanks = 32, kEpiRanksSmall = 16;         // ranks of u and v staged at a time
+constexpr int kEpiRanks = 64;                              // ranks of v staged at a time
 constexpr int kMaxRank = 128;                              // under dropout, all of v (256 x 256)
 constexpr int kEpiRow = 32 * kEpiPitch * 4;                // staged output of 32 rows
-static_assert((64 + 256) * (kEpiRanks + 8) * 2 <= kEpiWave, "staged v and u");
 static_assert(64 * kMaxRank * 2 + 2 * kEpiRow <= kEpiWave, "staged v, products and low-rank terms");
-static_assert((64 + kWM) * (kEpiRanksSmall + 8) * 2 <= kEpiWaveSmall && kEpiRow <= kEpiWaveSmall, "128 x 128 kernel");
+static_assert(64 * (kEpiRanks + 8) * 2 <= kEpiWaveSmall && kEpiRow <= kEpiWaveSmall, "128 x 128 kernel");
 
 // Keeps the accumulators in accumulation registers up to here: without it the
 // epilogue's other uses of them drew some of them into vector registers, and the
@@ -340,6 +340,15 @@ __device__ __forceinline__ void pin_acc(f32x16 (&acc)[MT][2])
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) __asm__ volatile("" : "+a"(acc[i][j]));
+}
+
+// A uniform value as the epilogue's own, in scalar registers: its many vector uses
+// there must not pull the main loop's load bases into vector registers (each load
+// would then become a loop over the distinct bases).
+__device__ __forceinline__ int64_t scalar_copy(int64_t x)
+{
+    __asm__ volatile("" : "+s"(x));
+    return x;
 }
 
 // Orders a wave's LDS writes before its own lanes' later reads (and the
@@ -364,13 +373,14 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* row, int k, int R)
     return d;
 }
 
-// The wave's 64 columns of v, ranks k0 .. k0 + n - 1 (n a multiple of 16; zero
-// from the rank on), to LDS: forward [64][pitch], the rank contiguous as in
+// The wave's 64 columns of v, ranks k0 .. k0 + n - 1 (n a multiple of 16, cut to
+// the rank rounded up to 16; zero from the rank on), to LDS: forward [64][pitch], the rank contiguous as in
 // memory; backward [n][64], read back transposed.
 template <bool FWD>
 __device__ __forceinline__ void stage_v(const EpiArgs& e, int64_t ncol, int64_t c0, int k0, int n, int pitch, uint16_t* vs)
 {
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, left = (e.rank - k0 + 15) & ~15;
+    if (n > left) n = left;
     if constexpr (FWD) {
         const uint16_t* src = e.v + (c0 + lane) * e.rank;
 #pragma unroll 2
@@ -407,42 +417,48 @@ __device__ __forceinline__ typename Frag8<DT>::T frag_v(const uint16_t* vs, int 
     }
 }
 
+// Which 32-row blocks of a tile a split of the reduction adds the low-rank term
+// to: block i is split i % of's (every block with one split), so that no split
+// runs much longer than the others (all of it on the first split cost 6 to 17 us
+// of a 55 us call).
+struct Share {
+    int split, of;
+    __device__ __forceinline__ bool has(int i) const { return of <= 1 || i % of == split; }
+};
+
 // acc += the low-rank term of rows m0 .. m0 + 32 MT - 1, columns c0 .. c0 + 63
-// (accumulator layout of the 32 x 32 MFMA), CH ranks at a time.
+// (accumulator layout of the 32 x 32 MFMA), CH ranks at a time: v of the wave's
+// columns through LDS, u straight to fragments.
 template <int DT, bool FWD, int MT, int CH>
 __device__ __forceinline__ void add_lowrank(const EpiArgs& e, int64_t M, int64_t ncol, int64_t m0, int64_t c0,
-                                            uint8_t* reg, f32x16 (&acc)[MT][2])
+                                            uint8_t* reg, Share share, f32x16 (&acc)[MT][2])
 {
     if (!e.u) return;
-    constexpr int P = CH + 8, G = CH / 8;   // pitch, groups of eight ranks per row
+    constexpr int P = CH + 8;   // pitch of v forward
     typedef typename Frag8<DT>::T F;
     const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5, R = e.rank;
     uint16_t* vs = (uint16_t*)reg;
-    uint16_t* us = vs + 64 * P;
 #pragma unroll 1
     for (int k0 = 0; k0 < R; k0 += CH) {
         wave_sync();
         stage_v<FWD>(e, ncol, c0, k0, CH, P, vs);
-#pragma unroll 4
-        for (int t = lane; t < 32 * MT * G; t += 64) {
-            const int64_t row = m0 + t / G;
-            *(u32x4*)(us + (t / G) * P + 8 * (t % G)) =
-                load8(e.u + (row < M ? row : M - 1) * R, k0 + 8 * (t % G), R);
-        }
         wave_sync();
-        F b[CH / 16][2];
+#pragma unroll 1
+        for (int k = k0; k < k0 + CH && k < R; k += 16) {
+            u32x4 a[MT];
 #pragma unroll
-        for (int s = 0; s < CH / 16; ++s)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) b[s][j] = frag_v<DT, FWD>(vs, P, j, 16 * s);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int s = 0; s < CH / 16; ++s) {
-                const F a = *(const F*)(us + (32 * i + q) * P + 16 * s + 8 * h);
-                acc[i][0] = mfma32<DT>(a, b[s][0], acc[i][0]);
-                acc[i][1] = mfma32<DT>(a, b[s][1], acc[i][1]);
+            for (int i = 0; i < MT; ++i) {
+                const int64_t row = m0 + 32 * i + q;
+                if (share.has(i)) a[i] = load8(e.u + (row < M ? row : M - 1) * R, k + 8 * h, R);
             }
+            const F b0 = frag_v<DT, FWD>(vs, P, 0, k - k0), b1 = frag_v<DT, FWD>(vs, P, 1, k - k0);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                if (share.has(i)) {
+                    acc[i][0] = mfma32<DT>(__builtin_bit_cast(F, a[i]), b0, acc[i][0]);
+                    acc[i][1] = mfma32<DT>(__builtin_bit_cast(F, a[i]), b1, acc[i][1]);
+                }
+        }
     }
 }
 
@@ -605,41 +621,57 @@ __device__ __forceinline__ void store_epi(const EpiArgs& e, void* out, int64_t M
     }
 }
 
+// A 32-row accumulator block as it lies (one column per lane) to the fp32 partial.
+__device__ __forceinline__ void store_part(float* part, int64_t ldp, int64_t M, int64_t m0, int64_t c0, const f32x16 (&a)[2])
+{
+    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int64_t row = m0 + 8 * (r >> 2) + 4 * h + (r & 3);
+        if (row < M) {
+            ((GLOBAL float*)part)[row * ldp + c0 + q] = a[0][r];
+            ((GLOBAL float*)part)[row * ldp + c0 + 32 + q] = a[1][r];
+        }
+    }
+}
+
 // The 256 x 256 kernel's backward store under dropout: acc + keep . (u v) /
 // (1 - p), 32 rows at a time, as the final value (out) or as the split's fp32
-// partial (element (row, col) at part[row * ldp + col]; without `add` as for
-// rank 0).
+// partial (element (row, col) at part[row * ldp + col]).
 // Both terms go through LDS.
-template <int DT, bool OUT_F32, bool PART, int MT>
-__device__ __forceinline__ void store_drop(const EpiArgs& e, void* out, float* part, int64_t ldp, int64_t M,
-                                           int64_t ncol, int64_t m0, int64_t c0, uint8_t* reg, bool add,
-                                           const f32x16 (&acc)[MT][2])
+constexpr int kDropAhead = 4;   // 16-rank steps of u loaded one block ahead
+
+template <int DT>
+__device__ __forceinline__ void load_u(const EpiArgs& e, int64_t M, int64_t m0, u32x4 (&u)[kDropAhead])
+{
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int64_t r = m0 + (lane & 31);
+    const uint16_t* row = e.u + (r < M ? r : M - 1) * e.rank;
+#pragma unroll
+    for (int t = 0; t < kDropAhead; ++t)
+        if (16 * t < e.rank) u[t] = load8(row, 16 * t + 8 * h, e.rank);
+}
+
+// Block I of store_drop, and the next ones: constant indices by recursion (the
+// accumulators must not be indexed at run time, and the body is too long for the
+// unroller).  u holds the block's rows.
+template <int DT, bool OUT_F32, bool PART, int MT, int I>
+__device__ __forceinline__ void store_drop_from(const EpiArgs& e, void* out, float* part, int64_t ldp, int64_t M,
+                                                int64_t ncol, int64_t m0, int64_t c0, uint8_t* reg, PhiloxKey key,
+                                                Share share, u32x4 (&u)[kDropAhead], const f32x16 (&acc)[MT][2])
 {
     typedef typename Frag8<DT>::T F;
     typedef float f4 __attribute__((ext_vector_type(4)));
-    constexpr int kAhead = 4;   // 16-rank steps of u loaded one block ahead
-    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5, R = add ? e.rank : 0, rr = (R + 15) & ~15;
-    const int cc = 8 * (lane & 7);
-    uint16_t* vs = (uint16_t*)reg;
+    const int lane = threadIdx.x & 63, h = lane >> 5, rank = e.rank, cc = 8 * (lane & 7);
+    const int64_t row = m0 + 32 * I + (lane >> 3);
+    const uint16_t* vs = (const uint16_t*)reg;
     float* s = (float*)(reg + 64 * kMaxRank * 2);
     float* sl = s + kEpiRow / 4;
-    const PhiloxKey key = philox_key(e.drop.rng);
-    auto urow = [&](int i) {
-        const int64_t r = m0 + 32 * i + q;
-        return e.u + (r < M ? r : M - 1) * R;
-    };
-    u32x4 un[kAhead];
-    auto ahead = [&](int i) {
-#pragma unroll
-        for (int t = 0; t < kAhead; ++t)
-            if (16 * t < R) un[t] = load8(urow(i), 16 * t + 8 * h, R);
-    };
-    ahead(0);
-    stage_v<false>(e, ncol, c0, 0, rr, 0, vs);
-    wave_sync();
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t row = m0 + 32 * i + (lane >> 3);
+    const bool next = I + 1 < MT && share.has(I + 1);
+    if (PART && !share.has(I)) {   // another split's block
+        store_part(part, ldp, M, m0 + 32 * I, c0, acc[I]);
+        if (next) load_u<DT>(e, M, m0 + 32 * (I + 1), u);
+    } else {
         float res[4][8];
         if constexpr (!PART) {
 #pragma unroll
@@ -647,100 +679,117 @@ __device__ __forceinline__ void store_drop(const EpiArgs& e, void* out, float* p
                 if (row + 8 * p < M) load_residual<DT, OUT_F32, 8>(e, (row + 8 * p) * ncol + c0 + cc, res[p]);
         }
         wave_sync();
-        stage_block(s, acc[i]);
+        stage_block(s, acc[I]);
         f32x16 lr[2];
 #pragma unroll
         for (int r = 0; r < 16; ++r) lr[0][r] = lr[1][r] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < kAhead; ++t)
-            if (16 * t < R) {
-                const F a = __builtin_bit_cast(F, un[t]);
+        for (int t = 0; t < kDropAhead; ++t)
+            if (16 * t < rank) {
+                const F a = __builtin_bit_cast(F, u[t]);
                 lr[0] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 0, 16 * t), lr[0]);
                 lr[1] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 1, 16 * t), lr[1]);
             }
+        const int64_t ur = m0 + 32 * I + (lane & 31);
 #pragma unroll 1
-        for (int k = 16 * kAhead; k < R; k += 16) {
-            const F a = __builtin_bit_cast(F, load8(urow(i), k + 8 * h, R));
+        for (int k = 16 * kDropAhead; k < rank; k += 16) {
+            const F a = __builtin_bit_cast(F, load8(e.u + (ur < M ? ur : M - 1) * rank, k + 8 * h, rank));
             lr[0] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 0, k), lr[0]);
             lr[1] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 1, k), lr[1]);
         }
-        if (i + 1 < MT) ahead(i + 1);
+        if (next) load_u<DT>(e, M, m0 + 32 * (I + 1), u);
         stage_block(sl, lr);
         wave_sync();
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            if (row + 8 * p >= M) continue;
-            const int64_t at = (row + 8 * p) * ncol + c0 + cc;
-            uint32_t bits = 0;
-            if (R) bits = keep_bits8(philox7(key, (uint64_t)at >> 3), e.drop.thr);
-            float z[8], l[8];
-            staged8(s, 8 * p + (lane >> 3), cc, z);
-            staged8(sl, 8 * p + (lane >> 3), cc, l);
+            if (row + 8 * p < M) {
+                const int64_t at = (row + 8 * p) * ncol + c0 + cc;
+                const uint32_t bits = keep_bits8(philox7(key, (uint64_t)at >> 3), e.drop.thr);
+                float z[8], l[8];
+                staged8(s, 8 * p + (lane >> 3), cc, z);
+                staged8(sl, 8 * p + (lane >> 3), cc, l);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) z[t] += (bits >> t & 1) ? l[t] * e.drop.keep : 0.0f;
-            if constexpr (PART) {
-                GLOBAL float* o = (GLOBAL float*)part + (row + 8 * p) * ldp + c0 + cc;
-                *(GLOBAL f4*)o = f4{z[0], z[1], z[2], z[3]};
-                *(GLOBAL f4*)(o + 4) = f4{z[4], z[5], z[6], z[7]};
-            } else {
-                const float none[8] = {};
-                finish<DT, false, OUT_F32, 8>(e, z, none, res[p], at, out);
+                for (int t = 0; t < 8; ++t) z[t] += (bits >> t & 1) ? l[t] * e.drop.keep : 0.0f;
+                if constexpr (PART) {
+                    GLOBAL float* o = (GLOBAL float*)part + (row + 8 * p) * ldp + c0 + cc;
+                    *(GLOBAL f4*)o = f4{z[0], z[1], z[2], z[3]};
+                    *(GLOBAL f4*)(o + 4) = f4{z[4], z[5], z[6], z[7]};
+                } else {
+                    const float none[8] = {};
+                    finish<DT, false, OUT_F32, 8>(e, z, none, res[p], at, out);
+                }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);   // one 32-row block at a time
     }
+    __builtin_amdgcn_sched_barrier(0);   // one 32-row block at a time
+    if constexpr (I + 1 < MT)
+        store_drop_from<DT, OUT_F32, PART, MT, I + 1>(e, out, part, ldp, M, ncol, m0, c0, reg, key, share, u, acc);
 }
 
-// The same in the 128 x 128 kernel's LDS: 16 ranks of v at a time, restaged for
+template <int DT, bool OUT_F32, bool PART, int MT>
+__device__ __forceinline__ void store_drop(const EpiArgs& e, void* out, float* part, int64_t ldp, int64_t M,
+                                           int64_t ncol, int64_t m0, int64_t c0, uint8_t* reg, Share share,
+                                           const f32x16 (&acc)[MT][2])
+{
+    u32x4 u[kDropAhead];
+    if (share.has(0)) load_u<DT>(e, M, m0, u);
+    stage_v<false>(e, ncol, c0, 0, kMaxRank, 0, (uint16_t*)reg);
+    wave_sync();
+    store_drop_from<DT, OUT_F32, PART, MT, 0>(e, out, part, ldp, M, ncol, m0, c0, reg, philox_key(e.drop.rng), share, u,
+                                              acc);
+}
+
+// The same in the 128 x 128 kernel's LDS: 64 ranks of v at a time, restaged for
 // each 32 rows (the staged output replaces them), the mask as bytes of groups.
 template <int DT, bool OUT_F32, bool PART>
 __device__ __forceinline__ void store_drop_small(const EpiArgs& e, void* out, float* part, int64_t ldp, int64_t M,
-                                                 int64_t ncol, int64_t m0, int64_t c0, uint8_t* reg, uint8_t* mask,
+                                                 int64_t ncol, int64_t m0, int64_t c0, uint8_t* reg, uint8_t* mask, Share share,
                                                  const f32x16 (&acc)[kTM][2])
 {
     typedef typename Frag8<DT>::T F;
-    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5, R = e.rank;
+    const int lane = threadIdx.x & 63, q = lane & 31, h = lane >> 5, rank = e.rank;
     uint16_t* vs = (uint16_t*)reg;
     const PhiloxKey key = philox_key(e.drop.rng);
-#pragma unroll 1
-    for (int g = lane; g < 32 * kTM * 8; g += 64) {   // row g / 8, columns 8 (g % 8) .. + 7
-        const uint64_t at = (uint64_t)((m0 + (g >> 3)) * ncol + c0 + 8 * (g & 7));
-        mask[g] = (uint8_t)keep_bits8(philox7(key, at >> 3), e.drop.thr);
-    }
-#pragma unroll
-    for (int i = 0; i < kTM; ++i) {
+    auto block = [&](int i) {
         const int64_t urow = m0 + 32 * i + q;
-        const uint16_t* up = e.u + (urow < M ? urow : M - 1) * R;
+        wave_sync();
+#pragma unroll
+        for (int g = lane; g < 32 * 8; g += 64) {   // row g / 8, columns 8 (g % 8) .. + 7
+            const uint64_t at = (uint64_t)((m0 + 32 * i + (g >> 3)) * ncol + c0 + 8 * (g & 7));
+            mask[g] = (uint8_t)keep_bits8(philox7(key, at >> 3), e.drop.thr);
+        }
+        const uint16_t* up = e.u + (urow < M ? urow : M - 1) * rank;
         f32x16 lr[1][2];
 #pragma unroll
         for (int r = 0; r < 16; ++r) lr[0][0][r] = lr[0][1][r] = 0.0f;
 #pragma unroll 1
-        for (int k = 0; k < R; k += 16) {
-            const F a = __builtin_bit_cast(F, load8(up, k + 8 * h, R));
+        for (int k0 = 0; k0 < rank; k0 += kEpiRanks) {
             wave_sync();
-            stage_v<false>(e, ncol, c0, k, 16, 0, vs);
+            stage_v<false>(e, ncol, c0, k0, kEpiRanks, 0, vs);
             wave_sync();
-            lr[0][0] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 0, 0), lr[0][0]);
-            lr[0][1] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 1, 0), lr[0][1]);
+#pragma unroll 1
+            for (int k = k0; k < k0 + kEpiRanks && k < rank; k += 16) {
+                const F a = __builtin_bit_cast(F, load8(up, k + 8 * h, rank));
+                lr[0][0] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 0, k - k0), lr[0][0]);
+                lr[0][1] = mfma32<DT>(a, frag_v<DT, false>(vs, 0, 1, k - k0), lr[0][1]);
+            }
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const u32x2 w = *(const u32x2*)(mask + 8 * (32 * i + 8 * (r >> 2) + 4 * h + (r & 3)));
+            const u32x2 w = *(const u32x2*)(mask + 8 * (8 * (r >> 2) + 4 * h + (r & 3)));
             lr[0][0][r] = acc[i][0][r] + ((w.x >> q & 1) ? lr[0][0][r] * e.drop.keep : 0.0f);
             lr[0][1][r] = acc[i][1][r] + ((w.y >> q & 1) ? lr[0][1][r] * e.drop.keep : 0.0f);
         }
         if constexpr (PART) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t row = m0 + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (row < M) {
-                    ((GLOBAL float*)part)[row * ldp + c0 + q] = lr[0][0][r];
-                    ((GLOBAL float*)part)[row * ldp + c0 + 32 + q] = lr[0][1][r];
-                }
-            }
+            store_part(part, ldp, M, m0 + 32 * i, c0, lr[0]);
         } else {
             store_epi<DT, false, OUT_F32, 1, 1>(e, out, M, ncol, m0 + 32 * i, c0, reg, lr);
         }
+    };
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+        if (!PART || share.has(i)) block(i);
+        else store_part(part, ldp, M, m0 + 32 * i, c0, acc[i]);   // another split's block
     }
 }
 
@@ -822,15 +871,14 @@ __global__ __launch_bounds__(kGThreads, 3) void k_nf4_matmul(GemmArgs g, E e)
         // mask bits in the level table
         uint8_t* reg = (uint8_t*)(wv < 2 ? s_a : s_w) + (wv & 1) * kEpiWaveSmall;
         const int64_t mw = m0 + kWM * wm, cw = c0 + kWN * wn;
+        const Share share = {split, PART ? g.nsplit : 1};
         if constexpr (E::kDrop) {
-            if (split == 0) {
-                store_drop_small<DT, OUT_F32, PART>(e.a, g.out, g.part, g.ldo, g.M, g.ncol, mw, cw, reg,
-                                                    (uint8_t*)s_lv + 512 * wv, acc);
-                return;
-            }
+            store_drop_small<DT, OUT_F32, PART>(e.a, g.out, g.part + (PART ? (int64_t)split * g.M * g.ldo : 0), g.ldo, g.M,
+                                                g.ncol, mw, cw, reg, (uint8_t*)s_lv + 512 * wv, share, acc);
+            return;
         }
         if constexpr (!E::kDrop) {
-            if (split == 0) add_lowrank<DT, FWD, kTM, kEpiRanksSmall>(e.a, g.M, g.ncol, mw, cw, reg, acc);
+            add_lowrank<DT, FWD, kTM, kEpiRanks>(e.a, g.M, g.ncol, mw, cw, reg, share, acc);
         }
         if constexpr (!PART) {
             store_epi<DT, FWD, OUT_F32, kTM, 1>(e.a, g.out, g.M, g.ncol, mw, cw, reg, acc);
@@ -1094,10 +1142,12 @@ __device__ __forceinline__ void mm_fwd_tile(const GemmArgs& g, const E& e, uint8
 
     if constexpr (E::kOn) {
         pin_acc(acc);
+        const int64_t me = scalar_copy(m0), ce = scalar_copy(wrow);
         uint8_t* reg = s_mem + wv * kEpiWave;   // past the last barrier
-        if (split == 0) add_lowrank<DT, true, MT, kEpiRanks>(e.a, g.M, g.ncol, m0, wrow, reg, acc);
+        const Share share = {split, !PART ? 1 : g.tail_split > 0 ? g.tail_split : g.nsplit};
+        add_lowrank<DT, true, MT, kEpiRanks>(e.a, g.M, g.ncol, me, ce, reg, share, acc);
         if constexpr (!PART) {
-            store_epi<DT, true, OUT_F32, MT, (MT < 4 ? MT : 4)>(e.a, g.out, g.M, g.ncol, m0, wrow, reg, acc);
+            store_epi<DT, true, OUT_F32, MT, (MT < 4 ? MT : 4)>(e.a, g.out, g.M, g.ncol, me, ce, reg, acc);
             return;
         }
     }
@@ -1432,16 +1482,18 @@ __device__ __forceinline__ void mm_bwd_tile(const GemmArgs& g, const E& e, uint8
 
     if constexpr (E::kOn) {
         pin_acc(acc);
+        const int64_t me = scalar_copy(m0), ce = scalar_copy(cw);
         uint8_t* reg = s_mem + wv * kEpiWave;   // past the last barrier
+        const Share share = {split, !PART ? 1 : g.tail_split > 0 ? g.tail_split : g.nsplit};
         if constexpr (E::kDrop) {
-            store_drop<DT, OUT_F32, PART, MT>(e.a, g.out, g.part + poff, ldp, g.M, g.ncol, m0, cw, reg,
-                                              !PART || split == 0, acc);
+            store_drop<DT, OUT_F32, PART, MT>(e.a, g.out, g.part + scalar_copy(poff), scalar_copy(ldp), g.M, g.ncol,
+                                              me, ce, reg, share, acc);
             return;
         } else {
-            if (split == 0) add_lowrank<DT, false, MT, kEpiRanks>(e.a, g.M, g.ncol, m0, cw, reg, acc);
+            add_lowrank<DT, false, MT, kEpiRanks>(e.a, g.M, g.ncol, me, ce, reg, share, acc);
         }
         if constexpr (!PART) {
-            store_epi<DT, false, OUT_F32, MT, (MT < 4 ? MT : 4)>(e.a, g.out, g.M, g.ncol, m0, cw, reg, acc);
+            store_epi<DT, false, OUT_F32, MT, (MT < 4 ? MT : 4)>(e.a, g.out, g.M, g.ncol, me, ce, reg, acc);
             return;
         }
     }
