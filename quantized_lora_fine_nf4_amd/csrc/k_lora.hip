@@ -548,6 +548,8 @@ __global__ __launch_bounds__(64 * kGradWaves<RT>) void k_lora_grad(GradArgs g)
                 const Bits128 bits = philox7(key, (uint64_t)(row * g.n + nc) >> 3);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[i][j] = keep2(x[i][j], bits.w[j], g.drop.thr);
+                // two generator calls at a time: more of them interleaved spill beside 64 ranks of sums
+                if (RT == 4 && (i & 1)) __builtin_amdgcn_sched_barrier(0);
             }
             if (row >= s1) x[i] = u32x4{0, 0, 0, 0};
         }

@@ -383,8 +383,15 @@ __device__ __forceinline__ void stage_v(const EpiArgs& e, int64_t ncol, int64_t 
     if (n > left) n = left;
     if constexpr (FWD) {
         const uint16_t* src = e.v + (c0 + lane) * e.rank;
-#pragma unroll 2
-        for (int g = 0; g < n; g += 8) *(u32x4*)(vs + lane * pitch + g) = load8(src, k0 + g, e.rank);
+#pragma unroll 1
+        for (int g = 0; g < n; g += 32) {   // four loads in flight
+            u32x4 d[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) d[t] = load8(src, k0 + g + 8 * t, e.rank);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (g + 8 * t < n) *(u32x4*)(vs + lane * pitch + g + 8 * t) = d[t];
+        }
     } else {
         const int cg = lane & 7;
 #pragma unroll 4
