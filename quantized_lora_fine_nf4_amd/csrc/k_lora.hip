@@ -214,8 +214,8 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float* part, int nparts
 //
 // The reduction index of a [k x rank] matrix is its slow index, while an MFMA
 // fragment wants eight consecutive k of one rank.  With the rank a multiple of
-// 8 a wave copies a 32 x 16 RT tile to LDS (16 bytes a lane, rank contiguous)
-// and reads it back with the transposing 64-bit read: in each group of 16
+// V = 8 or 4 a wave copies a 32 x 16 RT tile to LDS (16 or 8 bytes a piece, rank
+// contiguous) and reads it back with the transposing 64-bit read: in each group of 16
 // lanes, lane i receives element i % 4 of the pieces read by lanes 4 j + i / 4,
 // so lanes reading rows r .. r + 3 at columns C + 4 (i % 4) get column C + i of
 // those rows.  Otherwise each lane gathers its eight values from memory.
@@ -237,29 +237,44 @@ __device__ __forceinline__ u32x4 ld16(const uint16_t* base, uint32_t off)
 }
 
 // Rows k0 .. k0 + 31 (past `rows` the last row again), ranks r0 .. r0 + 16 RT
-// - 1 of p [rows x rank], rank a multiple of 8: 16-byte piece t * 64 + lane.
-template <int RT>
+// - 1 of p [rows x rank], rank a multiple of V: piece t * 64 + lane of V values.
+template <int RT, int V>
 __device__ __forceinline__ void load_tile(const uint16_t* p, int64_t rows, int rank, int64_t k0, int r0, u32x4 (&d)[RT])
 {
+    constexpr int kRow = 16 * RT / V;   // pieces per row
     const int lane = threadIdx.x & 63;
     const uint16_t* base = p + k0 * rank;
     const int left = k0 + 32 <= rows ? 31 : (int)(rows - 1 - k0);
+    auto off = [&](int t) {
+        const int item = t * 64 + lane, r = r0 + V * (item % kRow), k = item / kRow;
+        return (uint32_t)((k < left ? k : left) * rank + (r < rank ? r : rank - V)) * 2;
+    };
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        const int item = t * 64 + lane, r = r0 + 8 * (item % (2 * RT)), k = item / (2 * RT);
-        d[t] = ld16(base, (uint32_t)((k < left ? k : left) * rank + (r < rank ? r : rank - 8)) * 2);
+        if constexpr (V == 8) d[t] = ld16(base, off(t));
+        else {
+            const u32x2 a = *(const GLOBAL u32x2*)((const GLOBAL uint8_t*)base + off(2 * t));
+            const u32x2 b = *(const GLOBAL u32x2*)((const GLOBAL uint8_t*)base + off(2 * t + 1));
+            d[t] = u32x4{a.x, a.y, b.x, b.y};
+        }
     }
 }
 
 // Through LDS (32 x 16 RT values of the wave's own) to the fragments of the RT
 // rank tiles.
-template <int RT>
+template <int RT, int V>
 __device__ __forceinline__ void transpose_tile(const u32x4 (&d)[RT], uint16_t* lds, u32x4 (&f)[RT])
 {
     const int lane = threadIdx.x & 63, q = lane & 15, kg = lane >> 4;
     wave_sync();
 #pragma unroll
-    for (int t = 0; t < RT; ++t) *(u32x4*)(lds + (t * 64 + lane) * 8) = d[t];
+    for (int t = 0; t < RT; ++t) {
+        if constexpr (V == 8) *(u32x4*)(lds + (t * 64 + lane) * 8) = d[t];
+        else {
+            *(u32x2*)(lds + (2 * t * 64 + lane) * 4) = u32x2{d[t].x, d[t].y};
+            *(u32x2*)(lds + ((2 * t + 1) * 64 + lane) * 4) = u32x2{d[t].z, d[t].w};
+        }
+    }
     wave_sync();
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
@@ -302,7 +317,7 @@ __device__ __forceinline__ void gather_tile(const uint16_t* p, int64_t rows, int
 // from its rows, 64 bytes each, took 1.5 times as long at rank 64).  Bound by
 // x's bytes at rank 16 (4096 x 5120 in 9.3 us, 4.5 TB/s; 4096 x 13824 backward
 // in 26 us), by the reads of W from the L2 above: every 16 or 32 rows read all of it.
-enum ProjMode { PROJ_FWD, PROJ_DROP, PROJ_BACK, PROJ_BACK_ANY };   // forward, with dropout, backward, any rank
+enum ProjMode { PROJ_FWD, PROJ_DROP, PROJ_BACK8, PROJ_BACK4, PROJ_BACK_ANY };   // backward: pieces of W, or gathered
 
 struct ProjArgs {
     const uint16_t* x;    // [m x k]
@@ -324,7 +339,9 @@ __global__ __launch_bounds__(64 * kProjWaves) void k_lora_project(ProjArgs g)
     constexpr bool DROP = MODE == PROJ_DROP;
     // the waves' operand tiles, then the sums
     constexpr bool FWD = MODE == PROJ_FWD || MODE == PROJ_DROP;
-    constexpr int kWave = FWD ? 16 * RT * kProjPitch * 2 : MODE == PROJ_BACK ? RT * 1024 : 0;
+    constexpr bool TILE = MODE == PROJ_BACK8 || MODE == PROJ_BACK4;
+    constexpr int V = MODE == PROJ_BACK4 ? 4 : 8;
+    constexpr int kWave = FWD ? 16 * RT * kProjPitch * 2 : TILE ? RT * 1024 : 0;
     constexpr int kTile = W * kWave, kSums = W / 2 * MB * RT * 1024;
     __shared__ __attribute__((aligned(16))) uint8_t s_mem[kTile > kSums ? kTile : kSums > 0 ? kSums : 16];
     const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
@@ -368,7 +385,7 @@ __global__ __launch_bounds__(64 * kProjWaves) void k_lora_project(ProjArgs g)
             for (int s = 0; s < 2; ++s) {
                 if (32 * s >= 64 - over) break;   // no step there (uniform)
                 u32x4 d[RT];
-                if constexpr (MODE == PROJ_BACK) load_tile<RT>(g.w, g.k, g.rank, k0 + 32 * s, r0, d);
+                if constexpr (TILE) load_tile<RT, V>(g.w, g.k, g.rank, k0 + 32 * s, r0, d);
                 else gather_tile<RT>(g.w, g.k, g.rank, k0 + 32 * s, r0, d);
 #pragma unroll
                 for (int j = 0; j < RT; ++j) w[s * RT + j] = d[j];
@@ -404,7 +421,7 @@ __global__ __launch_bounds__(64 * kProjWaves) void k_lora_project(ProjArgs g)
                 u32x4 d[RT];
 #pragma unroll
                 for (int j = 0; j < RT; ++j) d[j] = f[j] = w[s * RT + j];
-                if constexpr (MODE == PROJ_BACK) transpose_tile<RT>(d, tile, f);
+                if constexpr (TILE) transpose_tile<RT, V>(d, tile, f);
             }
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
@@ -507,10 +524,11 @@ struct GradArgs {
 // room for on a CU.
 template <int RT> constexpr int kGradWaves = RT == 1 ? 16 : 8;
 
-template <int DT, bool DROP, bool VEC, int RT>
+template <int DT, bool DROP, int V, int RT>
 __global__ __launch_bounds__(64 * kGradWaves<RT>) void k_lora_grad(GradArgs g)
 {
     constexpr int W = kGradWaves<RT>;
+    constexpr bool VEC = V > 1;   // pieces of u; gathered otherwise
     // the waves' tiles of u, then the sums
     constexpr int kTile = VEC ? W * RT * 1024 : 0, kSums = W / 2 * 8 * RT * 1024;
     __shared__ __attribute__((aligned(16))) uint8_t s_mem[kTile > kSums ? kTile : kSums];
@@ -536,8 +554,8 @@ __global__ __launch_bounds__(64 * kGradWaves<RT>) void k_lora_grad(GradArgs g)
         }
         if constexpr (VEC) {
             u32x4 d[RT];
-            load_tile<RT>(g.u, s1, g.rank, m0, r0, d);
-            transpose_tile<RT>(d, (uint16_t*)(s_mem + wv * RT * 1024), a);
+            load_tile<RT, V>(g.u, s1, g.rank, m0, r0, d);
+            transpose_tile<RT, V>(d, (uint16_t*)(s_mem + wv * RT * 1024), a);
         } else {
             gather_tile<RT>(g.u, s1, g.rank, m0, r0, a);
         }
@@ -720,7 +738,10 @@ hipError_t project_shape(const ProjArgs& g, hipStream_t s)
 template <int DT>
 hipError_t project_dt(const ProjArgs& g, bool backward, hipStream_t s)
 {
-    if (backward) return g.rank % 8 == 0 ? project_shape<DT, PROJ_BACK>(g, s) : project_shape<DT, PROJ_BACK_ANY>(g, s);
+    if (backward) {
+        if (g.rank % 8 == 0) return project_shape<DT, PROJ_BACK8>(g, s);
+        return g.rank % 4 == 0 ? project_shape<DT, PROJ_BACK4>(g, s) : project_shape<DT, PROJ_BACK_ANY>(g, s);
+    }
     return g.drop.thr ? project_shape<DT, PROJ_DROP>(g, s) : project_shape<DT, PROJ_FWD>(g, s);
 }
 
@@ -766,25 +787,30 @@ int lora_grad_splits(int64_t m, int64_t n, int rank)
 
 namespace {
 
-template <int DT, bool DROP, bool VEC>
+template <int DT, bool DROP, int V>
 hipError_t grad_go(const GradArgs& g, int splits, hipStream_t s)
 {
     const int rt = grad_rt(g.rank);
     const int64_t gx = (g.n + 127) / 128;
     if (gx > kMaxGrid || splits > 65535) return hipErrorInvalidValue;
     const dim3 grid((unsigned)gx, (unsigned)splits, (unsigned)((g.rank + 16 * rt - 1) / (16 * rt)));
-    if (rt == 1) hipLaunchKernelGGL((k_lora_grad<DT, DROP, VEC, 1>), grid, dim3(64 * kGradWaves<1>), 0, s, g);
-    else if (rt == 2) hipLaunchKernelGGL((k_lora_grad<DT, DROP, VEC, 2>), grid, dim3(64 * kGradWaves<2>), 0, s, g);
-    else hipLaunchKernelGGL((k_lora_grad<DT, DROP, VEC, 4>), grid, dim3(64 * kGradWaves<4>), 0, s, g);
+    if (rt == 1) hipLaunchKernelGGL((k_lora_grad<DT, DROP, V, 1>), grid, dim3(64 * kGradWaves<1>), 0, s, g);
+    else if (rt == 2) hipLaunchKernelGGL((k_lora_grad<DT, DROP, V, 2>), grid, dim3(64 * kGradWaves<2>), 0, s, g);
+    else hipLaunchKernelGGL((k_lora_grad<DT, DROP, V, 4>), grid, dim3(64 * kGradWaves<4>), 0, s, g);
     return hipGetLastError();
+}
+
+template <int DT, bool DROP>
+hipError_t grad_rank(const GradArgs& g, int splits, hipStream_t s)
+{
+    if (g.rank % 8 == 0) return grad_go<DT, DROP, 8>(g, splits, s);
+    return g.rank % 4 == 0 ? grad_go<DT, DROP, 4>(g, splits, s) : grad_go<DT, DROP, 1>(g, splits, s);
 }
 
 template <int DT>
 hipError_t grad_dt(const GradArgs& g, int splits, hipStream_t s)
 {
-    const bool vec = g.rank % 8 == 0;
-    if (g.drop.thr) return vec ? grad_go<DT, true, true>(g, splits, s) : grad_go<DT, true, false>(g, splits, s);
-    return vec ? grad_go<DT, false, true>(g, splits, s) : grad_go<DT, false, false>(g, splits, s);
+    return g.drop.thr ? grad_rank<DT, true>(g, splits, s) : grad_rank<DT, false>(g, splits, s);
 }
 
 }  // namespace
