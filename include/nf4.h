@@ -420,7 +420,7 @@ nf4_status nf4_linear(const nf4_layer* w, int64_t rows, int64_t cols, nf4_format
  *   dy, preact, dz  device [m x n] of dtype, 16-byte aligned; dz may be dy
  *   dbias           device fp32 [n], 16-byte aligned, or NULL
  * NF4_ACT_NONE: preact is not read and may be NULL, and so may dz (dbias
- * alone).  n < 2^27, a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25.  ws:
+ * alone).  n < 2^26, a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25.  ws:
  * nf4_act_grad_workspace_bytes(m, n) with dbias, else unused. */
 nf4_status nf4_act_grad(const void* dy, const void* preact, int32_t act, int64_t m, int64_t n,
                         int32_t dtype, void* dz, float* dbias, void* ws, size_t ws_bytes,
@@ -435,7 +435,7 @@ nf4_status nf4_dropout(const void* x, int64_t n, int32_t dtype, nf4_drop drop, v
 /* The adapter's down product and its gradient's counterpart, rounded once:
  *   backward 0: h[m x rank] = scale drop(x) w^T, x [m x k], w [rank x k]  (h = s drop(x) A^T)
  *   backward 1: h[m x rank] = scale x w,         x [m x k], w [k x rank]  (dh = s dz B)
- * k < 2^27, a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25; device
+ * k < 2^26, a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25; device
  * buffers of dtype, 16-byte aligned.  Dropout with backward 1: NF4_E_UNSUPPORTED. */
 nf4_status nf4_lora_project(const void* x, int64_t m, int64_t k, const void* w, int32_t rank,
                             int32_t dtype, int32_t backward, float scale, nf4_drop drop, void* h,
@@ -446,7 +446,7 @@ typedef enum { NF4_LORA_A = 0, NF4_LORA_B = 1 } nf4_lora_side;
 /* The adapter's weight gradients, fp32:
  *   side NF4_LORA_A: grad[rank x n] = u^T drop(x)   (dA, u = dh, x the layer's input)
  *   side NF4_LORA_B: grad[n x rank] = x^T u         (dB, u = h, x = dz)
- * u [m x rank] and x [m x n] of dtype, grad fp32, all 16-byte aligned; n < 2^27,
+ * u [m x rank] and x [m x n] of dtype, grad fp32, all 16-byte aligned; n < 2^26,
  * a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25.  Dropout on side B:
  * NF4_E_UNSUPPORTED.  ws: nf4_lora_grad_workspace_bytes(m, n, rank), may be
  * NULL when that is 0. */

@@ -380,8 +380,9 @@ def _rng_arg(p: float, rng, where: str, dev: int) -> nf4_drop:
         return _NO_DROP
     if rng is None:
         _misfit(where, "dropout needs rng")
-    if (rng.numel() != 2 or rng.element_size() != 8 or rng.is_floating_point() or rng.get_device() != dev
-            or not rng.is_contiguous()):
+    import torch
+    if (rng.numel() != 2 or (rng.dtype is not torch.int64 and rng.dtype is not torch.uint64)
+            or rng.get_device() != dev or not rng.is_contiguous()):
         _misfit(where, f"rng must hold {{seed, offset}} as 64-bit integers on device {dev}")
     return nf4_drop(rng.data_ptr(), p)
 
@@ -443,7 +444,7 @@ def nf4_linear(layer, rows: int, cols: int, f: nf4_format, x, out, ws=None, back
         e.u = _fits(u, "u", w, (m, r) if u.dim() == 2 or m > 1 else (r,), t16, dev)
         e.v = _fits(v, "v", w, (r, cols) if backward else (rows, r), t16, dev)
         e.rank = r
-    e.act = act
+    e.act = int(act)
     if p:
         e.drop = _rng_arg(p, rng, w, dev)
     if bias is not None:
@@ -453,7 +454,7 @@ def nf4_linear(layer, rows: int, cols: int, f: nf4_format, x, out, ws=None, back
     if residual is not None:
         e.residual = _fits(residual, "residual", w, os_, out.dtype, dev)
     wp, wb = _ws_arg(ws, w, dev)
-    _enqueue(w, dev, stream, ctypes.byref(layer), rows, cols, f, 1 if backward else 0, xp, m, ctypes.byref(e), op,
+    _enqueue(w, dev, stream, ctypes.byref(layer), int(rows), int(cols), f, 1 if backward else 0, xp, m, ctypes.byref(e), op,
              1 if f32 else 0, wp, wb)
 
 
@@ -473,7 +474,7 @@ def nf4_act_grad(dy, preact, act: int, dz=None, dbias=None, ws=None, stream=None
     zp = None if dz is None else _fits(dz, "dz", w, shape, dy.dtype, dev)
     bp = None if dbias is None else _fits(dbias, "dbias", w, (n,), torch.float32, dev)
     wp, wb = _ws_arg(ws, w, dev)
-    _enqueue(w, dev, stream, dp, pp, act, m, n, dt, zp, bp, wp, wb)
+    _enqueue(w, dev, stream, dp, pp, int(act), m, n, dt, zp, bp, wp, wb)
 
 
 def nf4_act_grad_workspace_bytes(m: int, n: int) -> int:

@@ -144,8 +144,8 @@ __global__ __launch_bounds__(256) void k_act_grad(ActArgs g)
 {
     __shared__ __attribute__((aligned(16))) float s_sum[256 * 8];
     const int t = threadIdx.x, L = 1 << g.lshift, lane = t & (L - 1), row0 = t >> g.lshift, nrow = 256 >> g.lshift;
-    const int64_t col = ((int64_t)blockIdx.y * L + lane) * 8;
-    const int64_t m0 = (int64_t)blockIdx.x * nrow * g.rows + row0;
+    const int64_t col = ((int64_t)blockIdx.x * L + lane) * 8;
+    const int64_t m0 = (int64_t)blockIdx.y * nrow * g.rows + row0;
     float sum[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
@@ -179,8 +179,8 @@ __global__ __launch_bounds__(256) void k_act_grad(ActArgs g)
     for (int c = t; c < 8 * L; c += 256) {
         float a = 0.0f;
         for (int r = 0; r < nrow; ++r) a += s_sum[(r << g.lshift) * 8 + c];
-        const int64_t cc = (int64_t)blockIdx.y * L * 8 + c;
-        if (cc < g.n) ((GLOBAL float*)g.part)[(int64_t)blockIdx.x * g.n + cc] = a;
+        const int64_t cc = (int64_t)blockIdx.x * L * 8 + c;
+        if (cc < g.n) ((GLOBAL float*)g.part)[(int64_t)blockIdx.y * g.n + cc] = a;
     }
 }
 
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(64 * kProjWaves) void k_lora_project(ProjArgs g)
     PhiloxKey key = {};
     if constexpr (DROP) key = philox_key(g.drop.rng);
     // Loads address a uniform base, advanced per chunk, plus a 32-bit lane
-    // offset (k is below 2^27).  Rows and ranks past the end repeat the last
+    // offset (k is below 2^26).  Rows and ranks past the end repeat the last
     // one: they feed only results that are not stored.
     uint32_t xo[MB];
     uint64_t grp[MB];   // mask group of this lane's k in the row, chunk at 0
@@ -694,9 +694,9 @@ hipError_t launch_act_grad(int dtype, const void* dy, const void* z, int act, in
     g.act = act;
     g.lshift = act_lshift(n);
     g.rows = act_rows(m, n);
-    const int64_t cols = int64_t(8) << g.lshift, gy = (n + cols - 1) / cols;
-    if (blocks > kMaxGrid || gy > 65535) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks, (unsigned)gy);
+    const int64_t cols = int64_t(8) << g.lshift, gx = (n + cols - 1) / cols;
+    if (gx > kMaxGrid || blocks > 65535) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)gx, (unsigned)blocks);
     if (dtype == 0) hipLaunchKernelGGL((k_act_grad<0>), grid, dim3(256), 0, s, g);
     else hipLaunchKernelGGL((k_act_grad<1>), grid, dim3(256), 0, s, g);
     hipError_t e = hipGetLastError();

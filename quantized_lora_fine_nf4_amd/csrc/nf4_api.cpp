@@ -262,8 +262,8 @@ size_t matmul_tail_bytes(int64_t rows, int64_t cols, int32_t backward, int64_t m
 
 constexpr int32_t kMaxLoraRank = 128;
 // tokens of the adapter and epilogue-gradient calls, and elements of a dropout
-// (their grids); columns of theirs are below 2^27 (32-bit offsets in 16 rows)
-constexpr int64_t kMaxTokens = int64_t(1) << 25, kMaxDrop = int64_t(1) << 36, kMaxCols = int64_t(1) << 27;
+// (their grids); columns of theirs are below 2^26 (32-bit byte offsets in 32 rows)
+constexpr int64_t kMaxTokens = int64_t(1) << 25, kMaxDrop = int64_t(1) << 36, kMaxCols = int64_t(1) << 26;
 
 // The drop probability as a 16-bit threshold.  p = 0 (or a p that rounds to
 // it) is no dropout and needs no rng.

@@ -70,7 +70,7 @@ def test_act_grad_arguments():
     assert call(m=0) == q.NF4_E_ARG
     assert call(m=(1 << 25) + 1) == q.NF4_E_ARG
     assert call(n=0) == q.NF4_E_ARG
-    assert call(n=1 << 31) == q.NF4_E_ARG
+    assert call(n=1 << 26) == q.NF4_E_ARG
     assert call(n=12) == q.NF4_E_UNSUPPORTED
     assert call(dt=2) == q.NF4_E_UNSUPPORTED
     for k in ("dy", "z", "dz", "db"):
@@ -81,7 +81,7 @@ def test_act_grad_arguments():
     assert call(ws=None) == q.NF4_E_WORKSPACE
     assert call(ws=FAKE + 16) == q.NF4_E_WORKSPACE
     assert q.nf4_act_grad_workspace_bytes(1, 512) == 0     # one block of tokens
-    for m, n in ((0, 8), (1, 0), (1, 12), ((1 << 25) + 1, 8), (1, 1 << 31)):
+    for m, n in ((0, 8), (1, 0), (1, 12), ((1 << 25) + 1, 8), (1, 1 << 26)):
         assert q.nf4_act_grad_workspace_bytes(m, n) == 0
 
 
@@ -96,7 +96,7 @@ def test_project_arguments():
     assert call(m=0) == q.NF4_E_ARG
     assert call(m=(1 << 25) + 1) == q.NF4_E_ARG
     assert call(k=0) == q.NF4_E_ARG
-    assert call(k=1 << 31) == q.NF4_E_ARG
+    assert call(k=1 << 26) == q.NF4_E_ARG
     assert call(k=100) == q.NF4_E_UNSUPPORTED
     assert call(r=0) == q.NF4_E_ARG
     assert call(r=-1) == q.NF4_E_ARG
@@ -119,6 +119,7 @@ def test_lora_grad_arguments():
     assert call(m=0) == q.NF4_E_ARG
     assert call(m=(1 << 25) + 1) == q.NF4_E_ARG
     assert call(n=0) == q.NF4_E_ARG
+    assert call(n=1 << 26) == q.NF4_E_ARG
     assert call(n=100) == q.NF4_E_UNSUPPORTED
     assert call(r=0) == q.NF4_E_ARG
     assert call(r=129) == q.NF4_E_UNSUPPORTED
@@ -201,6 +202,8 @@ def test_binding_checks_shapes_types_and_devices():
     assert "rng" in _bad(q.nf4_dropout, b(4), b(4), 0.1, None)
     assert "rng" in _bad(q.nf4_dropout, b(4), b(4), 0.1, torch.zeros(3, dtype=torch.int64))
     assert "rng" in _bad(q.nf4_dropout, b(4), b(4), 0.1, torch.zeros(2, dtype=torch.int32))
+    assert "rng" in _bad(q.nf4_dropout, b(4), b(4), 0.1, torch.zeros(2, dtype=torch.complex64))
+    assert "rng" in _bad(q.nf4_dropout, b(4), b(4), 0.1, torch.zeros(2, dtype=torch.float64))
     assert "GPU" in _bad(q.nf4_act_grad, b(4, 8), b(4, 8), 1, b(4, 8))
     assert "preact" in _bad(q.nf4_act_grad, b(4, 8), b(4, 7), 1, b(4, 8))
     assert "dz" in _bad(q.nf4_act_grad, b(4, 8), b(4, 8), 1, f32(4, 8))

@@ -199,7 +199,9 @@ def test_act_grad_past_32_bit_offsets():
 @pytest.mark.parametrize("dtype", DT, ids=IDS)
 @pytest.mark.parametrize("back,p", [(False, 0.0), (False, 0.2), (True, 0.0)], ids=["fwd", "drop", "bwd"])
 @pytest.mark.parametrize("m,k,r", [(1, 8, 1), (1, 5120, 16), (5, 136, 4), (16, 128, 16), (17, 1000, 24), (33, 2048, 64),
-                                   (1030, 264, 20), (1100, 520, 64), (1025, 128, 128), (40, 4104, 100)])
+                                   (1030, 264, 20), (1100, 520, 64), (1025, 128, 128), (40, 4104, 100),
+                                   # 16 ranks a workgroup and 32 rows; 32 ranks; 64 ranks and 32 rows; any-rank gathers
+                                   (4100, 72, 7), (2100, 200, 30), (2200, 136, 61), (4200, 80, 127), (4112, 64, 16)])
 def test_project(dtype, back, p, m, k, r):
     """Half a step, and in fp32: k products summed (k / 32 matrix steps per wave, up to 16 waves), scale times
     factor and the product with it (3 half steps)."""
@@ -249,7 +251,8 @@ def test_project_past_32_bit_offsets():
 @pytest.mark.parametrize("dtype", DT, ids=IDS)
 @pytest.mark.parametrize("side,p", [("A", 0.0), ("A", 0.2), ("B", 0.0)], ids=["A", "A-drop", "B"])
 @pytest.mark.parametrize("m,n,r", [(1, 8, 1), (1, 128, 16), (31, 136, 5), (33, 1000, 16), (300, 264, 24),
-                                   (777, 2048, 64), (2500, 64, 128), (1300, 136, 100), (4096, 256, 16)])
+                                   (777, 2048, 64), (2500, 64, 128), (1300, 136, 100), (4096, 256, 16), (500, 264, 30),
+                                   (600, 136, 61), (900, 72, 127)])
 def test_lora_grad(dtype, side, p, m, n, r):
     """fp32: m products summed (in 32-row matrix steps, waves and splits) and the factor (2 half steps)."""
     print_case("nf4_lora_grad", dtype, side, p, m, n, r)
@@ -383,6 +386,7 @@ class Case:
                                          (256, 384, 33), (384, 128, 128), (256, 128, 200), (128, 2048, 300)])
 @pytest.mark.parametrize("r,act,bias,residual,f32", [(16, "none", False, False, False), (0, "gelu", True, False, False),
                                                      (8, "silu", True, True, True), (5, "gelu_tanh", False, True, False),
+                                                     (67, "none", True, True, True),
                                                      (100, "relu", True, False, True), (128, "silu", False, False, False)])
 def test_linear_forward(dtype, rows, cols, m, r, act, bias, residual, f32):
     print_case("nf4_linear", dtype, rows, cols, m, r, act, bias, residual, f32)
@@ -400,6 +404,7 @@ def test_linear_forward(dtype, rows, cols, m, r, act, bias, residual, f32):
                                          (256, 5120, 200)])
 @pytest.mark.parametrize("r,p,residual,f32", [(16, 0.0, False, False), (0, 0.0, True, False), (8, 0.1, True, True),
                                               (5, 0.5, False, False), (100, 0.1, True, False), (128, 0.0, False, True),
+                                              (67, 0.1, False, False), (127, 0.0, True, True),
                                               (128, 0.3, False, True)])
 def test_linear_backward(dtype, rows, cols, m, r, p, residual, f32):
     print_case("nf4_linear backward", dtype, rows, cols, m, r, p, residual, f32)
@@ -419,7 +424,8 @@ BIG = [(False, 13824, 256, 700), (False, 4992, 4096, 3900), (False, 5120, 256, 3
 
 
 @pytest.mark.parametrize("back,rows,cols,m", BIG, ids=[f"{'bwd' if b else 'fwd'}-{r}x{c}-{m}" for b, r, c, m in BIG])
-@pytest.mark.parametrize("dtype,r,f32", [(torch.bfloat16, 16, False), (torch.float16, 72, True)], ids=["bf16-r16", "fp16-r72-f32"])
+@pytest.mark.parametrize("dtype,r,f32", [(torch.bfloat16, 16, False), (torch.float16, 72, True), (torch.bfloat16, 93, True)],
+                         ids=["bf16-r16", "fp16-r72-f32", "bf16-r93-f32"])
 def test_linear_large_tiles(back, rows, cols, m, dtype, r, f32):
     """Sampled rows of every tile row's first and last, and every row of the last 300."""
     print_case("nf4_linear large tiles", dtype, "bwd" if back else "fwd", rows, cols, m, r)
@@ -433,6 +439,28 @@ def test_linear_large_tiles(back, rows, cols, m, dtype, r, f32):
     if back:   # without dropout too: the accumulators' own path
         c.p = 0.0
         c.check(c.run(), None, rows=idx)
+
+
+@pytest.mark.parametrize("back", [False, True], ids=["fwd", "bwd"])
+def test_linear_past_32_bit_offsets(back):
+    """160,000 x 13,824 outputs (2.2e9): the last rows, with preactivation and residual forward (in place) and the
+    mask of the low-rank term backward."""
+    rows, cols, m, r = (128, 13824, 160_000, 8) if back else (13824, 128, 160_000, 8)
+    print_case("nf4_linear past 32 bits", "bwd" if back else "fwd")
+    W = Weight(rows, cols, torch.bfloat16, True, seed=3)
+    kw = dict(p=0.2) if back else dict(act="silu", bias=True)
+    c = Case(W, m, r, back, seed=9, **kw)
+    idx = [0, 77_000, 155_343, 155_344] + list(range(m - 40, m))
+    if back:
+        c.check(c.run(), None, rows=idx)
+        return
+    c.res = torch.ones(m, c.ncol, dtype=torch.bfloat16, device="cuda")
+    out, pre = torch.empty_like(c.res), torch.empty_like(c.res)
+    need = q.nf4_matmul_workspace_bytes(rows, cols, back, m)
+    out.fill_(1.0)
+    q.nf4_linear(W.layer, rows, cols, W.f, c.x, out, workspace(need), lora=c.lora, bias=c.bias, act=q.NF4_ACT_SILU,
+                 preact=pre, residual=out)
+    c.check(out, pre, rows=idx)
 
 
 def test_linear_empty_epilogue_is_the_matmul():
