@@ -66,7 +66,7 @@ __device__ __forceinline__ uint16_t pack1(float a) { return (uint16_t)pack2<DT>(
 
 // ---- dropout
 //
-// Bound by memory: 4 bytes per element; 8192 x 13824 in 80 us, 5.7 TB/s (the
+// Bound by memory: 4 bytes per element; 8192 x 13824 in 77 us, 5.9 TB/s (the
 // generator and the masks are about 45 vector instructions per eight elements,
 // 38 us of issue at that size).  One mask group (eight elements, 16 bytes) per
 // thread and step, four loads in flight.
@@ -84,8 +84,21 @@ __device__ __forceinline__ u32x4 drop8(const u32x4& x, const Bits128& b, uint32_
     return r;
 }
 
+// Results past what the caches hold for the next kernel go around them (stream):
+// at 113 MB dropout takes 39.6 us instead of 42.2, act_grad 69.8 instead of 73.1;
+// below that the next kernel reads them from the caches (act_grad, project and
+// grad over 28 MB: 48.6 us, 53.2 with streamed stores; over 113 MB 121 both ways).
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
+
+template <bool STREAM>
+__device__ __forceinline__ void store_result(const u32x4& v, GLOBAL u32x4* p)
+{
+    if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
 // DROP false (probability 0, no rng): a copy.
-template <int DT, bool DROP>
+template <int DT, bool DROP, bool STREAM>
 __global__ __launch_bounds__(256) void k_dropout(const uint16_t* x, int64_t n, DropArgs d, uint16_t* out)
 {
     PhiloxKey key = {};
@@ -102,7 +115,7 @@ __global__ __launch_bounds__(256) void k_dropout(const uint16_t* x, int64_t n, D
         const int64_t g = g0 + 256 * i;
         if (g >= groups) continue;
         if constexpr (DROP) v[i] = drop8<DT>(v[i], philox7(key, (uint64_t)g), d.thr, d.keep);
-        ((GLOBAL u32x4*)out)[g] = v[i];
+        store_result<STREAM>(v[i], (GLOBAL u32x4*)out + g);
     }
     // the last partial group, element by element
     if (blockIdx.x == 0 && threadIdx.x == 0 && (n & 7)) {
@@ -115,19 +128,19 @@ __global__ __launch_bounds__(256) void k_dropout(const uint16_t* x, int64_t n, D
     }
 }
 
-template <int DT>
+template <int DT, bool STREAM>
 hipError_t dropout_go(const uint16_t* x, int64_t n, DropArgs d, uint16_t* out, unsigned blocks, hipStream_t s)
 {
-    if (d.thr) hipLaunchKernelGGL((k_dropout<DT, true>), dim3(blocks), dim3(256), 0, s, x, n, d, out);
-    else hipLaunchKernelGGL((k_dropout<DT, false>), dim3(blocks), dim3(256), 0, s, x, n, d, out);
+    if (d.thr) hipLaunchKernelGGL((k_dropout<DT, true, STREAM>), dim3(blocks), dim3(256), 0, s, x, n, d, out);
+    else hipLaunchKernelGGL((k_dropout<DT, false, STREAM>), dim3(blocks), dim3(256), 0, s, x, n, d, out);
     return hipGetLastError();
 }
 
 // ---- gradient of the epilogue
 //
 // Bound by memory: 6 bytes per element; 4096 x 13824 (silu, with the bias
-// gradient) in 72 us, 4.7 TB/s, and 4.6 us for the sum of the partials.  A
-// workgroup takes 8 L columns (L lanes
+// gradient) in 69.8 us with the sum of the partials, 4.9 TB/s.  A workgroup
+// takes 8 L columns (L lanes
 // of eight, a power of two up to 64) and `rows` rows per lane; the column
 // sums are kept per lane over its rows, added over the workgroup's rows in
 // LDS and stored as one partial row per row block, added in block order by
@@ -142,7 +155,7 @@ struct ActArgs {
     int64_t rows;      // rows per lane
 };
 
-template <int DT>
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(256) void k_act_grad(ActArgs g)
 {
     __shared__ __attribute__((aligned(16))) float s_sum[256 * 8];
@@ -153,25 +166,35 @@ __global__ __launch_bounds__(256) void k_act_grad(ActArgs g)
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
     if (col < g.n) {
-        for (int64_t r = 0; r < g.rows; ++r) {
-            const int64_t row = m0 + r * nrow;
-            if (row >= g.m) break;
-            const int64_t at = row * g.n + col;
-            const u32x4 dy = *(const GLOBAL u32x4*)(g.dy + at);
-            u32x4 zv = {0, 0, 0, 0};
-            if (g.act != ACT_NONE) zv = *(const GLOBAL u32x4*)(g.z + at);
-            u32x4 o;
+        // two rows' loads in flight (the last row of an odd count twice, once used)
+        for (int64_t r = 0; r < g.rows; r += 2) {
+            const int64_t row[2] = {m0 + r * nrow, m0 + (r + 1) * nrow};
+            const bool in[2] = {row[0] < g.m, r + 1 < g.rows && row[1] < g.m};
+            if (!in[0]) break;
+            u32x4 dy[2], zv[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f32x2 v = unpack2<DT>(dy[j]);
-                const f32x2 z = unpack2<DT>(zv[j]);
-                v.x *= act_slope(z.x, g.act);
-                v.y *= act_slope(z.y, g.act);
-                sum[2 * j] += v.x;
-                sum[2 * j + 1] += v.y;
-                o[j] = pack2<DT>(v.x, v.y);
+            for (int k = 0; k < 2; ++k) {
+                const int64_t at = (in[k] ? row[k] : row[0]) * g.n + col;
+                dy[k] = *(const GLOBAL u32x4*)(g.dy + at);
+                zv[k] = u32x4{0, 0, 0, 0};
+                if (g.act != ACT_NONE) zv[k] = *(const GLOBAL u32x4*)(g.z + at);
             }
-            if (g.dz) *(GLOBAL u32x4*)(g.dz + at) = o;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (!in[k]) continue;
+                u32x4 o;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f32x2 v = unpack2<DT>(dy[k][j]);
+                    const f32x2 z = unpack2<DT>(zv[k][j]);
+                    v.x *= act_slope(z.x, g.act);
+                    v.y *= act_slope(z.y, g.act);
+                    sum[2 * j] += v.x;
+                    sum[2 * j + 1] += v.y;
+                    o[j] = pack2<DT>(v.x, v.y);
+                }
+                if (g.dz) store_result<STREAM>(o, (GLOBAL u32x4*)(g.dz + row[k] * g.n + col));
+            }
         }
     }
     if (!g.part) return;   // uniform
@@ -657,7 +680,10 @@ hipError_t launch_dropout(int dtype, const void* x, int64_t n, DropArgs d, void*
     if (blocks > kMaxGrid) return hipErrorInvalidValue;
     const uint16_t* xi = static_cast<const uint16_t*>(x);
     uint16_t* o = static_cast<uint16_t*>(out);
-    return dtype == 0 ? dropout_go<0>(xi, n, d, o, (unsigned)blocks, s) : dropout_go<1>(xi, n, d, o, (unsigned)blocks, s);
+    const unsigned b = (unsigned)blocks;
+    if (2 * n > kStreamBytes)
+        return dtype == 0 ? dropout_go<0, true>(xi, n, d, o, b, s) : dropout_go<1, true>(xi, n, d, o, b, s);
+    return dtype == 0 ? dropout_go<0, false>(xi, n, d, o, b, s) : dropout_go<1, false>(xi, n, d, o, b, s);
 }
 
 namespace {
@@ -671,13 +697,18 @@ int act_lshift(int64_t n)
 }
 
 // Rows per lane: eight (32 rows and a 4% partial per workgroup at 64 lanes),
-// more where that would make over 4,096 workgroups.
+// more where that would make over 4,096 workgroups, four or two where it would
+// make fewer than 1,024 and there is more than one block of tokens anyway (333 x
+// 8192: two 9.2 us, eight 14.1; 17 x 5120 in one block 6.5 us, in three 9.4).
 int64_t act_rows(int64_t m, int64_t n)
 {
     const int ls = act_lshift(n);
-    const int64_t cols = int64_t(8) << ls, gy = (n + cols - 1) / cols, lrows = (m + (256 >> ls) - 1) / (256 >> ls);
-    const int64_t target = 4096 / gy > 1 ? 4096 / gy : 1, rows = (lrows + target - 1) / target;
-    return rows > 8 ? rows : 8;
+    const int64_t cols = int64_t(8) << ls, gx = (n + cols - 1) / cols, lrows = (m + (256 >> ls) - 1) / (256 >> ls);
+    if (lrows <= 8) return lrows;
+    const int64_t target = 4096 / gx > 1 ? 4096 / gx : 1, rows = (lrows + target - 1) / target;
+    if (rows > 8) return rows;
+    const int64_t fill = lrows * gx / 1024;
+    return fill >= 8 ? 8 : fill >= 4 ? 4 : 2;
 }
 
 }  // namespace
@@ -705,8 +736,13 @@ hipError_t launch_act_grad(int dtype, const void* dy, const void* z, int act, in
     const int64_t cols = int64_t(8) << g.lshift, gx = (n + cols - 1) / cols;
     if (gx > kMaxGrid || blocks > 65535) return hipErrorInvalidValue;
     const dim3 grid((unsigned)gx, (unsigned)blocks);
-    if (dtype == 0) hipLaunchKernelGGL((k_act_grad<0>), grid, dim3(256), 0, s, g);
-    else hipLaunchKernelGGL((k_act_grad<1>), grid, dim3(256), 0, s, g);
+    if (2 * m * n > kStreamBytes) {
+        if (dtype == 0) hipLaunchKernelGGL((k_act_grad<0, true>), grid, dim3(256), 0, s, g);
+        else hipLaunchKernelGGL((k_act_grad<1, true>), grid, dim3(256), 0, s, g);
+    } else {
+        if (dtype == 0) hipLaunchKernelGGL((k_act_grad<0, false>), grid, dim3(256), 0, s, g);
+        else hipLaunchKernelGGL((k_act_grad<1, false>), grid, dim3(256), 0, s, g);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !dbias || blocks <= 1) return e;
     return sum_parts(part, (int)blocks, n, 1.0f, dbias, s);
