@@ -67,7 +67,8 @@ hipError_t launch_nf4_matmul(int dtype, const uint8_t* codes, const int8_t* qabs
 {
     const GemmArgs g = gemm_args(codes, qabsmax, scale2, absmax, rows, cols, forward, x, m, out, part, nsplit,
                                  tail_split);
-    return gemm_any(dtype, forward, qabsmax != nullptr, out_f32, g, NoEpi{}, s);
+    return forward ? gemm_any<true>(dtype, qabsmax != nullptr, out_f32, g, NoEpi{}, s)
+                   : gemm_any<false>(dtype, qabsmax != nullptr, out_f32, g, NoEpi{}, s);
 }
 
 }  // namespace nf4k

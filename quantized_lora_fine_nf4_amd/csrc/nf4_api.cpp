@@ -619,8 +619,8 @@ nf4_status nf4_linear(const nf4_layer* w, int64_t rows, int64_t cols, nf4_format
         const int nsplit = nf4k::nf4_matmul_splits(rows, cols, fwd, m);
         int tail = 0;
         if (nsplit <= 1) matmul_tail_bytes(rows, cols, backward, m, &tail);
-        e = nf4k::launch_nf4_linear(fmt.dtype, w->codes, qa, s2, am, rows, cols, fwd, x, m, out, out_fp32 == 1, part,
-                                    nsplit, tail, ep, stream);
+        e = (fwd ? nf4k::launch_nf4_linear : nf4k::launch_nf4_linear_back)(
+            fmt.dtype, w->codes, qa, s2, am, rows, cols, x, m, out, out_fp32 == 1, part, nsplit, tail, ep, stream);
     }
     return e == hipSuccess ? NF4_OK : hip_fail(e);
 }

@@ -93,7 +93,7 @@ hipError_t launch_select_ex(const double* err, const double* denom, const int64_
                             const int32_t* group_end, int nu, int64_t budget, int kcap, int rule,
                             uint8_t* selected, int32_t* k_out, SelectScratch w, hipStream_t s);
 
-// ---- the adapted layer's operators (k_lora.hip, k_linear.hip)
+// ---- the adapted layer's operators (k_lora.hip, k_linear.hip, k_linear_back.hip)
 
 // Dropout of a launch; thr == 0: none (rng not read).
 struct DropArgs {
@@ -119,7 +119,7 @@ int lora_grad_splits(int64_t m, int64_t n, int rank);
 hipError_t launch_lora_grad(int dtype, const void* u, const void* x, int64_t m, int64_t n, int rank, bool by_col,
                             DropArgs drop, float* grad, float* part, hipStream_t s);
 
-// What the matmul's epilogue adds to the product (k_linear.hip).  Forward
+// What the matmul's epilogue adds to the product.  Forward
 // columns are W's rows, backward W's columns.
 struct EpiArgs {
     const uint16_t* u;     // [m x rank]; null: no low-rank term
@@ -130,11 +130,14 @@ struct EpiArgs {
     int rank, act;
     DropArgs drop;         // of the low-rank term (backward)
 };
-// As launch_nf4_matmul / launch_nf4_gemv, with the epilogue.
+// As launch_nf4_matmul (forward, backward) and launch_nf4_gemv, with the epilogue.
 hipError_t launch_nf4_linear(int dtype, const uint8_t* codes, const int8_t* qabsmax, const float* scale2,
-                             const float* absmax, int64_t rows, int64_t cols, bool forward, const void* x, int64_t m,
-                             void* out, bool out_f32, float* part, int nsplit, int tail_split, const EpiArgs& epi,
-                             hipStream_t s);
+                             const float* absmax, int64_t rows, int64_t cols, const void* x, int64_t m, void* out,
+                             bool out_f32, float* part, int nsplit, int tail_split, const EpiArgs& epi, hipStream_t s);
+hipError_t launch_nf4_linear_back(int dtype, const uint8_t* codes, const int8_t* qabsmax, const float* scale2,
+                                  const float* absmax, int64_t rows, int64_t cols, const void* x, int64_t m, void* out,
+                                  bool out_f32, float* part, int nsplit, int tail_split, const EpiArgs& epi,
+                                  hipStream_t s);
 hipError_t launch_nf4_linear_gemv(int dtype, const uint8_t* codes, const int8_t* qabsmax, const float* scale2,
                                   const float* absmax, int64_t rows, int64_t cols, const void* x, int64_t m, void* out,
                                   bool out_f32, float* part, int parts, const EpiArgs& epi, hipStream_t s);
