@@ -29,7 +29,8 @@
 //     workgroups per CU, the weight tile dequantised into LDS (transposed on
 //     the way backward).
 //   * forward with m <= 32 and a workspace: k_nf4_gemv16, one wave per 16
-//     weight rows on the 16 x 16 x 32 MFMA.
+//     weight rows on the 16 x 16 x 32 MFMA; for one token, where the chip holds
+//     all its workgroups at once, k_nf4_gemv1: the same waves in one launch.
 //
 // k_nf4_matmul: the first operand A is row-major with the reduction index
 // contiguous (x, or the output gradient); the W tile is stored in LDS with the
@@ -1592,7 +1593,7 @@ __global__ __launch_bounds__(256, 1) void k_nf4_mm_bwd(GemmArgs g, E e)
 // ---- few tokens, forward: one wave per 16 W rows and one part of the reduction
 //
 // out[m x rows] = x[m x cols] W^T for m <= 32 on v_mfma_f32_16x16x32 (x rows
-// padded with zeros to 16 or 32).  The reduction is cut into 128-wide super-chunks;
+// padded to 16 or 32).  The reduction is cut into 128-wide super-chunks;
 // in each, lane l takes W row n0 + l % 16 and x row l % 16 over the 32
 // consecutive k at 32 (l / 16), four MFMA steps of 8 k (any assignment of k
 // to steps gives the same dot product as long as x and W agree), so its
@@ -1628,6 +1629,78 @@ struct GemvArgs {
 
 constexpr int kGvMaxSc = 8;   // super-chunks per part with one 16-row x block (MB = 1); 8 / MB with MB blocks
 
+// Eight codes to eight weights in the 16-bit type, lv the 16 levels in LDS (one
+// bank each: reads of any mix of levels do not conflict).  The table offsets of
+// four low and four high nibbles come from one shift and mask each.
+template <int DT>
+__device__ __forceinline__ u32x4 gv_deq8(uint32_t c, float adq, const float* lv)
+{
+    uint32_t lo = (c << 2) & 0x3c3c3c3cu, hi = (c >> 2) & 0x3c3c3c3cu;
+    asm("" : "+v"(lo), "+v"(hi));   // else each nibble is shifted and masked by itself: two steps for one
+    u32x4 w;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const float a = *(const float*)((const uint8_t*)lv + ((lo >> (8 * h)) & 255u));
+        const float b = *(const float*)((const uint8_t*)lv + ((hi >> (8 * h)) & 255u));
+        w[h] = pack16<DT>(a * adq, b * adq);
+    }
+    return w;
+}
+
+// A lane's codes and block constants of one part: W row n, super-chunks s0 ..
+// s0 + ns - 1 (past them, the last one again, not used).  A whole part's loads
+// share one address; its at most 2 SC - 1 blocks meet at most two scale groups.
+template <bool DQ, int SC>
+struct GvSlab {
+    u32x4 cw[SC];
+    int32_t q[SC];
+    float s[DQ ? 2 : SC];
+    int in;   // the first block's place in its scale group
+
+    template <bool WHOLE>
+    __device__ __forceinline__ void load_part(const GemvArgs& g, int64_t n, int s0, int ns, int kg)
+    {
+        const int64_t e = n * g.cols + (int64_t)s0 * 128 + 32 * kg, b = e >> 6;
+        const GLOBAL uint8_t* cp = (const GLOBAL uint8_t*)g.codes + (e >> 1);
+        const GLOBAL int8_t* qp = (const GLOBAL int8_t*)g.qabsmax + b;
+        const GLOBAL float* ap = (const GLOBAL float*)g.absmax + b;
+        if constexpr (DQ) {
+            s[0] = ((const GLOBAL float*)g.scale2)[b >> 8];
+            s[1] = ((const GLOBAL float*)g.scale2)[(b + 2 * (ns - 1)) >> 8];
+            in = (int)(b & 255);
+        }
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            const int sc = WHOLE ? i : min(i, ns - 1);
+            cw[i] = *(const GLOBAL u32x4*)(cp + 64 * sc);
+            if constexpr (DQ) q[i] = qp[2 * sc];
+            else s[i] = ap[2 * sc];
+        }
+    }
+    __device__ __forceinline__ void load(const GemvArgs& g, int64_t n, int s0, int ns, int kg)
+    {
+        if (ns == SC) load_part<true>(g, n, s0, ns, kg);
+        else load_part<false>(g, n, s0, ns, kg);
+    }
+    __device__ __forceinline__ float absmax(int sc) const
+    {
+        if constexpr (DQ) return (float)q[sc] * (in + 2 * sc < 256 ? s[0] : s[1]);
+        else return s[sc];
+    }
+};
+
+// The low-rank term of the lane's product: 32 ranks a step, its own at 8 (l / 16).
+template <int DT>
+__device__ __forceinline__ void gv_low_rank(const EpiArgs& e, int64_t n, int64_t row, int kg, f32x4& acc)
+{
+    typedef typename Frag8<DT>::T F;
+    for (int k = 0; k < e.rank; k += 32) {
+        const u32x4 v = load8(e.v + n * e.rank, k + 8 * kg, e.rank);
+        const u32x4 u = load8(e.u + row * e.rank, k + 8 * kg, e.rank);
+        acc = mfma16<DT>(__builtin_bit_cast(F, u), __builtin_bit_cast(F, v), acc);
+    }
+}
+
 // MB: 16-row blocks of x (m <= 16 MB); each dequantised weight fragment feeds
 // MB MFMAs.  The staged x slice is always 16 MB rows x (8 / MB) super-chunks
 // (33 KB of LDS, rows padded by 16 B so the 16 lanes of a row group read
@@ -1654,74 +1727,52 @@ __global__ __launch_bounds__(256, 4) void k_nf4_gemv16(GemvArgs g, E e)
     // loads alone and the MFMAs of the first super-chunks overlap the arrival
     // of the later ones.  The x slice (cache-resident) goes first: waiting for
     // it leaves the code loads in flight.
-    const int units = ns * 16;
-    const int64_t rmax = g.m - 1;
+    const int units = ns * 16, rmax = (int)g.m - 1;
+    const int w0 = __builtin_amdgcn_readfirstlane(t & ~63);   // a wave's 64 units lie in one row
     u32x4 xv[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int u = t + 256 * i;
-        const int64_t r = min((int64_t)(u / kRowUnits), rmax);
-        const int c8 = min(u % kRowUnits, units - 1);
+        const int r = min((w0 + 256 * i) / kRowUnits, rmax), c8 = min((w0 + 256 * i) % kRowUnits + lane, units - 1);
         xv[i] = *(const GLOBAL u32x4*)((const GLOBAL uint16_t*)g.x + r * g.cols + (int64_t)s0 * 128 + 8 * c8);
     }
-    u32x4 cw[kSc];
-    RawConst kc[kSc];
-    const int64_t e0 = n * g.cols + (int64_t)s0 * 128 + 32 * kg;
-#pragma unroll
-    for (int sc = 0; sc < kSc; ++sc) {
-        const int64_t e = e0 + 128 * min(sc, ns - 1);
-        cw[sc] = *(const GLOBAL u32x4*)(g.codes + (e >> 1));
-        const int64_t b = e >> 6;
-        if constexpr (DQ) kc[sc] = RawConst{((const GLOBAL int8_t*)g.qabsmax)[b], ((const GLOBAL float*)g.scale2)[b >> 8]};
-        else kc[sc] = RawConst{0, ((const GLOBAL float*)g.absmax)[b]};
-    }
+    GvSlab<DQ, kSc> w;
+    w.load(g, n, s0, ns, kg);
     if (t == 0) {   // immediates: an indexed table would be one more memory load to wait for
 #pragma unroll
         for (int i = 0; i < 16; ++i) s_lv[i] = as_f(nf4fmt::kLevelBits[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int u = t + 256 * i, r = u / kRowUnits, c8 = u % kRowUnits;
-        if (r < g.m && c8 < units) *(u32x4*)(s_x + r * kRow + 8 * c8) = xv[i];
+        const int r = (w0 + 256 * i) / kRowUnits, c8 = (w0 + 256 * i) % kRowUnits + lane;
+        if (r <= rmax) *(u32x4*)(s_x + r * kRow + 8 * c8) = xv[i];
     }
     __syncthreads();
     typedef typename Frag8<DT>::T F;
     f32x4 acc[MB];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) acc[mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // Product rows past m are not stored: their lanes read row m - 1.
+    const uint16_t* xp[MB];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) xp[mb] = s_x + min(16 * mb + xr, rmax) * kRow + 32 * kg;
 #pragma unroll
     for (int sc = 0; sc < kSc; ++sc) {
         if (sc >= ns) break;
-        const float adq = block_const<DQ>(kc[sc]);
+        const float adq = w.absmax(sc);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            u32x4 w;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const uint32_t b = (cw[sc][j] >> (8 * h)) & 255u;
-                w[h] = pack16<DT>(s_lv[b & 15] * adq, s_lv[b >> 4] * adq);
-            }
+            const u32x4 b = gv_deq8<DT>(w.cw[sc][j], adq, s_lv);
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
-                const int xrow = 16 * mb + xr;
-                const u32x4 a = xrow < g.m ? *(const u32x4*)(s_x + xrow * kRow + 32 * kg + 128 * sc + 8 * j)
-                                           : u32x4{0u, 0u, 0u, 0u};
-                acc[mb] = mfma16<DT>(__builtin_bit_cast(F, a), __builtin_bit_cast(F, w), acc[mb]);
+                const u32x4 a = *(const u32x4*)(xp[mb] + 128 * sc + 8 * j);
+                acc[mb] = mfma16<DT>(__builtin_bit_cast(F, a), __builtin_bit_cast(F, b), acc[mb]);
             }
         }
     }
     if constexpr (E::kOn) {
-        // the low-rank term: 32 ranks a step, lane l's at 8 (l / 16)
         if (e.a.u && part == 0) {
-            for (int k = 0; k < e.a.rank; k += 32) {
-                const u32x4 v = load8(e.a.v + n * e.a.rank, k + 8 * kg, e.a.rank);
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    const int64_t row = 16 * mb + xr;
-                    const u32x4 u = load8(e.a.u + (row < g.m ? row : g.m - 1) * e.a.rank, k + 8 * kg, e.a.rank);
-                    acc[mb] = mfma16<DT>(__builtin_bit_cast(F, u), __builtin_bit_cast(F, v), acc[mb]);
-                }
-            }
+            for (int mb = 0; mb < MB; ++mb) gv_low_rank<DT>(e.a, n, min(16 * mb + xr, rmax), kg, acc[mb]);
         }
     }
     // lane l: output rows 16 mb + 4 (l / 16) + r of W row n
@@ -1733,6 +1784,84 @@ __global__ __launch_bounds__(256, 4) void k_nf4_gemv16(GemvArgs g, E e)
             const int row = 16 * mb + 4 * kg + r;
             if (row < g.m) dst[(int64_t)row * g.rows + n] = acc[mb][r];
         }
+}
+
+// Four summed outputs from element i, column col, on through the epilogue.
+template <int DT, bool OUT_F32, class E>
+__device__ __forceinline__ void store_sum(const E& e, const f32x4& acc, int64_t i, int64_t col, void* out)
+{
+    if constexpr (E::kOn) {
+        float z[4] = {acc.x, acc.y, acc.z, acc.w}, bias[4], res[4];
+        load_bias<DT, 4>(e.a, col, bias);
+        load_residual<DT, OUT_F32, 4>(e.a, i, res);
+        finish<DT, true, OUT_F32, false, 4>(e.a, z, bias, res, i, out);
+    } else if constexpr (OUT_F32) {
+        *(GLOBAL f32x4*)((float*)out + i) = acc;
+    } else {
+        *(GLOBAL u32x2*)((uint16_t*)out + i) = u32x2{pack16<DT>(acc.x, acc.y), pack16<DT>(acc.z, acc.w)};
+    }
+}
+
+// ---- one token, forward, in one launch
+//
+// k_nf4_gemv16's waves of one 16-row group as one workgroup, a wave per part: the
+// parts meet in LDS, where the first lanes add them in part order (the same sums)
+// and apply the epilogue, and the second launch and the partials' traffic are
+// saved.  Each wave stages its own slice of x.  Taken where all its workgroups are
+// on the chip at once (two launches -> one, one token with an adapter of rank 16:
+// 13824 x 5120 18.3 -> 15.4 us, 4096 x 4096 11.3 -> 8.1, 2048 x 8192 12.5 -> 11.6);
+// past that a second round costs more than the launch (5120 x 13824 in 14 parts
+// 19.6 -> 19.9, 32000 x 1024 in one 11.3 -> 14.0).
+constexpr int kGoWaves = 16;   // parts at most
+
+template <int DT, bool DQ, bool OUT_F32, class E>
+__global__ __launch_bounds__(64 * kGoWaves, 4) void k_nf4_gemv1(GemvArgs g, void* out, E e)
+{
+    __shared__ float s_lv[16];
+    __shared__ __attribute__((aligned(16))) float s_acc[kGoWaves][16];
+    __shared__ __attribute__((aligned(16))) uint16_t s_xs[kGoWaves][kGvMaxSc * 128];
+    const int t = threadIdx.x, lane = t & 63, parts = blockDim.x >> 6;
+    const int part = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * 16, n = n0 + (lane & 15);
+    const int s0 = part * g.part_sc, ns = min(g.part_sc, (int)(g.cols / 128) - s0);
+    const int kg = lane >> 4;
+    // as in k_nf4_gemv16: every load unconditional and in bounds, x first
+    u32x4 xv[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        xv[i] = *(const GLOBAL u32x4*)((const GLOBAL uint16_t*)g.x + (int64_t)s0 * 128 + 8 * min(lane + 64 * i, ns * 16 - 1));
+    GvSlab<DQ, kGvMaxSc> w;
+    w.load(g, n, s0, ns, kg);
+    if (t == 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s_lv[i] = as_f(nf4fmt::kLevelBits[i]);
+    }
+    uint16_t* xs = s_xs[part];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *(u32x4*)(xs + 8 * (lane + 64 * i)) = xv[i];
+    __syncthreads();
+    typedef typename Frag8<DT>::T F;
+    f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};   // of row 0: the other lanes' rows repeat it
+#pragma unroll
+    for (int sc = 0; sc < kGvMaxSc; ++sc) {
+        if (sc >= ns) break;
+        const float adq = w.absmax(sc);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const u32x4 b = gv_deq8<DT>(w.cw[sc][j], adq, s_lv);
+            const u32x4 a = *(const u32x4*)(xs + 32 * kg + 128 * sc + 8 * j);
+            acc = mfma16<DT>(__builtin_bit_cast(F, a), __builtin_bit_cast(F, b), acc);
+        }
+    }
+    if constexpr (E::kOn) {
+        if (e.a.u && part == 0) gv_low_rank<DT>(e.a, n, 0, kg, acc);
+    }
+    if (kg == 0) s_acc[part][lane] = acc.x;
+    __syncthreads();
+    if (t >= 4) return;
+    f32x4 z = *(const f32x4*)&s_acc[0][4 * t];
+    for (int p = 1; p < parts; ++p) z += *(const f32x4*)&s_acc[p][4 * t];
+    store_sum<DT, OUT_F32>(e, z, n0 + 4 * t, n0 + 4 * t, out);
 }
 
 // The fp32 partials of the splits added in split order (fixed, so the result
@@ -1747,20 +1876,8 @@ __global__ __launch_bounds__(256) void k_splitk_sum(const float* __restrict__ pa
     typedef float f4 __attribute__((ext_vector_type(4)));
     f4 acc = *(const GLOBAL f4*)(part + i);
     for (int sp = 1; sp < nsplit; ++sp) acc += *(const GLOBAL f4*)(part + (int64_t)sp * n + i);
-    if constexpr (E::kOn) {
-        // n / 4 is below 2^32 (the grid's limit)
-        const uint32_t i4 = (uint32_t)(i >> 2);
-        float z[4] = {acc.x, acc.y, acc.z, acc.w}, bias[4];
-        load_bias<DT, 4>(e.a, (int64_t)(i4 % (uint32_t)(ncol >> 2)) * 4, bias);
-        float res[4];
-        load_residual<DT, OUT_F32, 4>(e.a, i, res);
-        finish<DT, true, OUT_F32, false, 4>(e.a, z, bias, res, i, out);
-    } else if constexpr (OUT_F32) {
-        *(GLOBAL f4*)((float*)out + i) = acc;
-    } else {
-        const u32x2 v = {pack16<DT>(acc.x, acc.y), pack16<DT>(acc.z, acc.w)};
-        *(GLOBAL u32x2*)((uint16_t*)out + i) = v;
-    }
+    // n / 4 is below 2^32 (the grid's limit)
+    store_sum<DT, OUT_F32>(e, acc, i, (int64_t)((uint32_t)(i >> 2) % (uint32_t)(ncol >> 2)) * 4, out);
 }
 
 // The tail splits' fp32 partials of each leftover tile added in split order
@@ -1781,18 +1898,7 @@ __global__ __launch_bounds__(256) void k_tail_sum(GemmArgs g, E ep)
     f4 acc = *(const GLOBAL f4*)p;
     for (int sp = 1; sp < g.tail_split; ++sp) acc += *(const GLOBAL f4*)(p + (int64_t)sp * g.nhalf * (kXM * kXN));
     const int64_t i = row * g.ldo + col;
-    if constexpr (E::kOn) {
-        float z[4] = {acc.x, acc.y, acc.z, acc.w}, bias[4];
-        load_bias<DT, 4>(ep.a, col, bias);
-        float res[4];
-        load_residual<DT, OUT_F32, 4>(ep.a, i, res);
-        finish<DT, true, OUT_F32, false, 4>(ep.a, z, bias, res, i, g.out);
-    } else if constexpr (OUT_F32) {
-        *(GLOBAL f4*)((float*)g.out + i) = acc;
-    } else {
-        const u32x2 v = {pack16<DT>(acc.x, acc.y), pack16<DT>(acc.z, acc.w)};
-        *(GLOBAL u32x2*)((uint16_t*)g.out + i) = v;
-    }
+    store_sum<DT, OUT_F32>(ep, acc, i, col, g.out);
 }
 
 // One-shot launches of at most 2^32 / 256 - 1 workgroups each.
@@ -2077,9 +2183,16 @@ inline int gemv_part_sc(int64_t rows, int64_t cols, int mb)
 
 inline int gemv_blocks(int64_t m) { return m <= 16 ? 1 : 2; }
 
+// Workgroups of k_nf4_gemv1 that a CU holds: 34 KB of LDS each, six waves a SIMD.
+inline int64_t gemv1_per_cu(int parts) { return parts > 6 ? 24 / parts : 4; }
+
 template <int DT, bool DQ, bool OUT_F32, class E>
 hipError_t gemv_go(const GemvArgs& g, const E& ep, int parts, void* out, hipStream_t s)
 {
+    if (g.m == 1 && parts <= kGoWaves && g.groups <= kPlanCus * gemv1_per_cu(parts)) {
+        hipLaunchKernelGGL((k_nf4_gemv1<DT, DQ, OUT_F32, E>), dim3((unsigned)g.groups), dim3(64u * parts), 0, s, g, out, ep);
+        return hipGetLastError();
+    }
     const int64_t blocks = (g.groups + 3) / 4;
     if (blocks > kMaxGemmGrid || parts > 65535) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks, (unsigned)parts);

@@ -474,6 +474,33 @@ def test_linear_empty_epilogue_is_the_matmul():
         assert torch.equal(out, want), (back, m)
 
 
+# parts of the reduction (its super-chunks of 128): one (1), two (8 + 1), three (8 + 8 + 1), five (2 x 4 + 1), nine, nine
+# (4 x 8 + 1), sixteen, and one of more workgroups than the chip holds at once
+@pytest.mark.parametrize("rows,cols", [(128, 128), (16384, 1152), (16384, 2176), (8192, 1152), (1024, 1152), (4096, 4224),
+                                       (2048, 8192), (32768, 384)])
+@pytest.mark.parametrize("dtype,dq,f32", [(torch.bfloat16, True, False), (torch.float16, False, True)], ids=["dq", "plain"])
+def test_linear_single_token(rows, cols, dtype, dq, f32):
+    print_case("nf4_linear single token", dtype, rows, cols)
+    W = Weight(rows, cols, dtype, dq, seed=rows + cols)
+    c = Case(W, 1, 40, False, act="silu", bias=True, residual=True, out_f32=f32, seed=3)
+    out, pre = c.run(preact=True)
+    c.check(out, pre)
+    assert torch.equal(c.run(inplace=True), out)
+    # as the first of two tokens, the other one not finite: the same bits
+    two = Case(W, 2, 40, False, act="silu", bias=True, residual=True, out_f32=f32, seed=4)
+    two.x[0], two.lora[0][0], two.res[0] = c.x[0], c.lora[0][0], c.res[0]
+    two.x[1] = float("nan")
+    two.lora = (two.lora[0], c.lora[1])
+    two.bias = c.bias
+    both, pre2 = two.run(preact=True)
+    assert torch.equal(both[0], out[0]) and torch.equal(pre2[0], pre[0]) and torch.isnan(both[1]).all()
+    # and without an epilogue, as the matmul
+    bare = Case(W, 1, 0, False, out_f32=f32, seed=3)
+    want = torch.empty(1, rows, dtype=out.dtype, device="cuda")
+    q.nf4_matmul_ws(W.layer, rows, cols, W.f, bare.x, want, workspace(q.nf4_matmul_workspace_bytes(rows, cols, False, 1)))
+    assert torch.equal(bare.run(), want)
+
+
 def test_linear_one_dimensional_token():
     W = Weight(256, 128, torch.bfloat16, True, 5)
     c = Case(W, 1, 8, False, act="silu", residual=True)
