@@ -450,6 +450,11 @@ __global__ __launch_bounds__(64 * kProjWaves) void k_lora_project(ProjArgs g)
                 for (int j = 0; j < RT; ++j) d[j] = f[j] = w[s * RT + j];
                 if constexpr (TILE) transpose_tile<RT, V>(d, tile, f);
             }
+            // k past the end: zeros on both sides (an infinite last weight times zero would be NaN)
+            const bool past = over && 32 * s + 8 * kg >= 64 - over;
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+                if (past) f[j] = u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
                 u32x4 a = x[s][b];
@@ -458,7 +463,7 @@ __global__ __launch_bounds__(64 * kProjWaves) void k_lora_project(ProjArgs g)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) a[j] = keep2(a[j], bits.w[j], g.drop.thr);
                 }
-                if (over && 32 * s + 8 * kg >= 64 - over) a = u32x4{0, 0, 0, 0};
+                if (past) a = u32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int j = 0; j < RT; ++j) acc[b][j] = mfma<DT>(a, f[j], acc[b][j]);
             }
@@ -600,7 +605,19 @@ __global__ __launch_bounds__(64 * kGradWaves<RT>) void k_lora_grad(GradArgs g)
                 // two generator calls at a time: more of them interleaved spill beside 64 ranks of sums
                 if (RT == 4 && (i & 1)) __builtin_amdgcn_sched_barrier(0);
             }
-            if (row >= s1) x[i] = u32x4{0, 0, 0, 0};
+        }
+        // rows past the end: zeros on both sides (an infinite last u times zero would be NaN)
+        if (m0 + 32 > s1) {
+            const int left = (int)(s1 - m0) - 8 * mg;   // of this lane's eight rows
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= left) x[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t keep = left > 2 * i + 1 ? 0xffffffffu : left > 2 * i ? 0xffffu : 0u;
+#pragma unroll
+                for (int j = 0; j < RT; ++j) a[j][i] &= keep;
+            }
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {

@@ -233,6 +233,18 @@ def test_project_masks_as_dropout_does():
     assert torch.equal(h, h2)
 
 
+@pytest.mark.parametrize("back", [False, True], ids=["fwd", "bwd"])
+@pytest.mark.parametrize("k,r", [(8, 16), (136, 16), (136, 4), (136, 5), (1000, 40), (552, 64)])
+def test_project_infinite_last_weight(back, k, r):
+    """Lengths that end inside a step: an infinite weight in the last place stays an infinity."""
+    x = draw((37, k), torch.bfloat16, 1).abs().cuda() + 0.5
+    w = draw((k, r) if back else (r, k), torch.bfloat16, 2).cuda()
+    (w if back else w.t())[k - 1, r - 1] = float("-inf")
+    h = torch.empty(37, r, dtype=torch.bfloat16, device="cuda")
+    q.nf4_lora_project(x, w, h, backward=back)
+    assert (h[:, r - 1] == float("-inf")).all() and h[:, :r - 1].isfinite().all()
+
+
 def test_project_past_32_bit_offsets():
     """(2^19 + 5) x 8192: the last rows' mask and product, against the 64-bit form."""
     m, k, r, p = (1 << 19) + 5, 8192, 8, 0.5
@@ -270,6 +282,20 @@ def test_lora_grad(dtype, side, p, m, n, r):
     g2 = torch.empty_like(grad)
     q.nf4_lora_grad(u.cuda(), x.cuda(), g2, workspace(need), side=side, p=p, rng=rng() if p else None)
     assert torch.equal(grad, g2)
+
+
+@pytest.mark.parametrize("side", ["A", "B"])
+@pytest.mark.parametrize("m,n,r", [(1, 8, 16), (33, 136, 16), (47, 128, 4), (1999, 64, 64), (550, 264, 5)])
+def test_lora_grad_infinite_last_token(side, m, n, r):
+    """Token counts that end inside a step: an infinity in the last token stays one, in u or in x."""
+    for of_u in (True, False):
+        u = draw((m, r), torch.float16, 1).abs().cuda() + 0.5
+        x = draw((m, n), torch.float16, 2).abs().cuda() + 0.5
+        (u if of_u else x)[m - 1, 0] = float("inf")
+        grad = torch.empty((r, n) if side == "A" else (n, r), device="cuda")
+        q.nf4_lora_grad(u, x, grad, workspace(q.nf4_lora_grad_workspace_bytes(m, n, r)), side=side)
+        rows = grad if (side == "A") == of_u else grad.t()
+        assert (rows[0] == float("inf")).all() and rows[1:].isfinite().all()
 
 
 def test_lora_grad_past_32_bit_offsets():
