@@ -378,7 +378,12 @@ nf4_status nf4_matmul_ws(const nf4_layer* w, int64_t rows, int64_t cols, nf4_for
  * (e / 8, offset), 64 bits each with the low word first, and key seed; it is
  * kept iff that lane >= t, t = p in units of 2^-16 (nearest).  1 - p is taken
  * as (65536 - t) / 65536, so that the mean is kept.  A dropped element is 0
- * whatever x holds. */
+ * whatever x holds.
+ *
+ * Unlike the codec, these calls define what a value that is not finite does:
+ * operands of the products and sums as fp32 arithmetic has it (a dropped element
+ * counts as 0, padding never counts), and a NaN preactivation gives NaN in out,
+ * dz and dbias with every activation that reads it. */
 typedef struct {
     const uint64_t* rng;   /* device {seed, offset}, 8-byte aligned, read in stream order; unused when p is 0 */
     float           p;     /* drop probability, 0 <= p <= 65535/65536                                         */

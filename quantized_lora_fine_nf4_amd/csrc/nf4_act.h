@@ -9,7 +9,8 @@
 //                                        slope S + z S (1 - S) 2 t'(z)
 // The slopes are taken at z limited to +-100, beyond which every one of them
 // has reached its limit in fp32, so an infinite z (a 16-bit preactivation that
-// overflowed) gives the limit and not inf * 0.
+// overflowed) gives the limit and not inf * 0.  A NaN stays NaN in every value
+// and slope, so that a run that has diverged shows it.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -22,7 +23,12 @@ enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GEL
 // relative error is about |x| 2^-24 (each function's argument is limited).
 __device__ __forceinline__ float act_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
-__device__ __forceinline__ float act_limit(float z) { return __builtin_amdgcn_fmed3f(z, -100.0f, 100.0f); }
+// +-100 at most.  The maximum and minimum that keep a NaN: the three-way median
+// of one is its lower limit.
+__device__ __forceinline__ float act_limit(float z)
+{
+    return __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -100.0f), 100.0f);
+}
 
 // S(x); exp overflows to inf below -88.7 and the reciprocal gives 0.
 __device__ __forceinline__ float act_sigmoid(float x)
@@ -57,7 +63,7 @@ constexpr float kTanhK = 1.59576912160573081f;   // 2 sqrt(2/pi)
 __device__ __forceinline__ float act_value(float z, int act)
 {
     switch (act) {
-        case ACT_RELU: return z > 0.0f ? z : 0.0f;
+        case ACT_RELU: return __builtin_elementwise_maximum(z, 0.0f);
         case ACT_SILU: return z * act_sigmoid(z);
         case ACT_GELU: {
             float e;
@@ -75,7 +81,7 @@ __device__ __forceinline__ float act_slope(float zin, int act)
 {
     const float z = act_limit(zin);
     switch (act) {
-        case ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+        case ACT_RELU: return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
         case ACT_SILU: {
             const float s = act_sigmoid(z);
             return s * fmaf(z, 1.0f - s, 1.0f);
