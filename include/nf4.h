@@ -383,7 +383,8 @@ nf4_status nf4_matmul_ws(const nf4_layer* w, int64_t rows, int64_t cols, nf4_for
  * Unlike the codec, these calls define what a value that is not finite does:
  * operands of the products and sums as fp32 arithmetic has it (a dropped element
  * counts as 0, padding never counts), and a NaN preactivation gives NaN in out,
- * dz and dbias with every activation that reads it. */
+ * dz and dbias with every activation that reads it, an infinite one their limits
+ * (act: infinity and 0, act': 1 and 0). */
 typedef struct {
     const uint64_t* rng;   /* device {seed, offset}, 8-byte aligned, read in stream order; unused when p is 0 */
     float           p;     /* drop probability, 0 <= p <= 65535/65536                                         */

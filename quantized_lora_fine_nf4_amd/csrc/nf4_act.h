@@ -9,7 +9,7 @@
 //                                        slope S + z S (1 - S) 2 t'(z)
 // The slopes are taken at z limited to +-100, beyond which every one of them
 // has reached its limit in fp32, so an infinite z (a 16-bit preactivation that
-// overflowed) gives the limit and not inf * 0.  A NaN stays NaN in every value
+// overflowed) gives the limit and not inf * 0; the values do so too.  A NaN stays NaN in every value
 // and slope, so that a run that has diverged shows it.
 #pragma once
 #include <hip/hip_runtime.h>
@@ -19,8 +19,9 @@ namespace nf4k {
 
 enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 
-// e^x: 2^t is within a step, t = x log2(e) within half a step of |t|, so the
-// relative error is about |x| 2^-24 (each function's argument is limited).
+// e^x: 2^t is within a step, t = x log2(e) within a step of |t| (log2(e) rounded,
+// then the product), so the relative error is about |x| 2^-23; 0 below 2^-126,
+// infinite past the largest fp32.
 __device__ __forceinline__ float act_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 // +-100 at most.  The maximum and minimum that keep a NaN: the three-way median
@@ -30,11 +31,13 @@ __device__ __forceinline__ float act_limit(float z)
     return __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -100.0f), 100.0f);
 }
 
-// S(x); exp overflows to inf below -88.7 and the reciprocal gives 0.
-__device__ __forceinline__ float act_sigmoid(float x)
-{
-    return __builtin_amdgcn_rcpf(1.0f + act_exp(-__builtin_amdgcn_fmed3f(x, -88.0f, 88.0f)));
-}
+// S(x): 0 below -88.7, where exp overflows, and 1 at +infinity.  Below -87.3 S is
+// less than the least normal fp32 and the reciprocal gives 0 as well.
+__device__ __forceinline__ float act_sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + act_exp(-x)); }
+
+// The z that a value's factor S or P multiplies: both are 0 at -100, so the value
+// reaches its limit 0 at -infinity and not inf * 0.
+__device__ __forceinline__ float act_floor(float z) { return __builtin_elementwise_maximum(z, -100.0f); }
 
 // P(z) and e = exp(-z^2/2): for z < 0, P(z) = e Q(t) / 2 with t = 1 / (1 + p
 // |z| / sqrt 2), Q(t) = erfc(x) exp(x^2) at x = |z| / sqrt 2 as a polynomial
@@ -42,9 +45,8 @@ __device__ __forceinline__ float act_sigmoid(float x)
 // relative error over 0 <= x <= 14.2 (2.6e-8; 3.6e-7 as evaluated in fp32).
 __device__ __forceinline__ float act_normal(float z, float& e)
 {
-    const float a = act_limit(z);
-    e = act_exp(-0.5f * a * a);
-    const float t = __builtin_amdgcn_rcpf(fmaf(__builtin_fabsf(a), 0.38f * 0.70710678118654752f, 1.0f));
+    e = act_exp(-0.5f * z * z);
+    const float t = __builtin_amdgcn_rcpf(fmaf(__builtin_fabsf(z), 0.38f * 0.70710678118654752f, 1.0f));
     float q = 0.05828981101512909f;
     q = fmaf(q, t, -0.2592635452747345f);
     q = fmaf(q, t, 0.3581995666027069f);
@@ -55,7 +57,7 @@ __device__ __forceinline__ float act_normal(float z, float& e)
     q = fmaf(q, t, 0.21395252645015717f);
     q = fmaf(q, t, 0.21440942585468292f);
     const float tail = 0.5f * e * (q * t);
-    return a < 0.0f ? tail : 1.0f - tail;
+    return z < 0.0f ? tail : 1.0f - tail;
 }
 
 constexpr float kTanhK = 1.59576912160573081f;   // 2 sqrt(2/pi)
@@ -64,14 +66,14 @@ __device__ __forceinline__ float act_value(float z, int act)
 {
     switch (act) {
         case ACT_RELU: return __builtin_elementwise_maximum(z, 0.0f);
-        case ACT_SILU: return z * act_sigmoid(z);
+        case ACT_SILU: return act_floor(z) * act_sigmoid(z);
         case ACT_GELU: {
             float e;
-            return z * act_normal(z, e);
+            return act_floor(z) * act_normal(z, e);
         }
         case ACT_GELU_TANH: {
-            const float c = act_limit(z);
-            return z * act_sigmoid(kTanhK * fmaf(0.044715f * c, c * c, c));
+            const float c = act_floor(z);
+            return c * act_sigmoid(kTanhK * fmaf(0.044715f * c, c * c, c));
         }
         default: return z;
     }
@@ -79,9 +81,9 @@ __device__ __forceinline__ float act_value(float z, int act)
 
 __device__ __forceinline__ float act_slope(float zin, int act)
 {
+    if (act == ACT_RELU) return zin > 0.0f ? 1.0f : zin != zin ? zin : 0.0f;
     const float z = act_limit(zin);
     switch (act) {
-        case ACT_RELU: return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
         case ACT_SILU: {
             const float s = act_sigmoid(z);
             return s * fmaf(z, 1.0f - s, 1.0f);

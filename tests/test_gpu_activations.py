@@ -96,3 +96,24 @@ def test_nan_token_reaches_its_outputs_and_gradients(act, m):
     for t in (out, pre, dz):
         assert torch.isnan(t[rows]).all() and torch.isfinite(t[~rows]).all()
     assert torch.isnan(db).all()
+
+
+# ---- infinities ------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DT, ids=IDS)
+@pytest.mark.parametrize("act", ACTS[1:])
+@pytest.mark.parametrize("m", [1, 40, 300])
+def test_infinite_preactivation_gives_the_limit(dtype, act, m):
+    """out is infinite at +infinity and 0 at -infinity and at the type's lowest value, as the slopes there are 1 and 0
+    for the gradient."""
+    print_case("infinite preactivations", dtype, act, m)
+    inf, big = float("inf"), torch.finfo(dtype).max
+    bias = torch.tensor([inf, -inf, big, -big] * 64, dtype=dtype)
+    for out_dtype in (dtype, torch.float32):
+        out, pre = forward(bias, act, m, out_dtype)
+        want = torch.tensor([inf, 0.0, big, 0.0] * 64, dtype=out_dtype).expand(m, 256)
+        assert torch.equal(pre, bias.expand(m, 256))
+        assert torch.equal(out, want), out[0, :4]
+    dz, db = gradient(bias[None], act)
+    want = torch.tensor([[1.0, 0.0, 1.0, 0.0] * 64])
+    assert torch.equal(dz.float(), want) and torch.equal(db[None], want)
