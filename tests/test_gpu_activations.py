@@ -1,9 +1,12 @@
 """The activations of nf4_linear and their slopes in nf4_act_grad at every value of a 16-bit type."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import quantized_lora_fine_nf4_amd as q
+from adapted_ref import TINY, U16, U32
 from conftest import print_case
 
 pytestmark = pytest.mark.gpu
@@ -117,3 +120,105 @@ def test_infinite_preactivation_gives_the_limit(dtype, act, m):
     dz, db = gradient(bias[None], act)
     want = torch.tensor([[1.0, 0.0, 1.0, 0.0] * 64])
     assert torch.equal(dz.float(), want) and torch.equal(db[None], want)
+
+
+# ---- accuracy, tails included ----------------------------------------------
+#
+# Bounds in half steps u = 2^-24 of fp32, to first order (the factor 1.01 covers the second).  Of its own result the
+# hardware's 2^t and reciprocal are within a step (2 u).
+#   e^x: log2(e) and its product with x are rounded, so t is within 2 u |t| and e^x within (2 |x| + 2) u of itself.
+#   S(x) = 1 / (1 + e^-x): e^-x acts with the weight 1 - S; the sum is rounded (1 u), the reciprocal (2 u).
+#   P(z): z^2 / 2 is rounded once more, so e = e^(-z^2/2) is within (1.5 z^2 + 2) u.  For z < 0, P = e q(t) t / 2:
+#     t = 1 / (1 + c |z|) with three roundings in c, one of the sum and 2 u of the reciprocal, at most 6 u; q(t) t is
+#     erfc(x) e^(x^2), whose relative slope in t is at most 3 (x = 0), so 18 u; the polynomial's fit and evaluation 6 u;
+#     two products: (1.5 z^2 + 28) u of P.  For z >= 0 the same of 1 - P, and 1 u of P.
+#   tanh's argument x = K (z + 0.044715 z^3) has three roundings in the cubic term, and the sum's, K's and the product's:
+#     6 u of |x| more in the exponent than S has by itself.
+# Where S or e is below the least normal fp32 the kernel has 0.
+
+K_TANH = math.sqrt(8 / math.pi)
+LEAST = 2.0 ** -126
+
+
+def logistic(x, extra):
+    """(S, 1 - S, error of S) at x whose own error is `extra` u |x|."""
+    s, c = torch.special.expit(x), torch.special.expit(-x)
+    return s, c, s * (c * ((2 + extra) * x.abs() + 2) + 3) * U32 + LEAST
+
+
+def normal(z):
+    """(P, error of P) for the normal distribution function."""
+    p, other = torch.special.erfc(-z / math.sqrt(2)) / 2, torch.special.erfc(z / math.sqrt(2)) / 2
+    return p, torch.minimum(p, other) * (1.5 * z * z + 28) * U32 + (z >= 0) * p * U32 + LEAST
+
+
+def tanh_argument(z):
+    return K_TANH * (z + 0.044715 * z ** 3)
+
+
+def value(z, act):
+    """(act(z), bound); z below -100 counts as -100, where every factor is below 1e-43."""
+    if act == "relu":
+        return z.clamp(min=0), torch.zeros_like(z)
+    lo, c = z.clamp(min=-100), z.clamp(-100, 100)
+    if act == "gelu":
+        f, err = normal(c)
+    else:
+        f, _, err = logistic(c, 0) if act == "silu" else logistic(tanh_argument(c), 6)
+    return lo * f, lo.abs() * (err + f * U32)
+
+
+def slope(z, act):
+    """(act'(z), bound) with z limited to +-100, beyond which every slope is 0 or 1 within 1e-40."""
+    if act == "relu":
+        return (z > 0).double(), torch.zeros_like(z)
+    z = z.clamp(-100, 100)
+    if act == "silu":
+        s, c, err = logistic(z, 0)
+        inner = 1 + z * c
+        d = s * inner
+        # S through its derivative; 1 - S, the inner sum and the product rounded
+        return d, err * (1 + z * (c - s)).abs() + (s * z.abs() * c + s * inner.abs() + d.abs()) * U32
+    if act == "gelu":
+        p, err = normal(z)
+        density = z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        d = p + density
+        return d, err + density.abs() * (1.5 * z * z + 4) * U32 + d.abs() * U32 + z.abs() * LEAST
+    x = tanh_argument(z)
+    w = K_TANH * (1 + 3 * 0.044715 * z * z)   # x', five roundings
+    s, c, err = logistic(x, 6)
+    term = z * s * c * w
+    d = s + term
+    return d, err * (1 + z * w * (c - s)).abs() + (8 * term.abs() + d.abs()) * U32
+
+
+@pytest.mark.parametrize("dtype", DT, ids=IDS)
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_every_finite_value(dtype, act):
+    """act(z) and act'(z) of every finite 16-bit z in fp32 against the bounds above, and rounded once to 16 bits."""
+    print_case("every finite value", dtype, act)
+    z = every_value(dtype)
+    z[~torch.isfinite(z)] = 0
+    want, tol = value(z.double(), act)
+    out, _ = forward(z, act, 1, torch.float32)
+    excess = ((out[0].double() - want).abs() - 1.01 * tol).max().item()
+    assert excess <= 0, z[((out[0].double() - want).abs() - 1.01 * tol).argmax()]
+    out, _ = forward(z, act, 1, dtype)
+    assert ((out[0].double() - want).abs() <= 1.01 * tol + U16[dtype] * want.abs() + TINY[dtype]).all()
+    want, tol = slope(z.double(), act)
+    dz, db = gradient(z[None], act)
+    excess = ((db.double() - want).abs() - 1.01 * tol).max().item()
+    assert excess <= 0, z[((db.double() - want).abs() - 1.01 * tol).argmax()]
+    assert ((dz[0].double() - want).abs() <= 1.01 * tol + U16[dtype] * want.abs() + TINY[dtype]).all()
+
+
+def test_the_bounds_see_a_lost_tail():
+    """The bounds against forms that lose the tail: 0 below -5, and the logistic's argument cut at -20."""
+    z = every_value(torch.bfloat16)
+    z = z[torch.isfinite(z)].double()
+    for act in ACTS[2:]:
+        want, tol = value(z, act)
+        assert (want.abs() > 1.01 * tol)[(z < -5) & (z > -9)].all(), act
+    want, tol = value(z, "silu")
+    cut = z * torch.special.expit(z.clamp(min=-20))
+    assert ((cut - want).abs() > 1.01 * tol)[(z < -21) & (z > -80)].all()
