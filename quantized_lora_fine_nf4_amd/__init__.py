@@ -347,7 +347,8 @@ def nf4_storage_bytes_variant(n: int, v: nf4_variant) -> int:
 # Unlike the codec calls, these take their shapes from the tensors, so they
 # check them: what does not fit raises NF4Error with NF4_E_ARG (or the status
 # the C call returns) and enqueues nothing.  Work goes to the current stream of
-# the tensors' device, or to `stream`, which must be one of that device's.
+# the tensors' device, or to `stream`, which must be one of that device's (of a
+# torch stream this is checked; an address is taken as it is).
 
 def _misfit(where: str, what: str):
     e = NF4Error(NF4_E_ARG, where)
@@ -403,6 +404,8 @@ def _enqueue(name: str, dev: int, stream, *args) -> None:
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev) without the Stream object
     else:
+        if getattr(stream, "device_index", dev) != dev:
+            _misfit(name, f"the stream must be one of device {dev}, got {stream}")
         s = _stream(stream)
     fn = getattr(_lib or lib(), name)
     if dev == torch.cuda.current_device():

@@ -230,3 +230,30 @@ def test_binding_checks_shapes_types_and_devices():
     assert "bias" in lin(b(3, 256), b(3, 128), bias=b(256))
     assert "preact" in lin(b(3, 256), f32(3, 128), preact=f32(3, 128))
     assert "residual" in lin(b(3, 256), f32(3, 128), residual=b(3, 128))
+
+
+class _Stream:
+    """What the binding reads of a torch stream."""
+
+    def __init__(self, device_index):
+        self.device_index, self.cuda_stream = device_index, 0
+
+
+def test_binding_refuses_a_stream_of_another_device(monkeypatch):
+    """Before the library is called; a stream of the tensors' device and a bare address pass on to it."""
+    calls = []
+
+    class Lib:
+        def nf4_status_str(self, st):
+            return b"bad argument"
+
+        def nf4_dropout(self, *a):
+            calls.append(a)
+            return q.NF4_OK
+    monkeypatch.setattr(q, "_lib", Lib())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert "device 1" in _bad(q._enqueue, "nf4_dropout", 1, _Stream(0))
+    assert not calls
+    q._enqueue("nf4_dropout", 1, _Stream(1), 5)
+    q._enqueue("nf4_dropout", 1, 77, 6)
+    assert calls == [(5, 0), (6, 77)]
