@@ -402,7 +402,9 @@ def _enqueue(name: str, dev: int, stream, *args) -> None:
     if dev < 0:
         _misfit(name, "tensors must be on the GPU")
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev) without the Stream object
+        # current_stream(dev) without the Stream object, where this torch offers it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        s = raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
     else:
         if getattr(stream, "device_index", dev) != dev:
             _misfit(name, f"the stream must be one of device {dev}, got {stream}")

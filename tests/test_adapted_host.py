@@ -257,3 +257,19 @@ def test_binding_refuses_a_stream_of_another_device(monkeypatch):
     q._enqueue("nf4_dropout", 1, _Stream(1), 5)
     q._enqueue("nf4_dropout", 1, 77, 6)
     assert calls == [(5, 0), (6, 77)]
+
+
+def test_binding_finds_the_current_stream_by_torchs_public_call(monkeypatch):
+    """A torch without the raw accessor, which is not of its public interface."""
+    calls = []
+
+    class Lib:
+        def nf4_dropout(self, *a):
+            calls.append(a)
+            return q.NF4_OK
+    monkeypatch.setattr(q, "_lib", Lib())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: _Stream(dev))
+    q._enqueue("nf4_dropout", 1, None, 5)
+    assert calls == [(5, 0)]
