@@ -552,6 +552,30 @@ def test_linear_dropped_low_rank_values_add_nothing():
         assert torch.isinf(out[k, 7]).all() and torch.equal(out[~k, 7], base[~k, 7])
 
 
+# rows, cols, m and the workspace in bytes that shows the plan: 256 x 256 tiles split in two (16 k-steps each; 128 x 128
+# tiles would be split in sixteen), whole (more than 256 tiles of 128 x 128, a reduction too short to split), and whole
+# with the leftover tiles split (320 tiles, 64 of them in four splits of 256 x 256 partials)
+@pytest.mark.parametrize("rows,cols,m,need", [(2048, 128, 300, 2 * 300 * 128 * 4), (256, 9216, 1000, 0),
+                                              (4096, 4992, 3900, 4 * 64 * 256 * 256 * 4)], ids=["split", "whole", "tail"])
+@pytest.mark.parametrize("r", [8, 72])
+def test_large_tiles_dropped_low_rank_values_add_nothing(rows, cols, m, need, r):
+    """Infinite adapter columns in the 256 x 256 kernels' own store: kept elements are infinite, dropped ones the
+    product alone."""
+    print_case("dropped infinities, large tiles", rows, cols, m, r)
+    assert q.nf4_matmul_workspace_bytes(rows, cols, True, m) == need
+    W = Weight(rows, cols, torch.bfloat16, True, 5)
+    c = Case(W, m, r, True, p=0.5, out_f32=True)
+    at = [7, 64, cols - 1]
+    c.lora[0][:] = 1.0
+    c.lora[1][:, at] = 1e38
+    out = c.run()
+    plain = Case(W, m, 0, True, out_f32=True)
+    plain.x = c.x
+    base = plain.run()
+    k = ref.mask((m, cols), 0.5, SEED, OFFSET)[:, at].bool().cuda()
+    assert torch.isinf(out[:, at][k]).all() and torch.equal(out[:, at][~k], base[:, at][~k])
+
+
 # ---- together --------------------------------------------------------------
 
 class Layer:
