@@ -339,7 +339,8 @@ nf4_status nf4_matmul(const nf4_layer* w, int64_t rows, int64_t cols, nf4_format
  * m <= 32 takes a kernel of its own with the same contract: one wave per 16
  * weight rows and part of the reduction (parts of at most 1024 k, 512 k
  * above 16 tokens), fp32 partials in ws added in part order by the same
- * second kernel.  Where the output tiles fill the GPU but leave a last round
+ * second kernel; with m = 1, where the chip holds all workgroups at once, by the
+ * first one, to the same bits and without writing ws.  Where the output tiles fill the GPU but leave a last round
  * at most half full (e.g. 4096 tokens through a 13824 x 5120 weight: 320
  * tiles of 256 x 256 on 256 compute units), the whole rounds run unsplit and
  * each leftover tile's reduction is split floor(256 / leftover) ways (at most
@@ -362,7 +363,7 @@ nf4_status nf4_matmul_ws(const nf4_layer* w, int64_t rows, int64_t cols, nf4_for
  *   dB  = dz^T h,  dA = dh^T drop(x)             nf4_lora_grad
  *   dx  = dz W + drop(dh A) + residual           nf4_linear, backward
  * with A [rank x cols], B [rows x rank] and x [m x cols], all row-major.  1 <=
- * rank <= 128.  16-bit operands are bf16 or fp16, products and sums fp32, each
+ * rank <= 128 (above: NF4_E_UNSUPPORTED).  16-bit operands are bf16 or fp16, products and sums fp32, each
  * 16-bit result rounded once (nearest even).  Every result is the same from
  * run to run; sums over a split axis are added in a fixed order.  Nothing is
  * kept between calls: calls that share no buffer may overlap, and every call
@@ -426,23 +427,25 @@ nf4_status nf4_linear(const nf4_layer* w, int64_t rows, int64_t cols, nf4_format
  *   dy, preact, dz  device [m x n] of dtype, 16-byte aligned; dz may be dy
  *   dbias           device fp32 [n], 16-byte aligned, or NULL
  * NF4_ACT_NONE: preact is not read and may be NULL, and so may dz (dbias
- * alone).  n < 2^26, a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25.  ws:
- * nf4_act_grad_workspace_bytes(m, n) with dbias, else unused. */
+ * alone).  1 <= m <= 2^25, n < 2^26 (else NF4_E_ARG), n a multiple of 8 (else
+ * NF4_E_UNSUPPORTED).  ws: nf4_act_grad_workspace_bytes(m, n) with dbias, else
+ * unused. */
 nf4_status nf4_act_grad(const void* dy, const void* preact, int32_t act, int64_t m, int64_t n,
                         int32_t dtype, void* dz, float* dbias, void* ws, size_t ws_bytes,
                         hipStream_t stream);
 
 /* out = drop(x) over n elements of dtype, rounded once.  x and out 16-byte
  * aligned; out may be x.  Its own gradient is the same call on the gradient.
- * 1 <= n < 2^36. */
+ * 1 <= n < 2^36 (2^36 or more: NF4_E_UNSUPPORTED). */
 nf4_status nf4_dropout(const void* x, int64_t n, int32_t dtype, nf4_drop drop, void* out,
                        hipStream_t stream);
 
 /* The adapter's down product and its gradient's counterpart, rounded once:
  *   backward 0: h[m x rank] = scale drop(x) w^T, x [m x k], w [rank x k]  (h = s drop(x) A^T)
  *   backward 1: h[m x rank] = scale x w,         x [m x k], w [k x rank]  (dh = s dz B)
- * k < 2^26, a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25; device
- * buffers of dtype, 16-byte aligned.  Dropout with backward 1: NF4_E_UNSUPPORTED. */
+ * 1 <= m <= 2^25, k < 2^26 (else NF4_E_ARG), k a multiple of 8 (else
+ * NF4_E_UNSUPPORTED); device buffers of dtype, 16-byte aligned.  Dropout with
+ * backward 1: NF4_E_UNSUPPORTED. */
 nf4_status nf4_lora_project(const void* x, int64_t m, int64_t k, const void* w, int32_t rank,
                             int32_t dtype, int32_t backward, float scale, nf4_drop drop, void* h,
                             hipStream_t stream);
@@ -452,9 +455,9 @@ typedef enum { NF4_LORA_A = 0, NF4_LORA_B = 1 } nf4_lora_side;
 /* The adapter's weight gradients, fp32:
  *   side NF4_LORA_A: grad[rank x n] = u^T drop(x)   (dA, u = dh, x the layer's input)
  *   side NF4_LORA_B: grad[n x rank] = x^T u         (dB, u = h, x = dz)
- * u [m x rank] and x [m x n] of dtype, grad fp32, all 16-byte aligned; n < 2^26,
- * a multiple of 8 (else NF4_E_UNSUPPORTED), 1 <= m <= 2^25.  Dropout on side B:
- * NF4_E_UNSUPPORTED.  ws: nf4_lora_grad_workspace_bytes(m, n, rank), may be
+ * u [m x rank] and x [m x n] of dtype, grad fp32, all 16-byte aligned; 1 <= m <=
+ * 2^25, n < 2^26 (else NF4_E_ARG), n a multiple of 8 (else NF4_E_UNSUPPORTED).  Dropout on
+ * side B: NF4_E_UNSUPPORTED.  ws: nf4_lora_grad_workspace_bytes(m, n, rank), may be
  * NULL when that is 0. */
 nf4_status nf4_lora_grad(const void* u, const void* x, int64_t m, int64_t n, int32_t rank,
                          int32_t dtype, int32_t side, nf4_drop drop, float* grad, void* ws,

@@ -66,10 +66,11 @@ __device__ __forceinline__ uint16_t pack1(float a) { return (uint16_t)pack2<DT>(
 
 // ---- dropout
 //
-// Bound by memory: 4 bytes per element; 8192 x 13824 in 77 us, 5.9 TB/s (the
-// generator and the masks are about 45 vector instructions per eight elements,
-// 38 us of issue at that size).  One mask group (eight elements, 16 bytes) per
-// thread and step, four loads in flight.
+// Bound by memory: 4 bytes per element and no more (counted); 8192 x 13824 in 78
+// us, 5.8 TB/s.  The generator, the masks and the conversions are 80 vector
+// instructions per eight elements (counted), hidden but for 2 us: with
+// probability 0 the call takes 76.7.  One mask group (eight elements, 16 bytes)
+// per thread and step, four loads in flight.
 constexpr int kDropGroups = 4;   // groups per thread
 
 template <int DT>
@@ -341,8 +342,11 @@ __device__ __forceinline__ void gather_tile(const uint16_t* p, int64_t rows, int
 // sums are added pairwise in LDS.  x goes straight to fragments; W goes through
 // LDS, so that memory is read in whole 128-byte lines (fragments read straight
 // from its rows, 64 bytes each, took 1.5 times as long at rank 64).  Bound by
-// x's bytes at rank 16 (4096 x 5120 in 9.3 us, 4.5 TB/s; 4096 x 13824 backward
-// in 26 us), by the reads of W from the L2 above: every 16 or 32 rows read all of it.
+// x's bytes at rank 16 (4096 x 5120 in 10 us, 4.2 TB/s; 4096 x 13824 backward in
+// 26 us, 4.5 TB/s, its waves waiting 80% of their time).  Above, by the reads of
+// W from the L2, which every 16 or 32 rows read whole (8192 x 5120 rank 64: 168 MB
+// beside x's 84, 22 us; the mask's work is hidden, 22.5 us with dropout).  Ranks
+// over 64 are two groups that read x twice (4096 x 13824 rank 128: 57 us).
 enum ProjMode { PROJ_FWD, PROJ_DROP, PROJ_BACK8, PROJ_BACK4, PROJ_BACK_ANY };   // backward: pieces of W, or gathered
 
 struct ProjArgs {
@@ -541,8 +545,10 @@ __global__ __launch_bounds__(64 * kProjWaves) void k_lora_project(ProjArgs g)
 // n0 + 8 q + c, q = 0 .. 15.  A wave covers 128 columns and 16 RT ranks, the
 // W waves of a workgroup share its rows, and their sums are added in LDS.
 // Bound by x's bytes where the tokens are many (4096 x 13824 rank 8: 25 us with
-// the sum of the splits, 4.5 TB/s), by latency and the splits' partials where
-// they are few (4096 x 5120 rank 16: 12.4 us, rank 64: 18 us).  Loading the next
+// the sum of the splits, 4.5 TB/s).  Where they are few a wave has two to four
+// rounds of loads, none of them ahead, and waits half its time and more, and the
+// splits' partials count beside x (4096 x 5120 rank 16: 12.4 us; 1999 x 8192 rank
+// 64 13 us, 12.6 MB of partials written and read beside 35 MB).  Loading the next
 // rows ahead, in fewer waves, took 4 to 10% longer.
 struct GradArgs {
     const uint16_t* u;     // [m x rank]

@@ -41,8 +41,9 @@ __device__ __forceinline__ float act_floor(float z) { return __builtin_elementwi
 
 // P(z) and e = exp(-z^2/2): for z < 0, P(z) = e Q(t) / 2 with t = 1 / (1 + p
 // |z| / sqrt 2), Q(t) = erfc(x) exp(x^2) at x = |z| / sqrt 2 as a polynomial
-// without constant term: degree 9 and p = 0.38 from a least-maximum fit of the
-// relative error over 0 <= x <= 14.2 (2.6e-8; 3.6e-7 as evaluated in fp32).
+// without constant term (the form of Abramowitz and Stegun, Handbook of
+// Mathematical Functions, 7.1.26): degree 9 and p = 0.38 from a least-maximum fit
+// of the relative error over 0 <= x <= 14.2 (2.6e-8; 3.6e-7 as evaluated in fp32).
 __device__ __forceinline__ float act_normal(float z, float& e)
 {
     e = act_exp(-0.5f * z * z);

@@ -312,12 +312,15 @@ __device__ __forceinline__ void group_coords(int64_t tile, int64_t mtiles, int64
 // is 16 bytes, or in the kernel that adds the splits.  All of it is private to a
 // wave: no barrier.
 //
-// Cost on the 13824 x 5120 weight at 4096 tokens, beside 590-640 us for the
-// product alone: an empty epilogue nothing (its 16-byte stores make up for LDS),
-// rank 16 nothing, silu 0-10 us, gelu 10, a preactivation 0-10, a residual 20-30
-// (one 113 MB read, at the end of each round of tiles), dropout backward 10-15
-// (the generator).  With an epilogue the leftover tiles of a reduction too short
-// to split (k below 2,048) run whole instead of in row pieces.
+// Cost on the 13824 x 5120 weight at 4096 tokens over nf4_matmul_ws (one process,
+// 589-594 us forward, 592 backward): an empty epilogue 6 us forward and 9 backward
+// (the way through LDS), rank 16 14 and 15, silu 17, gelu 38, a preactivation 10,
+// a residual 56 and 28 (read at the end of each round of tiles), rank 16 under
+// dropout 22; rank 16, bias, silu and preactivation together 29 (5%), rank 16,
+// dropout and residual backward 39 (7%).  With an epilogue the leftover tiles of
+// a reduction too short to split (k below 2,048) run whole instead of in row
+// pieces: forward at 4096 tokens 13824 x 1024 165 us against 153 in pieces, 5120 x
+// 1920 131 against 102.
 struct NoEpi {
     static constexpr bool kOn = false, kDrop = false;
 };
@@ -1807,7 +1810,8 @@ __device__ __forceinline__ void store_sum(const E& e, const f32x4& acc, int64_t 
 // k_nf4_gemv16's waves of one 16-row group as one workgroup, a wave per part: the
 // parts meet in LDS, where the first lanes add them in part order (the same sums)
 // and apply the epilogue, and the second launch and the partials' traffic are
-// saved.  Each wave stages its own slice of x.  Taken where all its workgroups are
+// saved (3.5 VALU instructions and 1.1 LDS reads a weight, counted; k_nf4_gemv16
+// 3.7 and 1.2 up to 16 tokens).  Each wave stages its own slice of x.  Taken where all its workgroups are
 // on the chip at once (two launches -> one, one token with an adapter of rank 16:
 // 13824 x 5120 18.3 -> 15.4 us, 4096 x 4096 11.3 -> 8.1, 2048 x 8192 12.5 -> 11.6);
 // past that a second round costs more than the launch (5120 x 13824 in 14 parts
