@@ -463,7 +463,44 @@ nf4_status nf4_lora_grad(const void* u, const void* x, int64_t m, int64_t n, int
                          int32_t dtype, int32_t side, nf4_drop drop, float* grad, void* ws,
                          size_t ws_bytes, hipStream_t stream);
 
+/* ---- layer norm ----
+ *
+ * The norm in front of a layer, over the n values of each of m tokens:
+ *   h   = x + residual, rounded to dtype, written to total   (residual and
+ *         total: both, or both NULL and h = x)
+ *   out = (h - mean) rstd weight + bias, rstd = 1 / sqrt(variance + eps)
+ * with the variance the mean of (h - mean)^2.  x, residual, out, total device
+ * [m x n] of dtype, weight and bias [n] of dtype; stats device fp32 [m x 2],
+ * written with mean and rstd of every token.  Sums and statistics are fp32;
+ * out is rounded once.  out may be x (or residual), and total may be either;
+ * out and total are two buffers.  1 <= m <= 2^25, n < 2^26, 0 <= eps finite
+ * (else NF4_E_ARG), n a multiple of 8 (else NF4_E_UNSUPPORTED); all 16-byte
+ * aligned, stats 8.  A value that is not finite acts in its own token only. */
+nf4_status nf4_layer_norm(const void* x, const void* residual, const void* weight, const void* bias,
+                          int64_t m, int64_t n, int32_t dtype, float eps, void* out, void* total,
+                          float* stats, hipStream_t stream);
+
+/* Its gradient, from dy = dL/dout, the normalised values' source x (total,
+ * where nf4_layer_norm took a residual) and the forward call's stats:
+ *   g  = dy weight,  c = (x - mean) rstd
+ *   dx = rstd (g - mean(g) - c mean(g c)) + residual
+ *   dweight = sum over tokens of dy c,  dbias = sum over tokens of dy
+ * residual (NULL: none) is the gradient that reaches the sum past the norm.
+ * dy, x, residual, dx device [m x n] of dtype, dx rounded once; it may be dy,
+ * x or residual.  dweight, dbias device fp32 [n], overwritten, summed in a
+ * fixed order.  Limits as above, dweight and dbias 16-byte aligned.  ws:
+ * nf4_layer_norm_grad_workspace_bytes(m, n), 256-byte aligned, may be NULL
+ * where that is 0. */
+nf4_status nf4_layer_norm_grad(const void* dy, const void* x, const void* weight, const float* stats,
+                               const void* residual, int64_t m, int64_t n, int32_t dtype, void* dx,
+                               float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+
 /* ---- host-only helpers (pure; no HIP calls) ---- */
+
+/* fp32 partial column sums, two rows of n per workgroup; 0 where one workgroup
+ * does it, or on bad input. */
+size_t      nf4_layer_norm_grad_workspace_bytes(int64_t m, int64_t n);
 
 /* Workspaces of nf4_act_grad (fp32 partial column sums, one row per block of
  * tokens) and nf4_lora_grad (one fp32 partial gradient per split of the

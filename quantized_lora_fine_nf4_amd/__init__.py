@@ -11,6 +11,10 @@ missing library raises instead of falling back.
     nf4_linear, nf4_act_grad, nf4_dropout, nf4_lora_project, nf4_lora_grad
                                             -- one adapted layer, on the
                                                tensors' device
+    nf4_layer_norm, nf4_layer_norm_grad     -- the norm in front of a layer
+    mx4_quantize, mx4_dequantize, mx4_matmul, mx4_matmul4
+                                            -- microscaled 4-bit weights (C ABI:
+                                               ``include/mx4.h``)
     nf4_workspace_bytes, aqlora_workspace_bytes, nf4_storage_bytes,
     aqlora_promote_cost, nf4_levels, nf4_thresholds, nf4_abi_version
                                             -- host-only helpers
@@ -154,6 +158,27 @@ EXPORTS = {
     "nf4_last_hip_error": (ctypes.c_int32, []),
 }
 
+_P, _I32, _I64, _SZ, _ST = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+
+# The layer norm's part of nf4.h.
+EXPORTS.update({
+    "nf4_layer_norm": (_ST, [_P, _P, _P, _P, _I64, _I64, _I32, ctypes.c_float, _P, _P, _P, _P]),
+    "nf4_layer_norm_grad": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "nf4_layer_norm_grad_workspace_bytes": (_SZ, [_I64, _I64]),
+})
+
+# include/mx4.h, in the same library.
+MX4_EXPORTS = {
+    "mx4_quantize": (_ST, [_P, _I64, _I64, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "mx4_dequantize": (_ST, [_P, _P, _I64, _I64, _I32, _P, _P]),
+    "mx4_matmul": (_ST, [_P, _P, _I64, _I64, _I32, _I32, _P, _I64, _P, _I32, _P, _SZ, _P]),
+    "mx4_matmul4": (_ST, [_P, _P, _I64, _I64, _P, _P, _I64, _I32, _P, _I32, _P, _SZ, _P]),
+    "mx4_quantize_workspace_bytes": (_SZ, [_I64, _I64]),
+    "mx4_matmul_workspace_bytes": (_SZ, [_I64, _I64, _I32, _I64]),
+    "mx4_matmul4_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "mx4_storage_bytes": (_I64, [_I64, _I64]),
+}
+
 _lib = None
 
 
@@ -169,7 +194,7 @@ def lib() -> ctypes.CDLL:
             raise ImportError(f"{LIB_PATH} is missing: build it with "
                               "`python quantized_lora_fine_nf4_amd/build.py`")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in EXPORTS.items():
+        for name, (res, args) in (*EXPORTS.items(), *MX4_EXPORTS.items()):
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -536,6 +561,156 @@ def nf4_lora_grad(u, x, grad, ws=None, side: str = "A", p: float = 0.0, rng=None
 
 def nf4_lora_grad_workspace_bytes(m: int, n: int, rank: int) -> int:
     return int(lib().nf4_lora_grad_workspace_bytes(int(m), int(n), int(rank)))
+
+
+# ---- the layer norm -------------------------------------------------------
+
+def nf4_layer_norm(x, weight, bias, out, stats, eps: float = 1e-5, residual=None, total=None, stream=None) -> None:
+    """out = (h - mean) rstd weight + bias over the last axis, h = x, or total = x +
+    residual rounded to their type (residual and total: both or neither).  x,
+    residual, out, total [m, n], weight and bias [n], bfloat16 or float16; stats
+    float32 [m, 2], written with each token's mean and rstd."""
+    import torch
+    w = "nf4_layer_norm"
+    dt, dev, t16 = _dtype16(x, w), x.get_device(), x.dtype
+    if x.dim() != 2:
+        _misfit(w, "x must be [m, n]")
+    m, n = shape = x.shape
+    xp = _fits(x, "x", w, shape, t16, dev)
+    wp = _fits(weight, "weight", w, (n,), t16, dev)
+    bp = _fits(bias, "bias", w, (n,), t16, dev)
+    op = _fits(out, "out", w, shape, t16, dev)
+    sp = _fits(stats, "stats", w, (m, 2), torch.float32, dev)
+    rp = None if residual is None else _fits(residual, "residual", w, shape, t16, dev)
+    tp = None if total is None else _fits(total, "total", w, shape, t16, dev)
+    _enqueue(w, dev, stream, xp, rp, wp, bp, m, n, dt, eps, op, tp, sp)
+
+
+def nf4_layer_norm_grad(dy, x, weight, stats, dx, dweight, dbias, ws=None, residual=None, stream=None) -> None:
+    """The norm's gradients: dx (plus residual, the gradient that reaches the sum
+    past the norm), dweight and dbias (float32 [n], overwritten).  x: what was
+    normalised (total, with a residual), stats: nf4_layer_norm's; dx may be dy, x or
+    residual.  ws: device tensor of nf4_layer_norm_grad_workspace_bytes(m, n) bytes,
+    or None when that is 0."""
+    import torch
+    w = "nf4_layer_norm_grad"
+    dt, dev, t16 = _dtype16(dy, w), dy.get_device(), dy.dtype
+    if dy.dim() != 2:
+        _misfit(w, "dy must be [m, n]")
+    m, n = shape = dy.shape
+    yp = _fits(dy, "dy", w, shape, t16, dev)
+    xp = _fits(x, "x", w, shape, t16, dev)
+    gp = _fits(weight, "weight", w, (n,), t16, dev)
+    sp = _fits(stats, "stats", w, (m, 2), torch.float32, dev)
+    rp = None if residual is None else _fits(residual, "residual", w, shape, t16, dev)
+    dp = _fits(dx, "dx", w, shape, t16, dev)
+    dwp = _fits(dweight, "dweight", w, (n,), torch.float32, dev)
+    dbp = _fits(dbias, "dbias", w, (n,), torch.float32, dev)
+    wp, wb = _ws_arg(ws, w, dev)
+    _enqueue(w, dev, stream, yp, xp, gp, sp, rp, m, n, dt, dp, dwp, dbp, wp, wb)
+
+
+def nf4_layer_norm_grad_workspace_bytes(m: int, n: int) -> int:
+    return int(lib().nf4_layer_norm_grad_workspace_bytes(int(m), int(n)))
+
+
+# ---- microscaled 4-bit weights --------------------------------------------
+#
+# A matrix [rows, cols] in this form is a pair of uint8 tensors: codes [rows,
+# cols / 2] and scales [rows, cols / 32].  Shapes come from the tensors; streams
+# and errors as for the adapted layer.
+
+def _mx4_pair(codes, scales, names: tuple, where: str, dev: int):
+    """The addresses, rows and cols of a matrix in microscaled form."""
+    import torch
+    if codes.dim() != 2 or codes.shape[1] % 16:
+        _misfit(where, f"{names[0]} must be [rows, cols / 2] with cols a multiple of 32, got {tuple(codes.shape)}")
+    rows, half = codes.shape
+    cp = _fits(codes, names[0], where, (rows, half), torch.uint8, dev)
+    return cp, _fits(scales, names[1], where, (rows, half // 16), torch.uint8, dev), rows, 2 * half
+
+
+_MX4_W, _MX4_X = ("codes", "scales"), ("xcodes", "xscales")
+
+
+def mx4_quantize(x, codes, scales, err=None, ws=None, stream=None) -> None:
+    """codes and scales of x [rows, cols] (bfloat16 or float16) and, with err
+    (float64 [1]), the sum of squared differences to their values: a score for
+    aqlora_select.  ws: device tensor of mx4_quantize_workspace_bytes(rows, cols)
+    bytes with err, or None when that is 0."""
+    import torch
+    w = "mx4_quantize"
+    dt, dev = _dtype16(x, w), x.get_device()
+    cp, sp, rows, cols = _mx4_pair(codes, scales, _MX4_W, w, dev)
+    xp = _fits(x, "x", w, (rows, cols), x.dtype, dev)
+    ep = None if err is None else _fits(err, "err", w, (1,), torch.float64, dev)
+    wp, wb = _ws_arg(ws, w, dev)
+    _enqueue(w, dev, stream, xp, rows, cols, dt, cp, sp, ep, wp, wb)
+
+
+def mx4_dequantize(codes, scales, out, stream=None) -> None:
+    """out [rows, cols] (bfloat16 or float16) = the values of codes and scales."""
+    w = "mx4_dequantize"
+    dt, dev = _dtype16(out, w), out.get_device()
+    cp, sp, rows, cols = _mx4_pair(codes, scales, _MX4_W, w, dev)
+    _enqueue(w, dev, stream, cp, sp, rows, cols, dt, _fits(out, "out", w, (rows, cols), out.dtype, dev))
+
+
+def _mx4_out(out, t16, where: str, shape: tuple, dev: int):
+    import torch
+    f32 = out.dtype is torch.float32
+    return _fits(out, "out", where, shape, torch.float32 if f32 else t16, dev), 1 if f32 else 0
+
+
+def mx4_matmul(codes, scales, x, out, ws=None, backward: bool = False, stream=None) -> None:
+    """out [m, rows] = x W^T (x [m, cols]), or backward out [m, cols] = x W (x [m,
+    rows]), W [rows, cols] by its codes and scales.  x bfloat16 or float16, out that
+    type or float32.  ws: device tensor of mx4_matmul_workspace_bytes(rows, cols,
+    backward, m) bytes, or None when that is 0."""
+    w = "mx4_matmul"
+    dt, dev, t16 = _dtype16(x, w), x.get_device(), x.dtype
+    cp, sp, rows, cols = _mx4_pair(codes, scales, _MX4_W, w, dev)
+    if x.dim() != 2:
+        _misfit(w, "x must have two dimensions")
+    m = x.shape[0]
+    xp = _fits(x, "x", w, (m, rows if backward else cols), t16, dev)
+    op, f32 = _mx4_out(out, t16, w, (m, cols if backward else rows), dev)
+    wp, wb = _ws_arg(ws, w, dev)
+    _enqueue(w, dev, stream, cp, sp, rows, cols, dt, 1 if backward else 0, xp, m, op, f32, wp, wb)
+
+
+def mx4_matmul4(codes, scales, xcodes, xscales, out, ws=None, stream=None) -> None:
+    """out [m, rows] = x W^T with W [rows, cols] and x [m, cols] both by codes and
+    scales; out bfloat16, float16 or float32.  ws: device tensor of
+    mx4_matmul4_workspace_bytes(rows, cols, m) bytes, or None when that is 0."""
+    import torch
+    w = "mx4_matmul4"
+    dev = codes.get_device()
+    cp, sp, rows, cols = _mx4_pair(codes, scales, _MX4_W, w, dev)
+    xcp, xsp, m, xcols = _mx4_pair(xcodes, xscales, _MX4_X, w, dev)
+    if xcols != cols:
+        _misfit(w, f"xcodes must have {cols} columns, got {xcols}")
+    t16 = torch.float16 if out.dtype is torch.float16 else torch.bfloat16
+    op, f32 = _mx4_out(out, t16, w, (m, rows), dev)
+    wp, wb = _ws_arg(ws, w, dev)
+    _enqueue(w, dev, stream, cp, sp, rows, cols, xcp, xsp, m, NF4_FP16 if t16 is torch.float16 else NF4_BF16, op, f32,
+             wp, wb)
+
+
+def mx4_quantize_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().mx4_quantize_workspace_bytes(int(rows), int(cols)))
+
+
+def mx4_matmul_workspace_bytes(rows: int, cols: int, backward: bool, m: int) -> int:
+    return int(lib().mx4_matmul_workspace_bytes(int(rows), int(cols), int(bool(backward)), int(m)))
+
+
+def mx4_matmul4_workspace_bytes(rows: int, cols: int, m: int) -> int:
+    return int(lib().mx4_matmul4_workspace_bytes(int(rows), int(cols), int(m)))
+
+
+def mx4_storage_bytes(rows: int, cols: int) -> int:
+    return int(lib().mx4_storage_bytes(int(rows), int(cols)))
 
 
 # ---- host helpers ---------------------------------------------------------

@@ -1,0 +1,309 @@
+// k_mx4_few.hip -- the microscaled products at few tokens, on gfx950 matrix
+// cores.  The weights' codes are read once, 16 bytes a lane, and that read bounds
+// the call; nothing of them goes through LDS.
+//
+//   forward   out[t, n] = sum_k x[t, k] W[n, k]
+//   backward  out[t, k] = sum_n x[t, n] W[n, k]
+//
+// Forward: a wave takes kRT x 16 weight rows and every kWaves-th step of 128
+// columns.  Lane (r, g) holds row r's 32 codes of block g: one load, one scale.
+// In 16 bits they make four fragments of v_mfma_f32_16x16x32 (the reduction index
+// of element j of fragment f in group g is 32 g + 8 f + j; x is read to match);
+// with x in 4 bits too, they are the operand of v_mfma_scale_f32_16x16x128 as they
+// are.  The waves' sums meet in LDS.
+//
+// Backward the reduction runs over the weight's rows, whose scales differ.  Lane
+// (r, g) reads eight columns (a dword) of rows 8 g .. 8 g + 7 of a 32-row slab; a
+// byte (two columns of one row) is converted under that row's scale, and the
+// halves of two rows' results are put together as the fragments' pairs.  Column
+// 8 r + c of a 128-column stripe is row r of tile c, so that a lane ends with
+// eight consecutive columns.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx4_format.h"
+#include "mx4_launch.h"
+#include "mx4_sum.h"
+
+namespace mx4k {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr u32x4 kZero = {0, 0, 0, 0};
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c)
+{
+    if constexpr (DT == 0)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 mfma4(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb, const f32x4& c)
+{
+    const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8 y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+struct FewArgs {
+    const uint8_t *codes, *scales;   // W [rows x cols]
+    const void* x;                   // [m x cols] (backward [m x rows]) in 16 bits, or codes
+    const uint8_t* xscales;
+    void* out;
+    float* part;                     // backward with parts > 1: fp32 [parts][m x cols]
+    int64_t m, rows, cols;
+    int kind;                        // of out
+    int parts;
+};
+
+__device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+
+constexpr int kWaves = 8;
+
+// DT 0, 1: x in bf16, fp16; 2: in codes.
+template <int DT, int kRT, int kMT>
+__global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
+{
+    __shared__ f32x4 sums[kWaves][kRT * kMT][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * kRT), t0 = (int64_t)blockIdx.y * (16 * kMT);
+    const int64_t blocks = a.cols / kGroup;
+    const MX4_GLOBAL uint8_t *wc[kRT], *ws[kRT];
+#pragma unroll
+    for (int i = 0; i < kRT; ++i) {
+        const int64_t n = least(n0 + 16 * i + r, a.rows - 1);
+        wc[i] = (const MX4_GLOBAL uint8_t*)a.codes + n * (a.cols / 2);
+        ws[i] = (const MX4_GLOBAL uint8_t*)a.scales + n * blocks;
+    }
+    const MX4_GLOBAL uint8_t* xc[kMT];   // the token's row, bytes
+    const MX4_GLOBAL uint8_t* xs[kMT];
+#pragma unroll
+    for (int u = 0; u < kMT; ++u) {
+        const int64_t t = least(t0 + 16 * u + r, a.m - 1);
+        xc[u] = (const MX4_GLOBAL uint8_t*)a.x + t * (DT == 2 ? a.cols / 2 : a.cols * 2);
+        xs[u] = (const MX4_GLOBAL uint8_t*)a.xscales + t * blocks;
+    }
+    f32x4 acc[kRT][kMT] = {};
+    for (int64_t blk = 4 * wave + g; blk - g < blocks; blk += 4 * kWaves) {
+        const bool in = blk < blocks;   // a block is whole or not there
+        u32x4 c[kRT];
+        uint32_t s[kRT];
+#pragma unroll
+        for (int i = 0; i < kRT; ++i) {
+            c[i] = in ? *(const MX4_GLOBAL u32x4*)(wc[i] + 16 * blk) : kZero;
+            s[i] = in ? ws[i][blk] : 0u;
+        }
+        if constexpr (DT == 2) {
+#pragma unroll
+            for (int u = 0; u < kMT; ++u) {
+                const u32x4 d = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 16 * blk) : kZero;
+                const uint32_t e = in ? xs[u][blk] : 0u;
+#pragma unroll
+                for (int i = 0; i < kRT; ++i) acc[i][u] = mfma4(c[i], s[i], d, e, acc[i][u]);
+            }
+        } else {
+            u32x4 x[kMT][4];
+#pragma unroll
+            for (int u = 0; u < kMT; ++u)
+#pragma unroll
+                for (int f = 0; f < 4; ++f) x[u][f] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 64 * blk + 16 * f) : kZero;
+#pragma unroll
+            for (int i = 0; i < kRT; ++i)
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const u32x4 w = decode8<DT>(c[i][f], scale_arg(s[i]));
+#pragma unroll
+                    for (int u = 0; u < kMT; ++u) acc[i][u] = mfma16<DT>(w, x[u][f], acc[i][u]);
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRT; ++i)
+#pragma unroll
+        for (int u = 0; u < kMT; ++u) sums[wave][i * kMT + u][lane] = acc[i][u];
+    __syncthreads();
+    // lane (r, g) of a tile: token r, weight rows 4 g .. 4 g + 3
+    for (int e = threadIdx.x; e < kRT * kMT * 64; e += 64 * kWaves) {
+        const int tile = e >> 6, l = e & 63;
+        f32x4 v = sums[0][tile][l];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += sums[w][tile][l];
+        const int64_t t = t0 + 16 * (tile % kMT) + (l & 15), n = n0 + 16 * (tile / kMT) + 4 * (l >> 4);
+        if (t < a.m && n < a.rows) store4(a.out, a.kind, t * a.rows + n, v);
+    }
+}
+
+// The low and the high halves of two dwords, put together.
+__device__ __forceinline__ uint32_t low16(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high16(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+// Two columns (byte B of each row's dword) of eight rows to two fragments.
+template <int DT, int B>
+__device__ __forceinline__ void decode_columns(const uint32_t (&c)[8], const float (&s)[8], u32x4& even, u32x4& odd)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t p = decode2<DT, B>(c[2 * j], s[2 * j]), q = decode2<DT, B>(c[2 * j + 1], s[2 * j + 1]);
+        even[j] = low16(p, q);
+        odd[j] = high16(p, q);
+    }
+}
+
+template <int DT, int kMT>
+__global__ __launch_bounds__(64 * kWaves) void k_few_back(FewArgs a)
+{
+    __shared__ f32x4 sums[kWaves / 2][8 * kMT][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int64_t c0 = (int64_t)blockIdx.x * 128, t0 = (int64_t)blockIdx.y * (16 * kMT);
+    const int64_t col = least(c0 + 8 * r, a.cols - 8);
+    const MX4_GLOBAL uint8_t* wc = (const MX4_GLOBAL uint8_t*)a.codes + col / 2;
+    const MX4_GLOBAL uint8_t* ws = (const MX4_GLOBAL uint8_t*)a.scales + col / kGroup;
+    const MX4_GLOBAL uint16_t* xr[kMT];
+#pragma unroll
+    for (int u = 0; u < kMT; ++u) xr[u] = (const MX4_GLOBAL uint16_t*)a.x + least(t0 + 16 * u + r, a.m - 1) * a.rows;
+    f32x4 acc[kMT][8] = {};
+    const int64_t slabs = (a.rows + 31) / 32, stride = (int64_t)kWaves * a.parts;
+    for (int64_t slab = wave + (int64_t)kWaves * blockIdx.z; slab < slabs; slab += stride) {
+        const int64_t n = 32 * slab + 8 * g;
+        const bool in = n < a.rows;   // rows come in eights
+        uint32_t c[8];
+        float s[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            c[j] = in ? *(const MX4_GLOBAL uint32_t*)(wc + (n + j) * (a.cols / 2)) : 0u;
+            s[j] = scale_arg(in ? ws[(n + j) * (a.cols / kGroup)] : 0u);
+        }
+        u32x4 x[kMT], w[8];
+#pragma unroll
+        for (int u = 0; u < kMT; ++u) x[u] = in ? *(const MX4_GLOBAL u32x4*)(xr[u] + n) : kZero;
+        decode_columns<DT, 0>(c, s, w[0], w[1]);
+        decode_columns<DT, 1>(c, s, w[2], w[3]);
+        decode_columns<DT, 2>(c, s, w[4], w[5]);
+        decode_columns<DT, 3>(c, s, w[6], w[7]);
+#pragma unroll
+        for (int u = 0; u < kMT; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[u][i] = mfma16<DT>(x[u], w[i], acc[u][i]);
+    }
+    // the upper half of the waves' sums to LDS and added by the lower half, until one is left
+#pragma unroll
+    for (int half = kWaves / 2; half; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+            for (int i = 0; i < 8 * kMT; ++i) sums[wave - half][i][lane] = acc[i >> 3][i & 7];
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int i = 0; i < 8 * kMT; ++i) acc[i >> 3][i & 7] += sums[wave][i][lane];
+        }
+        __syncthreads();
+    }
+    if (wave != 0 || c0 + 8 * r >= a.cols) return;
+    void* out = a.parts > 1 ? (void*)(a.part + (int64_t)blockIdx.z * a.m * a.cols) : a.out;
+    const int kind = a.parts > 1 ? (int)kOutFp32 : a.kind;
+    // lane (r, g): tokens 4 g .. 4 g + 3, columns 8 r .. 8 r + 7
+#pragma unroll
+    for (int u = 0; u < kMT; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t t = t0 + 16 * u + 4 * g + i;
+            if (t < a.m)
+                store8(out, kind, t * a.cols + col, f32x4{acc[u][0][i], acc[u][1][i], acc[u][2][i], acc[u][3][i]},
+                       f32x4{acc[u][4][i], acc[u][5][i], acc[u][6][i], acc[u][7][i]});
+        }
+}
+
+__global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits, int64_t n, void* out, int kind)
+{
+    const int64_t at = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (at >= n) return;
+    const MX4_GLOBAL f32x4* p = (const MX4_GLOBAL f32x4*)(part + at);
+    f32x4 a = p[0], b = p[1];
+    for (int s = 1; s < splits; ++s) {
+        p += n / 4;
+        a += p[0];
+        b += p[1];
+    }
+    store8(out, kind, at, a, b);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int token_tiles(int64_t m) { return m <= 16 ? 1 : m <= 32 ? 2 : 4; }
+
+// Backward: parts of the reduction so that about 1,024 workgroups run, each
+// wave with two slabs at least.
+int back_parts(int64_t rows, int64_t cols, int64_t m)
+{
+    const int64_t groups = ceil_div(cols, 128) * ceil_div(m, 16 * token_tiles(m)), slabs = ceil_div(rows, 32);
+    int64_t p = ceil_div(1024, groups);
+    const int64_t most = ceil_div(slabs, 2 * kWaves);
+    if (p > most) p = most;
+    return (int)(p < 1 ? 1 : p > 16 ? 16 : p);
+}
+
+template <int DT>
+hipError_t few_go(const FewArgs& a, hipStream_t s)
+{
+    const int mt = token_tiles(a.m);
+    const dim3 grid((unsigned)ceil_div(a.rows, 32), (unsigned)ceil_div(a.m, 16 * mt));
+    if (mt == 1) k_few<DT, 2, 1><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (mt == 2) k_few<DT, 2, 2><<<grid, 64 * kWaves, 0, s>>>(a);
+    else k_few<DT, 2, 4><<<grid, 64 * kWaves, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t few_back_go(const FewArgs& a, hipStream_t s)
+{
+    const int mt = token_tiles(a.m);
+    const dim3 grid((unsigned)ceil_div(a.cols, 128), (unsigned)ceil_div(a.m, 16 * mt), (unsigned)a.parts);
+    if (mt == 1) k_few_back<DT, 1><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (mt == 2) k_few_back<DT, 2><<<grid, 64 * kWaves, 0, s>>>(a);
+    else k_few_back<DT, 4><<<grid, 64 * kWaves, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_split_sum(const float* part, int splits, int64_t n, void* out, int out_kind, hipStream_t s)
+{
+    k_split_sum<<<(unsigned)ceil_div(n, 2048), 256, 0, s>>>(part, splits, n, out, out_kind);
+    return hipGetLastError();
+}
+
+size_t matmul_ws(int64_t rows, int64_t cols, bool forward, int64_t m)
+{
+    if (forward) return 0;
+    const int parts = back_parts(rows, cols, m);
+    return parts > 1 ? size_t(parts) * size_t(m) * size_t(cols) * sizeof(float) : 0;
+}
+
+hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                         bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s)
+{
+    FewArgs a{codes, scales, x, nullptr, out, part, m, rows, cols, out_kind, 1};
+    if (forward) return dtype == 0 ? few_go<0>(a, s) : few_go<1>(a, s);
+    a.parts = back_parts(rows, cols, m);
+    const hipError_t e = dtype == 0 ? few_back_go<0>(a, s) : few_back_go<1>(a, s);
+    if (e != hipSuccess || a.parts == 1) return e;
+    return launch_split_sum(part, a.parts, m * cols, out, out_kind, s);
+}
+
+size_t matmul4_ws(int64_t, int64_t, int64_t) { return 0; }
+
+hipError_t launch_matmul4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                          const uint8_t* xcodes, const uint8_t* xscales, int64_t m, void* out, int out_kind, float*,
+                          hipStream_t s)
+{
+    const FewArgs a{codes, scales, xcodes, xscales, out, nullptr, m, rows, cols, out_kind, 1};
+    return few_go<2>(a, s);
+}
+
+}  // namespace mx4k

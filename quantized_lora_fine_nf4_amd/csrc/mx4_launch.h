@@ -1,0 +1,35 @@
+// mx4_launch.h -- the kernel launchers behind include/mx4.h, called by mx4_api.cpp after it has validated the arguments (not part of the
+// public ABI).  dtype: 0 bf16, 1 fp16.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mx4k {
+
+// n elements (a multiple of 32, consecutive) to codes and scales.  With err
+// their squared error in fp64, through quantize_blocks(n) fp64 partials at part
+// (one block: straight to err).
+int64_t quantize_blocks(int64_t n);
+hipError_t launch_quantize(int dtype, const void* x, int64_t n, uint8_t* codes, uint8_t* scales, double* err,
+                           double* part, hipStream_t s);
+hipError_t launch_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t n, void* out,
+                             hipStream_t s);
+
+// out[m x rows] = x W^T (forward) or out[m x cols] = x W, W [rows x cols] given
+// by codes and scales, x of dtype; out_kind 0 bf16, 1 fp16, 2 fp32.  matmul_ws
+// bytes of partials at part (0: unused), a function of the shape only.
+size_t matmul_ws(int64_t rows, int64_t cols, bool forward, int64_t m);
+hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                         bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s);
+
+// The same forward with x [m x cols] in the microscaled form too.
+size_t matmul4_ws(int64_t rows, int64_t cols, int64_t m);
+hipError_t launch_matmul4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                          const uint8_t* xcodes, const uint8_t* xscales, int64_t m, void* out, int out_kind,
+                          float* part, hipStream_t s);
+
+// The sum of `splits` fp32 partials of n values each (a multiple of 8) in split
+// order, to out (mx4_sum.h).
+hipError_t launch_split_sum(const float* part, int splits, int64_t n, void* out, int out_kind, hipStream_t s);
+
+}  // namespace mx4k

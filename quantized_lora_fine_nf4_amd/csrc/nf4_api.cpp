@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstring>
 #include <vector>
 
@@ -90,11 +91,7 @@ nf4_status check_ws(const void* ws, size_t ws_bytes, size_t need)
     return NF4_OK;
 }
 
-nf4_status hip_fail(hipError_t e)
-{
-    g_last_hip = static_cast<int32_t>(e);
-    return NF4_E_HIP;
-}
+nf4_status hip_fail(hipError_t e) { return static_cast<nf4_status>(nf4k::hip_failed(e)); }
 
 // Build the device layer table in host memory and copy it into the workspace
 // on the stream.  The copy is from pageable memory, which the runtime stages
@@ -332,6 +329,12 @@ nf4_status dequantize_impl(const nf4_layer* layers, int32_t nl, nf4_format fmt, 
 }
 
 }  // namespace
+
+int32_t nf4k::hip_failed(hipError_t e)
+{
+    g_last_hip = static_cast<int32_t>(e);
+    return NF4_E_HIP;
+}
 
 extern "C" {
 
@@ -697,6 +700,53 @@ nf4_status nf4_lora_grad(const void* u, const void* x, int64_t m, int64_t n, int
     if (need > 0 && (st = check_ws(ws, ws_bytes, need)) != NF4_OK) return st;
     hipError_t e = nf4k::launch_lora_grad(dtype, u, x, m, n, rank, side == NF4_LORA_B, d, grad, static_cast<float*>(ws),
                                           stream);
+    return e == hipSuccess ? NF4_OK : hip_fail(e);
+}
+
+nf4_status nf4_layer_norm(const void* x, const void* residual, const void* weight, const void* bias, int64_t m, int64_t n,
+                          int32_t dtype, float eps, void* out, void* total, float* stats, hipStream_t stream)
+{
+    nf4_status st = check_dtype(dtype);
+    if (st != NF4_OK) return st;
+    if (!x || !weight || !bias || !out || !stats || !residual != !total) return NF4_E_ARG;
+    if (m <= 0 || m > kMaxTokens || n <= 0 || n >= kMaxCols || !(eps >= 0.0f && eps < HUGE_VALF)) return NF4_E_ARG;
+    if (total && total == out) return NF4_E_ARG;
+    if (n % 8) return NF4_E_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(out, 16) ||
+        !aligned(total, 16) || !aligned(stats, 8))
+        return NF4_E_ALIGN;
+    typedef const uint16_t* In;
+    const nf4k::NormArgs a{In(x), In(residual), In(weight), In(bias), static_cast<uint16_t*>(out),
+                           static_cast<uint16_t*>(total), stats, m, int(n), eps};
+    hipError_t e = nf4k::launch_layer_norm(dtype, a, stream);
+    return e == hipSuccess ? NF4_OK : hip_fail(e);
+}
+
+size_t nf4_layer_norm_grad_workspace_bytes(int64_t m, int64_t n)
+{
+    if (m <= 0 || m > kMaxTokens || n <= 0 || n >= kMaxCols || n % 8) return 0;
+    const int blocks = nf4k::norm_grad_blocks(m, n);
+    return blocks > 1 ? align256(size_t(blocks) * 2 * size_t(n) * sizeof(float)) : 0;
+}
+
+nf4_status nf4_layer_norm_grad(const void* dy, const void* x, const void* weight, const float* stats,
+                               const void* residual, int64_t m, int64_t n, int32_t dtype, void* dx, float* dweight,
+                               float* dbias, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    nf4_status st = check_dtype(dtype);
+    if (st != NF4_OK) return st;
+    if (!dy || !x || !weight || !stats || !dx || !dweight || !dbias) return NF4_E_ARG;
+    if (m <= 0 || m > kMaxTokens || n <= 0 || n >= kMaxCols) return NF4_E_ARG;
+    if (n % 8) return NF4_E_UNSUPPORTED;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(weight, 16) || !aligned(stats, 8) || !aligned(residual, 16) ||
+        !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(dbias, 16))
+        return NF4_E_ALIGN;
+    const size_t need = nf4_layer_norm_grad_workspace_bytes(m, n);
+    if (need > 0 && (st = check_ws(ws, ws_bytes, need)) != NF4_OK) return st;
+    typedef const uint16_t* In;
+    const nf4k::NormGradArgs a{In(dy), In(x), In(weight), In(residual), stats, static_cast<uint16_t*>(dx), dweight,
+                               dbias, static_cast<float*>(ws), m, int(n)};
+    hipError_t e = nf4k::launch_layer_norm_grad(dtype, a, stream);
     return e == hipSuccess ? NF4_OK : hip_fail(e);
 }
 

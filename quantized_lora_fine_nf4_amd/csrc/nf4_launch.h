@@ -142,4 +142,30 @@ hipError_t launch_nf4_linear_gemv(int dtype, const uint8_t* codes, const int8_t*
                                   const float* absmax, int64_t rows, int64_t cols, const void* x, int64_t m, void* out,
                                   bool out_f32, float* part, int parts, const EpiArgs& epi, hipStream_t s);
 
+// ---- layer norm (k_norm.hip)
+
+// Layer norm of m rows of n (a multiple of 8).  residual and total: both or
+// neither.
+struct NormArgs {
+    const uint16_t *x, *residual, *weight, *bias;
+    uint16_t *out, *total;
+    float* stats;   // [m][2] mean, 1 / deviation
+    int64_t m;
+    int n;
+    float eps;
+};
+hipError_t launch_layer_norm(int dtype, const NormArgs& a, hipStream_t s);
+
+struct NormGradArgs {
+    const uint16_t *dy, *x, *weight, *residual;   // residual: null or added to dx
+    const float* stats;
+    uint16_t* dx;
+    float *dweight, *dbias;                       // [n] each
+    float* part;                                  // norm_grad_blocks [blocks][2][n] fp32 (one block: unused)
+    int64_t m;
+    int n;
+};
+int norm_grad_blocks(int64_t m, int64_t n);
+hipError_t launch_layer_norm_grad(int dtype, const NormGradArgs& a, hipStream_t s);
+
 }  // namespace nf4k
