@@ -1,0 +1,319 @@
+// k_mx4_mm4.hip -- the product of two microscaled 4-bit operands on gfx950's
+// scaled matrix instructions: out[t, n] = sum_k x[t, k] W[n, k].
+//
+// v_mfma_scale_f32_32x32x64 takes 32 codes (16 bytes, one group) and one scale
+// byte a lane, as they lie in memory: nothing is converted.  It does four times
+// the operations of the 16-bit instructions per cycle, so the operands' way to it
+// is what bounds the kernel: a 256 x 256 output tile by four waves of 128 x 128
+// (one per SIMD, 256 accumulator registers each) needs 192 KB through LDS for
+// 2,048 matrix cycles, 1,536 of the LDS's.  Eight waves of 128 x 64 would need
+// 256 KB, as many cycles as the matrix cores.
+//
+// A step is 256 columns: 128 bytes of codes and 8 scales of each row, through
+// registers into one of two LDS buffers while the other one is multiplied.  The
+// 16-byte pieces of a row are permuted by its index, so that eight lanes that read
+// eight rows touch all banks.  Weight row TN r + c of a wave's columns is row r of
+// its tile c: a lane ends with TN consecutive columns.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "mx4_format.h"
+#include "mx4_launch.h"
+#include "mx4_sum.h"
+#include "mx4_tile.h"
+
+namespace mx4k {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kThreads = 256;
+constexpr int kStep = 256;            // columns a step
+constexpr int kRowBytes = kStep / 2;
+constexpr int kGroups = kStep / kGroup;
+
+typedef std::integral_constant<bool, true> Yes;
+typedef std::integral_constant<bool, false> No;
+
+struct Mm4Args {
+    const uint8_t *codes, *scales, *xcodes, *xscales;
+    void* out;
+    float* part;   // parts > 1: fp32 [parts][m x rows]
+    int64_t m, rows;
+    int cols, kind;
+    TileGrid grid;
+};
+
+template <int S>
+__device__ __forceinline__ f32x16 mfma4(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb, const f32x16& c)
+{
+    const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8 y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, S, (int)sa, S, (int)sb);
+}
+
+// A wave's tile: TM x TN tiles of 32 x 32; the workgroup's: 2 x 2 waves.
+template <int TM, int TN>
+struct Shape {
+    static constexpr int kBM = 64 * TM, kBN = 64 * TN;
+    static constexpr int kA = 2 * TM, kW = 2 * TN;   // 16-byte pieces of the operands per thread and step
+};
+
+template <int TM, int TN>
+struct Buffer {
+    u32x4 a[64 * TM * (kRowBytes / 16)], w[64 * TN * (kRowBytes / 16)];
+    u32x2 as[64 * TM], ws[64 * TN];
+};
+
+// The eight scales of a row of n from group `at` on.  LONG, n >= 8: those past the
+// row's end are dropped by the shift of mask() below; else they are zeros already.
+template <bool LONG>
+__device__ __forceinline__ uint64_t load_scales(const MX4_GLOBAL uint8_t* row, int at, int n)
+{
+    uint64_t v = 0;
+    if (LONG || n >= kGroups) {
+        __builtin_memcpy(&v, (const uint8_t*)row + (at + kGroups <= n ? at : n - kGroups), 8);
+    } else {
+        for (int i = at; i < n; ++i) v |= (uint64_t)row[i] << (8 * (i - at));
+    }
+    return v;
+}
+
+template <int TM, int TN>
+__global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
+{
+    typedef Shape<TM, TN> S;
+    extern __shared__ char lds_raw[];
+    Buffer<TM, TN>* lds = (Buffer<TM, TN>*)lds_raw;
+    int tm, tn, part;
+    tile_of(g.grid, blockIdx.x, tm, tn, part);
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, r = lane & 31, h = lane >> 5;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int64_t m0 = (int64_t)tm * S::kBM, n0 = (int64_t)tn * S::kBN;
+    const uint32_t pitch = (uint32_t)g.cols / 2;
+    const int spitch = g.cols / kGroup;
+    const int steps_all = (g.cols + kStep - 1) / kStep, first = part * g.grid.per_part;
+    const int last = first + g.grid.per_part < steps_all ? first + g.grid.per_part : steps_all;
+
+    // this thread's pieces: rows t / 8 + 32 i, piece t % 8; offsets from the tile's first row
+    const int piece = t & 7;
+    uint32_t ao[S::kA], wo[S::kW];
+#pragma unroll
+    for (int i = 0; i < S::kA; ++i) {
+        int64_t row = m0 + 32 * i + (t >> 3);
+        row = (row < g.m ? row : g.m - 1) - m0;
+        ao[i] = (uint32_t)row * pitch;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kW; ++i) {
+        int64_t row = n0 + (i / TN) * (32 * TN) + TN * (t >> 3) + i % TN;
+        row = (row < g.rows ? row : g.rows - 1) - n0;
+        wo[i] = (uint32_t)row * pitch;
+    }
+    // and scale rows t of both (LDS order)
+    int64_t aso, wso;
+    {
+        int64_t row = m0 + t % S::kBM;
+        aso = ((row < g.m ? row : g.m - 1) - m0) * spitch;
+        const int l = t % S::kBN;
+        row = n0 + (l / (32 * TN)) * (32 * TN) + TN * (l & 31) + (l >> 5) % TN;
+        wso = ((row < g.rows ? row : g.rows - 1) - n0) * spitch;
+    }
+    const MX4_GLOBAL uint8_t* ap = (const MX4_GLOBAL uint8_t*)g.xcodes + m0 * pitch;
+    const MX4_GLOBAL uint8_t* wp = (const MX4_GLOBAL uint8_t*)g.codes + n0 * pitch;
+    const MX4_GLOBAL uint8_t* asp = (const MX4_GLOBAL uint8_t*)g.xscales + m0 * spitch + aso;
+    const MX4_GLOBAL uint8_t* wsp = (const MX4_GLOBAL uint8_t*)g.scales + n0 * spitch + wso;
+
+    u32x4 ra[S::kA], rw[S::kW];
+    uint64_t ras, rws;
+    auto load = [&](int step, auto long_row) {
+        const int left = spitch - step * kGroups;
+        // a piece past the row's end: the step's first one, zeroed before it is stored
+        const uint32_t at = (uint32_t)step * kRowBytes + (piece < left ? 16 * piece : 0);
+#pragma unroll
+        for (int i = 0; i < S::kA; ++i) ra[i] = *(const MX4_GLOBAL u32x4*)(ap + (ao[i] + at));
+#pragma unroll
+        for (int i = 0; i < S::kW; ++i) rw[i] = *(const MX4_GLOBAL u32x4*)(wp + (wo[i] + at));
+        ras = load_scales<long_row>(asp, step * kGroups, spitch);
+        rws = load_scales<long_row>(wsp, step * kGroups, spitch);
+    };
+    const int swz = (t >> 3) * 8 + (piece ^ ((t >> 3) & 7));
+    auto mask = [&](int step) {
+        const int left = spitch - step * kGroups;
+        const uint32_t in = piece < left ? 0xffffffffu : 0u;
+        if (left < kGroups && spitch >= kGroups) {
+            ras >>= 8 * (kGroups - left);
+            rws >>= 8 * (kGroups - left);
+        }
+#pragma unroll
+        for (int i = 0; i < S::kA; ++i) ra[i] &= in;
+#pragma unroll
+        for (int i = 0; i < S::kW; ++i) rw[i] &= in;
+    };
+    auto store = [&](Buffer<TM, TN>& b) {
+#pragma unroll
+        for (int i = 0; i < S::kA; ++i) b.a[swz + 256 * i] = ra[i];
+#pragma unroll
+        for (int i = 0; i < S::kW; ++i) b.w[swz + 256 * i] = rw[i];
+        // threads past the tile's rows write the rows of others once more, to the same values
+        b.as[t % S::kBM] = __builtin_bit_cast(u32x2, ras);
+        b.ws[t % S::kBN] = __builtin_bit_cast(u32x2, rws);
+    };
+
+    f32x16 acc[TM][TN] = {};
+    u32x4 fa[2][TM], fw[2][TN];
+    uint32_t sa[TM], sw[TN];
+    const uint32_t pick = h ? 0x07050301u : 0x06040200u;   // this half's scales of the four sub-steps
+    u32x2 na[TM], nw[TN];
+    auto frags = [&](const Buffer<TM, TN>& b, int s, int to) {
+        const int at = r * 8 + ((2 * s + h) ^ (r & 7));
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[to][i] = b.a[(wm * TM + i) * 256 + at];
+#pragma unroll
+        for (int i = 0; i < TN; ++i) fw[to][i] = b.w[(wn * TN + i) * 256 + at];
+    };
+    // the first sub-step's fragments and the scales of a step
+    auto begin = [&](const Buffer<TM, TN>& b) {
+        frags(b, 0, 0);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) na[i] = b.as[(wm * TM + i) * 32 + r];
+#pragma unroll
+        for (int i = 0; i < TN; ++i) nw[i] = b.ws[(wn * TN + i) * 32 + r];
+    };
+#define MX4_MULTIPLY(SUB, FROM)                                                                            \
+    _Pragma("unroll") for (int i = 0; i < TM; ++i)                                                         \
+        _Pragma("unroll") for (int j = 0; j < TN; ++j)                                                     \
+            acc[i][j] = mfma4<SUB>(fa[FROM][i], sa[i], fw[FROM][j], sw[j], acc[i][j])
+// matrix instructions with the given numbers of LDS reads, LDS writes and loads among them
+#define MX4_ORDER(READS, WRITES, LOADS)                                                                    \
+    _Pragma("unroll") for (int i = 0; i < TM * TN; ++i) {                                                  \
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                                 \
+        if (READS) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);                                  \
+        if (WRITES) __builtin_amdgcn_sched_group_barrier(0x200, WRITES, 0);                                \
+        if (LOADS) __builtin_amdgcn_sched_group_barrier(0x020, LOADS, 0);                                  \
+    }                                                                                                      \
+    __builtin_amdgcn_sched_barrier(0)
+
+    int cur = 0;
+    // one step: STORE puts the next step into the other buffer (MASK: it may be the row's last), LOAD fetches the one after it
+    auto body = [&](int step, auto store_next, auto mask_next, auto load_next) {
+        const Buffer<TM, TN>& now = lds[cur];
+        Buffer<TM, TN>& next = lds[cur ^ 1];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa[i] = __builtin_amdgcn_perm(na[i][1], na[i][0], pick);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sw[j] = __builtin_amdgcn_perm(nw[j][1], nw[j][0], pick);
+        frags(now, 1, 1);
+        MX4_MULTIPLY(0, 0);
+        MX4_ORDER(1, 0, 0);
+        frags(now, 2, 0);
+        MX4_MULTIPLY(1, 1);
+        MX4_ORDER(1, 0, 0);
+        if constexpr (mask_next) mask(step + 1);
+        frags(now, 3, 1);
+        if constexpr (store_next) store(next);
+        MX4_MULTIPLY(2, 0);
+        MX4_ORDER(1, 2, 0);
+        if constexpr (store_next) {
+            __syncthreads();
+            begin(next);
+        }
+        if constexpr (load_next) load(step + 2, Yes{});   // three steps or more: long rows
+        MX4_MULTIPLY(3, 1);
+        MX4_ORDER(1, 0, 2);
+        cur ^= 1;
+    };
+    if (first < last) {
+        load(first, No{});
+        if (first + 1 == steps_all) mask(first);
+        store(lds[0]);
+        if (first + 1 < last) load(first + 1, Yes{});
+        __syncthreads();
+        begin(lds[0]);
+        int step = first;
+        for (; step + 2 < last; ++step) body(step, Yes{}, No{}, Yes{});
+        if (step + 1 < last) body(step++, Yes{}, Yes{}, No{});
+        body(step, No{}, No{}, No{});
+    }
+#undef MX4_MULTIPLY
+#undef MX4_ORDER
+
+    const bool split = g.grid.parts > 1;
+    void* out = split ? (void*)(g.part + (int64_t)part * g.m * g.rows) : g.out;
+    const int kind = split ? (int)kOutFp32 : g.kind;
+    const int64_t n = n0 + wn * (32 * TN) + TN * r;
+    if (n >= g.rows) return;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int64_t row = m0 + (wm * TM + i) * 32 + 8 * (e >> 2) + 4 * h + (e & 3);
+            if (row < g.m) {
+                if constexpr (TN == 4) {
+                    store4(out, kind, row * g.rows + n, f32x4{acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]});
+                } else {
+                    static_assert(TN == 2, "two or four columns a lane");
+                    store2(out, kind, row * g.rows + n, f32x2{acc[i][0][e], acc[i][1][e]});
+                }
+            }
+        }
+}
+
+template <int TM, int TN>
+hipError_t mm4_go(Mm4Args a, hipStream_t s)
+{
+    const size_t bytes = 2 * sizeof(Buffer<TM, TN>);
+    const unsigned blocks = (unsigned)(a.grid.mt * a.grid.nt * a.grid.parts);
+    k_mm4<TM, TN><<<blocks, kThreads, bytes, s>>>(a);
+    return hipGetLastError();
+}
+
+// Which tile, and into how many parts the reduction goes.
+struct Plan {
+    bool big;
+    TileGrid grid;
+};
+
+Plan mm4_plan(int64_t rows, int64_t cols, int64_t m)
+{
+    const int steps = (int)ceil_div(cols, kStep);
+    Plan p;
+    p.big = ceil_div(m, 256) * ceil_div(rows, 256) >= 200;
+    const int bm = p.big ? 256 : 128;
+    p.grid = {(int)ceil_div(m, bm), (int)ceil_div(rows, bm), 1, steps};
+    const int64_t tiles = (int64_t)p.grid.mt * p.grid.nt;
+    if (!p.big && tiles < 256) {
+        int64_t parts = 512 / tiles;
+        if (parts > steps / 2) parts = steps / 2;
+        if (parts > 16) parts = 16;
+        if (parts > 1) {
+            p.grid.per_part = (int)ceil_div(steps, parts);
+            p.grid.parts = (int)ceil_div(steps, p.grid.per_part);
+        }
+    }
+    return p;
+}
+
+}  // namespace
+
+size_t mm4_tiled_ws(int64_t rows, int64_t cols, int64_t m)
+{
+    const Plan p = mm4_plan(rows, cols, m);
+    return p.grid.parts > 1 ? size_t(p.grid.parts) * size_t(m) * size_t(rows) * sizeof(float) : 0;
+}
+
+hipError_t launch_mm4_tiled(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                            const uint8_t* xcodes, const uint8_t* xscales, int64_t m, void* out, int out_kind,
+                            float* part, hipStream_t s)
+{
+    const Plan p = mm4_plan(rows, cols, m);
+    const Mm4Args a{codes, scales, xcodes, xscales, out, part, m, rows, (int)cols, out_kind, p.grid};
+    const hipError_t e = p.big ? mm4_go<4, 4>(a, s) : mm4_go<2, 2>(a, s);
+    if (e != hipSuccess || p.grid.parts == 1) return e;
+    return launch_split_sum(part, p.grid.parts, m * rows, out, out_kind, s);
+}
+
+}  // namespace mx4k

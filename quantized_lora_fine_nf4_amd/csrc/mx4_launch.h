@@ -28,6 +28,12 @@ hipError_t launch_matmul4(const uint8_t* codes, const uint8_t* scales, int64_t r
                           const uint8_t* xcodes, const uint8_t* xscales, int64_t m, void* out, int out_kind,
                           float* part, hipStream_t s);
 
+// Its tiled kernels (k_mx4_mm4.hip), for all but few tokens.
+size_t mm4_tiled_ws(int64_t rows, int64_t cols, int64_t m);
+hipError_t launch_mm4_tiled(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                            const uint8_t* xcodes, const uint8_t* xscales, int64_t m, void* out, int out_kind,
+                            float* part, hipStream_t s);
+
 // The sum of `splits` fp32 partials of n values each (a multiple of 8) in split
 // order, to out (mx4_sum.h).
 hipError_t launch_split_sum(const float* part, int splits, int64_t n, void* out, int out_kind, hipStream_t s);

@@ -7,8 +7,14 @@ namespace mx4k {
 
 enum OutKind { kOutBf16 = 0, kOutFp16 = 1, kOutFp32 = 2 };
 
-// Four or eight consecutive fp32 sums to the output type at element `at`
-// (a multiple of 4 or 8; 16-byte aligned buffer).
+// Two, four or eight consecutive fp32 sums to the output type at element `at`
+// (a multiple of their number; 16-byte aligned buffer).
+__device__ __forceinline__ void store2(void* out, int kind, int64_t at, const f32x2& v)
+{
+    if (kind == kOutFp32) *((MX4_GLOBAL f32x2*)((float*)out + at)) = v;
+    else *((MX4_GLOBAL uint32_t*)((uint16_t*)out + at)) = kind == kOutBf16 ? pack2<0>(v.x, v.y) : pack2<1>(v.x, v.y);
+}
+
 __device__ __forceinline__ void store4(void* out, int kind, int64_t at, const f32x4& v)
 {
     if (kind == kOutFp32) *((MX4_GLOBAL f32x4*)((float*)out + at)) = v;
