@@ -234,7 +234,8 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
     store8(out, kind, at, a, b);
 }
 
-constexpr int64_t kFewTokens4 = 64;   // up to here both operands in codes go through k_few
+// Both operands in codes: k_few up to 64 tokens, and where a row is shorter than a step of the tiled kernel.
+bool mm4_few(int64_t cols, int64_t m) { return m <= 64 || cols < 256; }
 
 int token_tiles(int64_t m) { return m <= 16 ? 1 : m <= 32 ? 2 : 4; }
 
@@ -297,13 +298,13 @@ hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales,
     return launch_split_sum(part, a.parts, m * cols, out, out_kind, s);
 }
 
-size_t matmul4_ws(int64_t rows, int64_t cols, int64_t m) { return m <= kFewTokens4 ? 0 : mm4_tiled_ws(rows, cols, m); }
+size_t matmul4_ws(int64_t rows, int64_t cols, int64_t m) { return mm4_few(cols, m) ? 0 : mm4_tiled_ws(rows, cols, m); }
 
 hipError_t launch_matmul4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                           const uint8_t* xcodes, const uint8_t* xscales, int64_t m, void* out, int out_kind,
                           float* part, hipStream_t s)
 {
-    if (m > kFewTokens4)
+    if (!mm4_few(cols, m))
         return launch_mm4_tiled(codes, scales, rows, cols, xcodes, xscales, m, out, out_kind, part, s);
     const FewArgs a{codes, scales, xcodes, xscales, out, nullptr, m, rows, cols, out_kind, 1};
     return few_go<2>(a, s);

@@ -9,10 +9,10 @@
 // 2,048 matrix cycles, 1,536 of the LDS's.  Eight waves of 128 x 64 would need
 // 256 KB, as many cycles as the matrix cores.
 //
-// A step is 256 columns: 128 bytes of codes and 8 scales of each row, through
-// registers into one of two LDS buffers while the other one is multiplied.  The
-// 16-byte pieces of a row are permuted by its index, so that eight lanes that read
-// eight rows touch all banks.  Weight row TN r + c of a wave's columns is row r of
+// A step is 256 columns: 128 bytes of codes and 8 scales of each row.  The codes go
+// straight to one of two LDS buffers (global_load_lds) while the other one is
+// multiplied.  The 16-byte pieces of a row are permuted by its index, so that eight
+// lanes that read eight rows touch all banks.  Weight row TN r + c of a wave's columns is row r of
 // its tile c: a lane ends with TN consecutive columns.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -34,10 +34,9 @@ constexpr int kThreads = 256;
 constexpr int kStep = 256;            // columns a step
 constexpr int kRowBytes = kStep / 2;
 constexpr int kGroups = kStep / kGroup;
+constexpr int kVmcnt0 = 0x0f70;       // s_waitcnt: vector memory only, none outstanding
 
-typedef std::integral_constant<bool, true> Yes;
-typedef std::integral_constant<bool, false> No;
-
+// cols >= kStep.
 struct Mm4Args {
     const uint8_t *codes, *scales, *xcodes, *xscales;
     void* out;
@@ -68,29 +67,14 @@ struct Buffer {
     u32x2 as[64 * TM], ws[64 * TN];
 };
 
-// The eight scales of a row of n from group `at` on.  LONG, n >= 8: those past the
-// row's end are dropped by the shift of mask() below; else they are zeros already.
-template <bool LONG>
-__device__ __forceinline__ uint64_t load_scales(const MX4_GLOBAL uint8_t* row, int at, int n)
-{
-    uint64_t v = 0;
-    if (LONG || n >= kGroups) {
-        __builtin_memcpy(&v, (const uint8_t*)row + (at + kGroups <= n ? at : n - kGroups), 8);
-    } else {
-        for (int i = at; i < n; ++i) v |= (uint64_t)row[i] << (8 * (i - at));
-    }
-    return v;
-}
-
 template <int TM, int TN>
 __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
 {
     typedef Shape<TM, TN> S;
-    extern __shared__ char lds_raw[];
-    Buffer<TM, TN>* lds = (Buffer<TM, TN>*)lds_raw;
+    __shared__ Buffer<TM, TN> b0, b1;   // two objects, so that reads of one need not wait for what comes into the other
     int tm, tn, part;
     tile_of(g.grid, blockIdx.x, tm, tn, part);
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, r = lane & 31, h = lane >> 5;
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), r = lane & 31, h = lane >> 5;
     const int wm = wave >> 1, wn = wave & 1;
     const int64_t m0 = (int64_t)tm * S::kBM, n0 = (int64_t)tn * S::kBN;
     const uint32_t pitch = (uint32_t)g.cols / 2;
@@ -98,8 +82,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     const int steps_all = (g.cols + kStep - 1) / kStep, first = part * g.grid.per_part;
     const int last = first + g.grid.per_part < steps_all ? first + g.grid.per_part : steps_all;
 
-    // this thread's pieces: rows t / 8 + 32 i, piece t % 8; offsets from the tile's first row
-    const int piece = t & 7;
+    // the rows t / 8 + 32 i of both operands, as offsets from the tile's first row
     uint32_t ao[S::kA], wo[S::kW];
 #pragma unroll
     for (int i = 0; i < S::kA; ++i) {
@@ -127,41 +110,37 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     const MX4_GLOBAL uint8_t* asp = (const MX4_GLOBAL uint8_t*)g.xscales + m0 * spitch + aso;
     const MX4_GLOBAL uint8_t* wsp = (const MX4_GLOBAL uint8_t*)g.scales + n0 * spitch + wso;
 
-    u32x4 ra[S::kA], rw[S::kW];
-    uint64_t ras, rws;
-    auto load = [&](int step, auto long_row) {
+    // the codes of a step: wave instructions of eight rows each; piece p of row i lies at p ^ (i & 7), and this
+    // thread fetches what belongs into slot t % 8 of rows t / 8 + 32 i
+    const int slot = t & 7, piece = slot ^ ((t >> 3) & 7);
+    auto fetch = [&](Buffer<TM, TN>& b, int step, auto from, auto to) {
         const int left = spitch - step * kGroups;
-        // a piece past the row's end: the step's first one, zeroed before it is stored
+        // a piece past the row's end: the step's first one, under scales of 0
         const uint32_t at = (uint32_t)step * kRowBytes + (piece < left ? 16 * piece : 0);
 #pragma unroll
-        for (int i = 0; i < S::kA; ++i) ra[i] = *(const MX4_GLOBAL u32x4*)(ap + (ao[i] + at));
-#pragma unroll
-        for (int i = 0; i < S::kW; ++i) rw[i] = *(const MX4_GLOBAL u32x4*)(wp + (wo[i] + at));
-        ras = load_scales<long_row>(asp, step * kGroups, spitch);
-        rws = load_scales<long_row>(wsp, step * kGroups, spitch);
-    };
-    const int swz = (t >> 3) * 8 + (piece ^ ((t >> 3) & 7));
-    auto mask = [&](int step) {
-        const int left = spitch - step * kGroups;
-        const uint32_t in = piece < left ? 0xffffffffu : 0u;
-        if (left < kGroups && spitch >= kGroups) {
-            ras >>= 8 * (kGroups - left);
-            rws >>= 8 * (kGroups - left);
+        for (int i = 0; i < S::kA + S::kW; ++i) {
+            if (i < from || i >= to) continue;
+            const MX4_GLOBAL uint8_t* src = i < S::kA ? ap + (ao[i < S::kA ? i : 0] + at) : wp + (wo[i < S::kA ? 0 : i - S::kA] + at);
+            u32x4* dst = (i < S::kA ? b.a + 256 * i : b.w + 256 * (i - S::kA)) + 64 * wave;
+            __builtin_amdgcn_global_load_lds((const MX4_GLOBAL uint32_t*)src, (MX4_LDS uint32_t*)dst, 16, 0, 0);
         }
-#pragma unroll
-        for (int i = 0; i < S::kA; ++i) ra[i] &= in;
-#pragma unroll
-        for (int i = 0; i < S::kW; ++i) rw[i] &= in;
     };
-    auto store = [&](Buffer<TM, TN>& b) {
-#pragma unroll
-        for (int i = 0; i < S::kA; ++i) b.a[swz + 256 * i] = ra[i];
-#pragma unroll
-        for (int i = 0; i < S::kW; ++i) b.w[swz + 256 * i] = rw[i];
+    uint64_t ras, rws;
+    auto fetch_scales = [&](int step) {
+        const int at = step * kGroups + kGroups <= spitch ? step * kGroups : spitch - kGroups;
+        __builtin_memcpy(&ras, (const uint8_t*)asp + at, 8);
+        __builtin_memcpy(&rws, (const uint8_t*)wsp + at, 8);
+    };
+    auto store_scales = [&](Buffer<TM, TN>& b, int step) {
+        // past the row's end: scales 0, 2^-254 for the two, so that those products are 0 in fp32 whatever the codes
+        const int left = spitch - step * kGroups, shift = left >= kGroups ? 0 : 8 * (kGroups - left);
         // threads past the tile's rows write the rows of others once more, to the same values
-        b.as[t % S::kBM] = __builtin_bit_cast(u32x2, ras);
-        b.ws[t % S::kBN] = __builtin_bit_cast(u32x2, rws);
+        b.as[t % S::kBM] = __builtin_bit_cast(u32x2, ras >> shift);
+        b.ws[t % S::kBN] = __builtin_bit_cast(u32x2, rws >> shift);
     };
+    typedef std::integral_constant<int, 0> Zero;
+    typedef std::integral_constant<int, (S::kA + S::kW) / 2> Half;
+    typedef std::integral_constant<int, S::kA + S::kW> All;
 
     f32x16 acc[TM][TN] = {};
     u32x4 fa[2][TM], fw[2][TN];
@@ -197,47 +176,57 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     }                                                                                                      \
     __builtin_amdgcn_sched_barrier(0)
 
-    int cur = 0;
-    // one step: STORE puts the next step into the other buffer (MASK: it may be the row's last), LOAD fetches the one after it
-    auto body = [&](int step, auto store_next, auto mask_next, auto load_next) {
-        const Buffer<TM, TN>& now = lds[cur];
-        Buffer<TM, TN>& next = lds[cur ^ 1];
+    // One step out of `now`.  The codes of the step after it are on their way to `next` (their first half was asked for
+    // in the step before).  Steps past the last one are the last one again, fetched and not used.
+    auto body = [&](Buffer<TM, TN>& now, Buffer<TM, TN>& next, int step) {
+        const int one = step + 1 < last ? step + 1 : last - 1, two = step + 2 < last ? step + 2 : last - 1;
 #pragma unroll
         for (int i = 0; i < TM; ++i) sa[i] = __builtin_amdgcn_perm(na[i][1], na[i][0], pick);
 #pragma unroll
         for (int j = 0; j < TN; ++j) sw[j] = __builtin_amdgcn_perm(nw[j][1], nw[j][0], pick);
+        fetch(next, one, Half{}, All{});
         frags(now, 1, 1);
         MX4_MULTIPLY(0, 0);
-        MX4_ORDER(1, 0, 0);
+        MX4_ORDER(1, 0, 1);
         frags(now, 2, 0);
         MX4_MULTIPLY(1, 1);
         MX4_ORDER(1, 0, 0);
-        if constexpr (mask_next) mask(step + 1);
         frags(now, 3, 1);
-        if constexpr (store_next) store(next);
         MX4_MULTIPLY(2, 0);
-        MX4_ORDER(1, 2, 0);
-        if constexpr (store_next) {
-            __syncthreads();
-            begin(next);
-        }
-        if constexpr (load_next) load(step + 2, Yes{});   // three steps or more: long rows
-        MX4_MULTIPLY(3, 1);
-        MX4_ORDER(1, 0, 2);
-        cur ^= 1;
-    };
-    if (first < last) {
-        load(first, No{});
-        if (first + 1 == steps_all) mask(first);
-        store(lds[0]);
-        if (first + 1 < last) load(first + 1, Yes{});
+        MX4_ORDER(1, 0, 0);
+        __builtin_amdgcn_s_waitcnt(kVmcnt0);
+        store_scales(next, one);
         __syncthreads();
-        begin(lds[0]);
-        int step = first;
-        for (; step + 2 < last; ++step) body(step, Yes{}, No{}, Yes{});
-        if (step + 1 < last) body(step++, Yes{}, Yes{}, No{});
-        body(step, No{}, No{}, No{});
+        begin(next);
+        fetch_scales(two);
+        fetch(now, two, Zero{}, Half{});
+        MX4_MULTIPLY(3, 1);
+        MX4_ORDER(1, 0, 1);
+    };
+    const int second = first + 1 < last ? first + 1 : first;
+    auto start = [&](Buffer<TM, TN>& b, Buffer<TM, TN>& other) {
+        fetch_scales(first);
+        fetch(b, first, Zero{}, All{});
+        __builtin_amdgcn_s_waitcnt(kVmcnt0);
+        store_scales(b, first);
+        __syncthreads();
+        begin(b);
+        fetch_scales(second);
+        fetch(other, second, Zero{}, Half{});
+    };
+    // an odd number of steps: one ahead of the pairs
+    int step = first;
+    if ((last - first) & 1) {
+        start(b1, b0);
+        body(b1, b0, step++);
+    } else {
+        start(b0, b1);
     }
+    for (; step < last; step += 2) {
+        body(b0, b1, step);
+        body(b1, b0, step + 1);
+    }
+    __builtin_amdgcn_s_waitcnt(kVmcnt0);   // nothing may come into LDS after the end
 #undef MX4_MULTIPLY
 #undef MX4_ORDER
 
@@ -265,9 +254,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
 template <int TM, int TN>
 hipError_t mm4_go(Mm4Args a, hipStream_t s)
 {
-    const size_t bytes = 2 * sizeof(Buffer<TM, TN>);
     const unsigned blocks = (unsigned)(a.grid.mt * a.grid.nt * a.grid.parts);
-    k_mm4<TM, TN><<<blocks, kThreads, bytes, s>>>(a);
+    k_mm4<TM, TN><<<blocks, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 

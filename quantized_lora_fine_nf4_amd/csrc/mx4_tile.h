@@ -23,12 +23,12 @@ __device__ __forceinline__ void tile_of(const TileGrid& g, int b, int& tm, int& 
 {
     const int total = g.mt * g.nt * g.parts, q = total / 8, r = total % 8, x = b % 8;
     int t = x * q + (x < r ? x : r) + b / 8;
-    part = t % g.parts;
+    part = __builtin_amdgcn_readfirstlane(t % g.parts);
     t /= g.parts;
     const int band = t / (kBand * g.nt), left = g.mt - band * kBand, h = left < kBand ? left : kBand;
     const int in = t - band * kBand * g.nt;
-    tm = band * kBand + in % h;
-    tn = in / h;
+    tm = __builtin_amdgcn_readfirstlane(band * kBand + in % h);
+    tn = __builtin_amdgcn_readfirstlane(in / h);
 }
 
 }  // namespace mx4k
