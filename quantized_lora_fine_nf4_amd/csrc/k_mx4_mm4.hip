@@ -54,6 +54,9 @@ __device__ __forceinline__ f32x16 mfma4(const u32x4& a, uint32_t sa, const u32x4
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
+template <int K>
+using Kind = std::integral_constant<int, K>;
+
 // A wave's tile: TM x TN tiles of 32 x 32; the workgroup's: 2 x 2 waves.
 template <int TM, int TN>
 struct Shape {
@@ -125,6 +128,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
             __builtin_amdgcn_global_load_lds((const MX4_GLOBAL uint32_t*)src, (MX4_LDS uint32_t*)dst, 16, 0, 0);
         }
     };
+    auto clamp = [&](int step) { return step < last ? step : last - 1; };
     uint64_t ras, rws;
     auto fetch_scales = [&](int step) {
         const int at = step * kGroups + kGroups <= spitch ? step * kGroups : spitch - kGroups;
@@ -132,11 +136,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
         __builtin_memcpy(&rws, (const uint8_t*)wsp + at, 8);
     };
     auto store_scales = [&](Buffer<TM, TN>& b, int step) {
-        // past the row's end: scales 0, 2^-254 for the two, so that those products are 0 in fp32 whatever the codes
-        const int left = spitch - step * kGroups, shift = left >= kGroups ? 0 : 8 * (kGroups - left);
+        // past the row's end, and past the last step: scales 0, 2^-254 for the two, so that those products are 0 in
+        // fp32 whatever the codes
+        const int left = spitch - step * kGroups, shift = left >= kGroups || left <= 0 ? 0 : 8 * (kGroups - left);
+        const uint64_t in = step < last ? ~0ull : 0ull;
         // threads past the tile's rows write the rows of others once more, to the same values
-        b.as[t % S::kBM] = __builtin_bit_cast(u32x2, ras >> shift);
-        b.ws[t % S::kBN] = __builtin_bit_cast(u32x2, rws >> shift);
+        b.as[t % S::kBM] = __builtin_bit_cast(u32x2, ras >> shift & in);
+        b.ws[t % S::kBN] = __builtin_bit_cast(u32x2, rws >> shift & in);
     };
     typedef std::integral_constant<int, 0> Zero;
     typedef std::integral_constant<int, (S::kA + S::kW) / 2> Half;
@@ -179,12 +185,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     // One step out of `now`.  The codes of the step after it are on their way to `next` (their first half was asked for
     // in the step before).  Steps past the last one are the last one again, fetched and not used.
     auto body = [&](Buffer<TM, TN>& now, Buffer<TM, TN>& next, int step) {
-        const int one = step + 1 < last ? step + 1 : last - 1, two = step + 2 < last ? step + 2 : last - 1;
 #pragma unroll
         for (int i = 0; i < TM; ++i) sa[i] = __builtin_amdgcn_perm(na[i][1], na[i][0], pick);
 #pragma unroll
         for (int j = 0; j < TN; ++j) sw[j] = __builtin_amdgcn_perm(nw[j][1], nw[j][0], pick);
-        fetch(next, one, Half{}, All{});
+        fetch(next, clamp(step + 1), Half{}, All{});
         frags(now, 1, 1);
         MX4_MULTIPLY(0, 0);
         MX4_ORDER(1, 0, 1);
@@ -195,34 +200,24 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
         MX4_MULTIPLY(2, 0);
         MX4_ORDER(1, 0, 0);
         __builtin_amdgcn_s_waitcnt(kVmcnt0);
-        store_scales(next, one);
+        store_scales(next, step + 1);
         __syncthreads();
         begin(next);
-        fetch_scales(two);
-        fetch(now, two, Zero{}, Half{});
+        fetch_scales(clamp(step + 2));
+        fetch(now, clamp(step + 2), Zero{}, Half{});
         MX4_MULTIPLY(3, 1);
         MX4_ORDER(1, 0, 1);
     };
-    const int second = first + 1 < last ? first + 1 : first;
-    auto start = [&](Buffer<TM, TN>& b, Buffer<TM, TN>& other) {
-        fetch_scales(first);
-        fetch(b, first, Zero{}, All{});
-        __builtin_amdgcn_s_waitcnt(kVmcnt0);
-        store_scales(b, first);
-        __syncthreads();
-        begin(b);
-        fetch_scales(second);
-        fetch(other, second, Zero{}, Half{});
-    };
-    // an odd number of steps: one ahead of the pairs
-    int step = first;
-    if ((last - first) & 1) {
-        start(b1, b0);
-        body(b1, b0, step++);
-    } else {
-        start(b0, b1);
-    }
-    for (; step < last; step += 2) {
+    fetch_scales(first);
+    fetch(b0, first, Zero{}, All{});
+    __builtin_amdgcn_s_waitcnt(kVmcnt0);
+    store_scales(b0, first);
+    __syncthreads();
+    begin(b0);
+    fetch_scales(clamp(first + 1));
+    fetch(b1, clamp(first + 1), Zero{}, Half{});
+    // pairs of steps: an odd one is followed by one under scales of 0
+    for (int step = first; step < last; step += 2) {
         body(b0, b1, step);
         body(b1, b0, step + 1);
     }
@@ -230,25 +225,44 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
 #undef MX4_MULTIPLY
 #undef MX4_ORDER
 
-    const bool split = g.grid.parts > 1;
-    void* out = split ? (void*)(g.part + (int64_t)part * g.m * g.rows) : g.out;
+    const bool split = g.grid.parts > 1, whole = m0 + S::kBM <= g.m;
+    char* out = split ? (char*)(g.part + (int64_t)part * g.m * g.rows) : (char*)g.out;
     const int kind = split ? (int)kOutFp32 : g.kind;
-    const int64_t n = n0 + wn * (32 * TN) + TN * r;
-    if (n >= g.rows) return;
+    const int col = wn * (32 * TN) + TN * r;
+    if (n0 + col >= g.rows) return;
+    // lane (r, h): columns from `col` on of rows 8 a + 4 h + b of each 32
+    auto put = [&](auto k, auto all) {
+        constexpr int kBytes = k == kOutFp32 ? 4 : 2;
+        char* base = out + ((m0 + wm * (32 * TM)) * g.rows + n0) * kBytes;   // uniform
+        const uint32_t at = (uint32_t)(4 * h * g.rows + col) * kBytes;
+        const int64_t pitch_out = g.rows * kBytes;
+        const int left = (int)(all || g.m - m0 > S::kBM ? S::kBM : g.m - m0) - wm * (32 * TM) - 4 * h;
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i) {
+            // one row of tiles at a time out of the accumulation registers: moved all at once the sums spill
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int64_t row = m0 + (wm * TM + i) * 32 + 8 * (e >> 2) + 4 * h + (e & 3);
-            if (row < g.m) {
-                if constexpr (TN == 4) {
-                    store4(out, kind, row * g.rows + n, f32x4{acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]});
-                } else {
-                    static_assert(TN == 2, "two or four columns a lane");
-                    store2(out, kind, row * g.rows + n, f32x2{acc[i][0][e], acc[i][1][e]});
+            for (int k2 = i; k2 < TM; ++k2)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) __asm__ volatile("" : "+a"(acc[k2][j]));
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int row = i * 32 + 8 * (e >> 2) + (e & 3);
+                if (all || row < left) {
+                    MX4_GLOBAL char* p = (MX4_GLOBAL char*)base + row * pitch_out;
+                    if constexpr (TN == 4) put4<k>(p + at, f32x4{acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]});
+                    else put2<k>(p + at, f32x2{acc[i][0][e], acc[i][1][e]});
                 }
             }
         }
+    };
+    auto of_kind = [&](auto all) {
+        if (kind == kOutBf16) put(Kind<kOutBf16>{}, all);
+        else if (kind == kOutFp16) put(Kind<kOutFp16>{}, all);
+        else put(Kind<kOutFp32>{}, all);
+    };
+    if (whole) of_kind(std::true_type{});
+    else of_kind(std::false_type{});
 }
 
 template <int TM, int TN>
