@@ -70,6 +70,25 @@ struct Buffer {
     u32x2 as[64 * TM], ws[64 * TN];
 };
 
+// READS LDS reads and LOADS loads spread over N matrix instructions (the reads over
+// the first three quarters, the next sub-step begins with what they bring): four
+// waves share the LDS and the address unit, and what is bunched waits there while
+// the matrix cores are idle.
+template <int N, int READS, int LOADS, int I = 0>
+__device__ __forceinline__ void spread()
+{
+    if constexpr (I < N) {
+        constexpr int kOver = N * 3 / 4, kTo = I + 1 < kOver ? I + 1 : kOver, kFrom = I < kOver ? I : kOver;
+        constexpr int kReads = kTo * READS / kOver - kFrom * READS / kOver, kLoads = (I + 1) * LOADS / N - I * LOADS / N;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if constexpr (kReads > 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+        if constexpr (kLoads > 0) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);
+        spread<N, READS, LOADS, I + 1>();
+    } else {
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 template <int TM, int TN>
 __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
 {
@@ -145,7 +164,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
         b.ws[t % S::kBN] = __builtin_bit_cast(u32x2, rws >> shift & in);
     };
     typedef std::integral_constant<int, 0> Zero;
-    typedef std::integral_constant<int, (S::kA + S::kW) / 2> Half;
+    typedef std::integral_constant<int, (S::kA + S::kW) / 3> Third;
+    typedef std::integral_constant<int, 2 * (S::kA + S::kW) / 3> TwoThirds;
     typedef std::integral_constant<int, S::kA + S::kW> All;
 
     f32x16 acc[TM][TN] = {};
@@ -155,10 +175,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     u32x2 na[TM], nw[TN];
     auto frags = [&](const Buffer<TM, TN>& b, int s, int to) {
         const int at = r * 8 + ((2 * s + h) ^ (r & 7));
-#pragma unroll
-        for (int i = 0; i < TM; ++i) fa[to][i] = b.a[(wm * TM + i) * 256 + at];
+        // in the order of their use
+        fa[to][0] = b.a[wm * TM * 256 + at];
 #pragma unroll
         for (int i = 0; i < TN; ++i) fw[to][i] = b.w[(wn * TN + i) * 256 + at];
+#pragma unroll
+        for (int i = 1; i < TM; ++i) fa[to][i] = b.a[(wm * TM + i) * 256 + at];
     };
     // the first sub-step's fragments and the scales of a step
     auto begin = [&](const Buffer<TM, TN>& b) {
@@ -172,41 +194,32 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     _Pragma("unroll") for (int i = 0; i < TM; ++i)                                                         \
         _Pragma("unroll") for (int j = 0; j < TN; ++j)                                                     \
             acc[i][j] = mfma4<SUB>(fa[FROM][i], sa[i], fw[FROM][j], sw[j], acc[i][j])
-// matrix instructions with the given numbers of LDS reads, LDS writes and loads among them
-#define MX4_ORDER(READS, WRITES, LOADS)                                                                    \
-    _Pragma("unroll") for (int i = 0; i < TM * TN; ++i) {                                                  \
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                                 \
-        if (READS) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);                                  \
-        if (WRITES) __builtin_amdgcn_sched_group_barrier(0x200, WRITES, 0);                                \
-        if (LOADS) __builtin_amdgcn_sched_group_barrier(0x020, LOADS, 0);                                  \
-    }                                                                                                      \
-    __builtin_amdgcn_sched_barrier(0)
-
-    // One step out of `now`.  The codes of the step after it are on their way to `next` (their first half was asked for
+    // One step out of `now`.  The codes of the step after it are on their way to `next` (their first third was asked for
     // in the step before).  Steps past the last one are the last one again, fetched and not used.
     auto body = [&](Buffer<TM, TN>& now, Buffer<TM, TN>& next, int step) {
 #pragma unroll
         for (int i = 0; i < TM; ++i) sa[i] = __builtin_amdgcn_perm(na[i][1], na[i][0], pick);
 #pragma unroll
         for (int j = 0; j < TN; ++j) sw[j] = __builtin_amdgcn_perm(nw[j][1], nw[j][0], pick);
-        fetch(next, clamp(step + 1), Half{}, All{});
+        fetch(next, clamp(step + 1), Third{}, TwoThirds{});
         frags(now, 1, 1);
         MX4_MULTIPLY(0, 0);
-        MX4_ORDER(1, 0, 1);
+        spread<TM * TN, TM + TN, TwoThirds::value - Third::value>();
+        fetch(next, clamp(step + 1), TwoThirds{}, All{});
         frags(now, 2, 0);
         MX4_MULTIPLY(1, 1);
-        MX4_ORDER(1, 0, 0);
+        spread<TM * TN, TM + TN, All::value - TwoThirds::value>();
         frags(now, 3, 1);
         MX4_MULTIPLY(2, 0);
-        MX4_ORDER(1, 0, 0);
+        spread<TM * TN, TM + TN, 0>();
         __builtin_amdgcn_s_waitcnt(kVmcnt0);
         store_scales(next, step + 1);
         __syncthreads();
         begin(next);
         fetch_scales(clamp(step + 2));
-        fetch(now, clamp(step + 2), Zero{}, Half{});
+        fetch(now, clamp(step + 2), Zero{}, Third{});
         MX4_MULTIPLY(3, 1);
-        MX4_ORDER(1, 0, 1);
+        spread<TM * TN, 2 * (TM + TN), Third::value + 2>();
     };
     fetch_scales(first);
     fetch(b0, first, Zero{}, All{});
@@ -215,7 +228,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     __syncthreads();
     begin(b0);
     fetch_scales(clamp(first + 1));
-    fetch(b1, clamp(first + 1), Zero{}, Half{});
+    fetch(b1, clamp(first + 1), Zero{}, Third{});
     // pairs of steps: an odd one is followed by one under scales of 0
     for (int step = first; step < last; step += 2) {
         body(b0, b1, step);
@@ -223,7 +236,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     }
     __builtin_amdgcn_s_waitcnt(kVmcnt0);   // nothing may come into LDS after the end
 #undef MX4_MULTIPLY
-#undef MX4_ORDER
 
     const bool split = g.grid.parts > 1, whole = m0 + S::kBM <= g.m;
     char* out = split ? (char*)(g.part + (int64_t)part * g.m * g.rows) : (char*)g.out;
