@@ -41,7 +41,7 @@ struct Mm4Args {
     const uint8_t *codes, *scales, *xcodes, *xscales;
     void* out;
     float* part;   // parts > 1: fp32 [parts][m x rows]
-    int64_t m, rows;
+    int64_t m, rows, ldo;   // ldo: out's row pitch
     int cols, kind;
     TileGrid grid;
 };
@@ -238,16 +238,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
 #undef MX4_MULTIPLY
 
     const bool split = g.grid.parts > 1, whole = m0 + S::kBM <= g.m;
-    char* out = split ? (char*)(g.part + (int64_t)part * g.m * g.rows) : (char*)g.out;
+    char* out = split ? (char*)(g.part + (int64_t)part * g.m * g.ldo) : (char*)g.out;
     const int kind = split ? (int)kOutFp32 : g.kind;
     const int col = wn * (32 * TN) + TN * r;
     if (n0 + col >= g.rows) return;
     // lane (r, h): columns from `col` on of rows 8 a + 4 h + b of each 32
     auto put = [&](auto k, auto all) {
         constexpr int kBytes = k == kOutFp32 ? 4 : 2;
-        char* base = out + ((m0 + wm * (32 * TM)) * g.rows + n0) * kBytes;   // uniform
-        const uint32_t at = (uint32_t)(4 * h * g.rows + col) * kBytes;
-        const int64_t pitch_out = g.rows * kBytes;
+        char* base = out + ((m0 + wm * (32 * TM)) * g.ldo + n0) * kBytes;   // uniform
+        const uint32_t at = (uint32_t)(4 * h * g.ldo + col) * kBytes;
+        const int64_t pitch_out = g.ldo * kBytes;
         const int left = (int)(all || g.m - m0 > S::kBM ? S::kBM : g.m - m0) - wm * (32 * TM) - 4 * h;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
@@ -285,27 +285,41 @@ hipError_t mm4_go(Mm4Args a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Which tile, and into how many parts the reduction goes.
+// Which tiles, and into how many parts the reduction goes.
 struct Plan {
-    bool big;
-    TileGrid grid;
+    TileGrid big;      // 256 x 256 tiles on the first big.nt * 256 columns (nt 0: none)
+    TileGrid small;    // 128 x 128 tiles on the others (nt 0: none)
 };
 
+constexpr int kCus = 256;
+
+// 200 tiles of 256 x 256 or more: whole rounds of them, one on each compute unit.
+// Tiles beyond the last whole round of at most three quarters of one run as four
+// small ones each, two on a compute unit (4096 x 13824 x 5120, 3.4 rounds: SMALL us
+// instead of 188).  Below 200 tiles small ones, with fewer than 256 of those the
+// reduction split.
 Plan mm4_plan(int64_t rows, int64_t cols, int64_t m)
 {
     const int steps = (int)ceil_div(cols, kStep);
-    Plan p;
-    p.big = ceil_div(m, 256) * ceil_div(rows, 256) >= 200;
-    const int bm = p.big ? 256 : 128;
-    p.grid = {(int)ceil_div(m, bm), (int)ceil_div(rows, bm), 1, steps};
-    const int64_t tiles = (int64_t)p.grid.mt * p.grid.nt;
-    if (!p.big && tiles < 256) {
+    Plan p = {};
+    const int64_t mt = ceil_div(m, 256), nt = ceil_div(rows, 256);
+    if (mt * nt >= 200) {
+        const int64_t rounds = mt * nt / kCus, whole = rounds * kCus / mt;
+        const bool cut = rounds > 0 && whole > 0 && whole < nt && 4 * (mt * (nt - whole)) <= 3 * kCus;
+        const int64_t nb = cut ? whole : nt;
+        p.big = {(int)mt, (int)nb, 1, steps};
+        if (cut) p.small = {(int)ceil_div(m, 128), (int)ceil_div(rows - 256 * nb, 128), 1, steps};
+        return p;
+    }
+    p.small = {(int)ceil_div(m, 128), (int)ceil_div(rows, 128), 1, steps};
+    const int64_t tiles = (int64_t)p.small.mt * p.small.nt;
+    if (tiles < 256) {
         int64_t parts = 512 / tiles;
         if (parts > steps / 2) parts = steps / 2;
         if (parts > 16) parts = 16;
         if (parts > 1) {
-            p.grid.per_part = (int)ceil_div(steps, parts);
-            p.grid.parts = (int)ceil_div(steps, p.grid.per_part);
+            p.small.per_part = (int)ceil_div(steps, parts);
+            p.small.parts = (int)ceil_div(steps, p.small.per_part);
         }
     }
     return p;
@@ -316,7 +330,7 @@ Plan mm4_plan(int64_t rows, int64_t cols, int64_t m)
 size_t mm4_tiled_ws(int64_t rows, int64_t cols, int64_t m)
 {
     const Plan p = mm4_plan(rows, cols, m);
-    return p.grid.parts > 1 ? size_t(p.grid.parts) * size_t(m) * size_t(rows) * sizeof(float) : 0;
+    return p.small.parts > 1 ? size_t(p.small.parts) * size_t(m) * size_t(rows) * sizeof(float) : 0;
 }
 
 hipError_t launch_mm4_tiled(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
@@ -324,10 +338,21 @@ hipError_t launch_mm4_tiled(const uint8_t* codes, const uint8_t* scales, int64_t
                             float* part, hipStream_t s)
 {
     const Plan p = mm4_plan(rows, cols, m);
-    const Mm4Args a{codes, scales, xcodes, xscales, out, part, m, rows, (int)cols, out_kind, p.grid};
-    const hipError_t e = p.big ? mm4_go<4, 4>(a, s) : mm4_go<2, 2>(a, s);
-    if (e != hipSuccess || p.grid.parts == 1) return e;
-    return launch_split_sum(part, p.grid.parts, m * rows, out, out_kind, s);
+    Mm4Args a{codes, scales, xcodes, xscales, out, part, m, rows, rows, (int)cols, out_kind, p.big};
+    if (p.big.nt > 0) {
+        const int64_t done = 256 * (int64_t)p.big.nt;
+        if (p.small.nt > 0) a.rows = done;
+        const hipError_t e = mm4_go<4, 4>(a, s);
+        if (e != hipSuccess || p.small.nt == 0) return e;
+        a.codes += done * (cols / 2);
+        a.scales += done * (cols / kGroup);
+        a.out = (char*)out + done * (out_kind == kOutFp32 ? 4 : 2);
+        a.rows = rows - done;
+    }
+    a.grid = p.small;
+    const hipError_t e = mm4_go<2, 2>(a, s);
+    if (e != hipSuccess || p.small.parts == 1) return e;
+    return launch_split_sum(part, p.small.parts, m * rows, out, out_kind, s);
 }
 
 }  // namespace mx4k
