@@ -234,6 +234,8 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
     store8(out, kind, at, a, b);
 }
 
+bool mm_few(int64_t m) { return m <= 64; }
+
 // Both operands in codes: k_few up to 64 tokens, and where a row is shorter than a step of the tiled kernel.
 bool mm4_few(int64_t cols, int64_t m) { return m <= 64 || cols < 256; }
 
@@ -282,6 +284,7 @@ hipError_t launch_split_sum(const float* part, int splits, int64_t n, void* out,
 
 size_t matmul_ws(int64_t rows, int64_t cols, bool forward, int64_t m)
 {
+    if (!mm_few(m)) return forward ? mm_tiled_ws(cols, rows, m) : mm_tiled_ws(rows, cols, m);
     if (forward) return 0;
     const int parts = back_parts(rows, cols, m);
     return parts > 1 ? size_t(parts) * size_t(m) * size_t(cols) * sizeof(float) : 0;
@@ -290,6 +293,7 @@ size_t matmul_ws(int64_t rows, int64_t cols, bool forward, int64_t m)
 hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                          bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s)
 {
+    if (!mm_few(m)) return launch_mm_tiled(dtype, codes, scales, rows, cols, forward, x, m, out, out_kind, part, s);
     FewArgs a{codes, scales, x, nullptr, out, part, m, rows, cols, out_kind, 1};
     if (forward) return dtype == 0 ? few_go<0>(a, s) : few_go<1>(a, s);
     a.parts = back_parts(rows, cols, m);

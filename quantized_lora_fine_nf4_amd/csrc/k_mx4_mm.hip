@@ -1,0 +1,367 @@
+// k_mx4_mm.hip -- the product of a 16-bit operand and a microscaled 4-bit weight
+// on gfx950 matrix cores: out = x W^T (forward) or x W (backward).
+//
+// v_mfma_f32_32x32x16; a 256 x 256 output tile by four waves of 128 x 128, one per
+// SIMD.  A step is 64 of the reduction: x's rows (128 bytes each) and the weight's
+// codes go straight into one of two LDS buffers while the other is multiplied.  The
+// codes leave LDS as codes: each wave converts the fragments it multiplies, two
+// values an instruction, in the shadow of the matrix instructions; the weight is
+// never written anywhere in 16 bits.
+//
+// Forward: lane (r, h) reads row r's 16 bytes of block h of the step, one scale
+// under which its four dwords become the fragments of the four sub-steps
+// (reduction index 32 h + 8 f + j).  Backward the reduction runs over the weight's
+// rows, whose scales differ: lane (r, h) reads its TN columns of rows 32 h + 8 f + j,
+// j = 0 .. 7, converts each row's byte (two columns) under that row's scale, and
+// two rows' halves are put together as pairs of the fragments.
+//
+// Weight row (column, backward) TN r + c of a wave's part is row r of its tile c,
+// so that a lane ends with TN consecutive columns.  16-byte pieces of x's rows lie
+// permuted by the row's index, so that eight lanes that read eight rows touch all
+// banks.  x comes through a buffer descriptor that ends with it: rows past its end,
+// and pieces past a row's end (offset kFar), arrive as zeros.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx4_format.h"
+#include "mx4_launch.h"
+#include "mx4_sum.h"
+#include "mx4_tile.h"
+
+namespace mx4k {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kStep = 64;             // of the reduction
+constexpr uint32_t kFar = 0x80000000u;
+
+struct MmArgs {
+    const uint8_t *codes, *scales;    // W [rows x cols]
+    const uint16_t* x;                // [m x kred]
+    void* out;                        // [m x ncol], row pitch ldo
+    float* part;                      // parts > 1: fp32 [parts][m x ldo]
+    int64_t m, ncol, ldo;
+    int cols, kred, kind;
+    TileGrid grid;
+};
+
+template <int DT>
+__device__ __forceinline__ f32x16 mfma16(const u32x4& a, const u32x4& b, const f32x16& c)
+{
+    if constexpr (DT == 0)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <int TM, int TN>
+struct Buffer {
+    u32x4 a[64 * TM * 8];       // x: 64 TM rows of 128 bytes
+    u32x4 w[64 * TN * 2];       // codes: forward 64 TN rows of 32 bytes, backward 64 rows of 32 TN
+    uint8_t s[128 * TN];        // scales: forward [64 TN rows][2], backward [2 TN groups][64 rows]
+};
+
+__device__ __forceinline__ uint32_t low16(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high16(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+template <int DT, bool FWD, int TM, int TN>
+__global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
+{
+    typedef Buffer<TM, TN> Buf;
+    __shared__ Buf b0, b1;   // two objects, so that reads of one need not wait for what comes into the other
+    constexpr int kBM = 64 * TM, kBN = 64 * TN;
+    constexpr int kA = 2 * TM, kW = TN / 2;   // 16-byte pieces per thread and step
+    int tm, tn, part;
+    tile_of(g.grid, blockIdx.x, tm, tn, part);
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), r = lane & 31, h = lane >> 5;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int64_t m0 = (int64_t)tm * kBM, n0 = (int64_t)tn * kBN;
+    const int steps_all = (g.kred + kStep - 1) / kStep, first = part * g.grid.per_part;
+    const int last = first + g.grid.per_part < steps_all ? first + g.grid.per_part : steps_all;
+    const uint32_t wpitch = (uint32_t)g.cols / 2;
+    const int spitch = g.cols / kGroup;
+
+    // x: this thread fetches slot t % 8 of rows t / 8 + 32 i, which holds piece (t % 8) ^ (row % 8)
+    const uint32_t xpitch = (uint32_t)g.kred * 2;
+    const int64_t xleft = (g.m - m0 < kBM ? g.m - m0 : kBM) * xpitch;
+    const __amdgpu_buffer_rsrc_t xr =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(g.x + m0 * g.kred), 0, (int)xleft, 0x00027000);
+    const int piece = (t & 7) ^ ((t >> 3) & 7);
+    const uint32_t ao = (uint32_t)(t >> 3) * xpitch + 16 * piece;
+    auto fetch_x = [&](Buf& b, int step, auto from, auto to) {
+        const bool in = step < last && step * kStep + 8 * piece < g.kred;
+        const uint32_t at = in ? ao + (uint32_t)step * (2 * kStep) : kFar;
+#pragma unroll
+        for (int i = from; i < to; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (MX4_LDS uint32_t*)(b.a + 256 * i + 64 * wave), 16,
+                                                     at + (uint32_t)i * (32 * xpitch), 0, 0, 0);
+    };
+    // codes.  Forward: two pieces a row, LDS row t / 2 + 128 i, slot (t & 1) holds piece (t & 1) ^ (row / 4 & 1).
+    // Backward: 2 TN pieces a row, row t / (2 TN) of the step (and 32 below with TN = 4).
+    const MX4_GLOBAL uint8_t* wp = (const MX4_GLOBAL uint8_t*)g.codes;
+    int64_t wo[kW];
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+        if constexpr (FWD) {
+            const int l = (t >> 1) + 128 * i;
+            const int64_t n = n0 + l / (32 * TN) * (32 * TN) + TN * (l % 32) + l / 32 % TN;
+            wo[i] = (n < g.ncol ? n : g.ncol - 1) * wpitch;
+        } else {
+            const int64_t c = n0 + 32 * (t % (2 * TN));
+            wo[i] = (c < g.ncol ? c : n0) / 2;
+        }
+    }
+    auto fetch_w = [&](Buf& b, int step) {
+        const int s = step < last ? step : last - 1;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            const MX4_GLOBAL uint8_t* src;
+            if constexpr (FWD) {
+                const int p = (t & 1) ^ ((t >> 3) & 1);   // past the row's end: the step's first piece, under scale 0
+                src = wp + wo[i] + (s * (kStep / 2) + (s * kStep + 32 * p < g.kred ? 16 * p : 0));
+            } else {
+                const int n = s * kStep + t / (2 * TN) + 32 * i;
+                src = wp + wo[i] + (int64_t)(n < g.kred ? n : g.kred - 1) * wpitch;
+            }
+            __builtin_amdgcn_global_load_lds((const MX4_GLOBAL uint32_t*)src, (MX4_LDS uint32_t*)(b.w + 256 * i + 64 * wave), 16, 0, 0);
+        }
+    };
+    // scales: forward byte t & 1 of row t / 2 + 128 i; backward group t % 4 + 4 i of row t / 4
+    const MX4_GLOBAL uint8_t* sp = (const MX4_GLOBAL uint8_t*)g.scales;
+    uint32_t rs[kW];
+    auto fetch_s = [&](int step) {
+        const int s = step < last ? step : last - 1;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            if constexpr (FWD) {
+                const int b = 2 * s + (t & 1);
+                rs[i] = sp[wo[i] / 16 + (b < spitch ? b : spitch - 1)];
+            } else {
+                const int n = s * kStep + (t >> 2);
+                const int64_t c = n0 / kGroup + (t & 3) + 4 * i;
+                rs[i] = sp[(int64_t)(n < g.kred ? n : g.kred - 1) * spitch + (c < g.ncol / kGroup ? c : 0)];
+            }
+        }
+    };
+    auto store_s = [&](Buf& b, int step) {
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            // past the end: 0 and not NaN, against zeros of x
+            if constexpr (FWD) {
+                const bool in = step < last && 2 * step + (t & 1) < spitch;
+                b.s[t + 256 * i] = (uint8_t)(in ? rs[i] : 0u);
+            } else {
+                const bool in = step < last && step * kStep + (t >> 2) < g.kred;
+                b.s[((t & 3) + 4 * i) * 64 + (t >> 2)] = (uint8_t)(in ? rs[i] : 0u);
+            }
+        }
+    };
+
+    f32x16 acc[TM][TN] = {};
+    u32x4 fa[2][TM], fw[2][TN];
+    auto frags = [&](const Buf& b, int f, int to) {
+        const int at = r * 8 + ((4 * h + f) ^ (r & 7));
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[to][i] = b.a[(wm * TM + i) * 256 + at];
+    };
+    // forward: a step's codes and scale arguments; backward: a sub-step's
+    u32x4 code[TN];
+    float scale[TN];
+    uint32_t raw[8];
+    u32x2 rawscale;
+    auto read_step = [&](const Buf& b) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int l = (wn * TN + j) * 32 + r;
+            code[j] = b.w[l * 2 + (h ^ ((l >> 2) & 1))];
+            scale[j] = __builtin_bit_cast(float, (uint32_t)b.s[2 * l + h]);
+        }
+    };
+    auto read_sub = [&](const Buf& b, int f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint8_t* p = (const uint8_t*)b.w + (32 * h + 8 * f + j) * (32 * TN) + wn * (16 * TN) + r * (TN / 2);
+            if constexpr (TN == 4) raw[j] = *(const uint16_t*)p;
+            else raw[j] = *p;
+        }
+        rawscale = *(const u32x2*)(b.s + (wn * TN + r * TN / 32) * 64 + 32 * h + 8 * f);
+    };
+    auto shift_scales = [&]() {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) scale[j] = scale_arg(__builtin_bit_cast(uint32_t, scale[j]));
+    };
+    auto decode = [&](int f, int to) {
+        if constexpr (FWD) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fw[to][j] = decode8<DT>(code[j][f], scale[j]);
+        } else {
+            float s[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = scale_arg((rawscale[j >> 2] >> (8 * (j & 3))) & 255);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t p = decode2<DT, 0>(raw[2 * j], s[2 * j]), q = decode2<DT, 0>(raw[2 * j + 1], s[2 * j + 1]);
+                fw[to][0][j] = low16(p, q);
+                fw[to][1][j] = high16(p, q);
+                if constexpr (TN == 4) {
+                    const uint32_t u = decode2<DT, 1>(raw[2 * j], s[2 * j]), v = decode2<DT, 1>(raw[2 * j + 1], s[2 * j + 1]);
+                    fw[to][2][j] = low16(u, v);
+                    fw[to][3][j] = high16(u, v);
+                }
+            }
+        }
+    };
+    auto multiply = [&](int from) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma16<DT>(fa[from][i], fw[from][j], acc[i][j]);
+    };
+    constexpr int kN = TM * TN;
+    constexpr int kReads = FWD ? TM : TM + 9, kValu = FWD ? 4 * TN : 8 * TN + 16;
+    typedef std::integral_constant<int, 0> Zero;
+    typedef std::integral_constant<int, kA / 2> Half;
+    typedef std::integral_constant<int, kA> All;
+
+    // One step out of `now`: each sub-step reads and converts what the next one multiplies.  The step after it is on
+    // its way to `next`; steps past the last one are zeros under scales of 0.
+    auto body = [&](Buf& now, Buf& next, int step) {
+        fetch_x(next, step + 1, Half{}, All{});
+        frags(now, 1, 1);
+        if constexpr (!FWD) read_sub(now, 1);
+        decode(1, 1);
+        multiply(0);
+        spread<kN, kReads, kValu, kA / 2>();
+        fetch_w(next, step + 1);
+        frags(now, 2, 0);
+        if constexpr (!FWD) read_sub(now, 2);
+        decode(2, 0);
+        multiply(1);
+        spread<kN, kReads, kValu, kW>();
+        frags(now, 3, 1);
+        if constexpr (!FWD) read_sub(now, 3);
+        decode(3, 1);
+        multiply(0);
+        spread<kN, kReads, kValu, 0>();
+        __builtin_amdgcn_s_waitcnt(kVmcnt0);
+        store_s(next, step + 1);
+        __syncthreads();
+        fetch_s(step + 2);
+        fetch_x(now, step + 2, Zero{}, Half{});
+        frags(next, 0, 0);
+        if constexpr (FWD) {
+            read_step(next);
+            shift_scales();
+        } else {
+            read_sub(next, 0);
+        }
+        decode(0, 0);
+        multiply(1);
+        spread<kN, FWD ? TM + 2 * TN : kReads, FWD ? 5 * TN : kValu, kA / 2 + kW>();
+    };
+
+    fetch_s(first);
+    fetch_x(b0, first, Zero{}, All{});
+    fetch_w(b0, first);
+    __builtin_amdgcn_s_waitcnt(kVmcnt0);
+    store_s(b0, first);
+    __syncthreads();
+    fetch_s(first + 1);
+    fetch_x(b1, first + 1, Zero{}, Half{});
+    frags(b0, 0, 0);
+    if constexpr (FWD) {
+        read_step(b0);
+        shift_scales();
+    } else {
+        read_sub(b0, 0);
+    }
+    decode(0, 0);
+    for (int step = first; step < last; step += 2) {
+        body(b0, b1, step);
+        body(b1, b0, step + 1);
+    }
+    __builtin_amdgcn_s_waitcnt(kVmcnt0);   // nothing may come into LDS after the end
+    store_tile<TM, TN>(acc, g.out, g.part, g.kind, g.grid, part, g.m, g.ncol, g.ldo, m0, n0, wm, wn, r, h);
+}
+
+template <int TM, int TN>
+hipError_t mm_go(int dtype, bool forward, const MmArgs& a, hipStream_t s)
+{
+    const unsigned blocks = (unsigned)(a.grid.mt * a.grid.nt * a.grid.parts);
+    if (dtype == 0) {
+        if (forward) k_mm<0, true, TM, TN><<<blocks, kThreads, 0, s>>>(a);
+        else k_mm<0, false, TM, TN><<<blocks, kThreads, 0, s>>>(a);
+    } else {
+        if (forward) k_mm<1, true, TM, TN><<<blocks, kThreads, 0, s>>>(a);
+        else k_mm<1, false, TM, TN><<<blocks, kThreads, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+constexpr int kCus = 256;
+
+struct Plan {
+    TileGrid big, small;   // 256 x 256 tiles on the first columns, 128 x 128 on the others (nt 0: none)
+};
+
+Plan mm_plan(int64_t kred, int64_t ncol, int64_t m)
+{
+    const int steps = (int)ceil_div(kred, kStep);
+    Plan p = {};
+    const int64_t mt = ceil_div(m, 256), nt = ceil_div(ncol, 256);
+    if (mt * nt >= 200) {
+        const int64_t rounds = mt * nt / kCus, whole = rounds * kCus / mt;
+        const bool cut = rounds > 0 && whole > 0 && whole < nt && 4 * (mt * (nt - whole)) <= 3 * kCus;
+        const int64_t nb = cut ? whole : nt;
+        p.big = {(int)mt, (int)nb, 1, steps};
+        if (cut) p.small = {(int)ceil_div(m, 128), (int)ceil_div(ncol - 256 * nb, 128), 1, steps};
+        return p;
+    }
+    p.small = {(int)ceil_div(m, 128), (int)ceil_div(ncol, 128), 1, steps};
+    const int64_t tiles = (int64_t)p.small.mt * p.small.nt;
+    if (tiles < 256) {
+        int64_t parts = 512 / tiles;
+        if (parts > steps / 4) parts = steps / 4;
+        if (parts > 16) parts = 16;
+        if (parts > 1) {
+            p.small.per_part = (int)ceil_div(steps, parts);
+            p.small.parts = (int)ceil_div(steps, p.small.per_part);
+        }
+    }
+    return p;
+}
+
+}  // namespace
+
+size_t mm_tiled_ws(int64_t kred, int64_t ncol, int64_t m)
+{
+    const Plan p = mm_plan(kred, ncol, m);
+    return p.small.parts > 1 ? size_t(p.small.parts) * size_t(m) * size_t(ncol) * sizeof(float) : 0;
+}
+
+hipError_t launch_mm_tiled(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                           bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s)
+{
+    const int64_t kred = forward ? cols : rows, ncol = forward ? rows : cols;
+    const Plan p = mm_plan(kred, ncol, m);
+    MmArgs a{codes, scales, static_cast<const uint16_t*>(x), out, part, m, ncol, ncol, (int)cols, (int)kred, out_kind, p.big};
+    if (p.big.nt > 0) {
+        const int64_t done = 256 * (int64_t)p.big.nt;
+        if (p.small.nt > 0) a.ncol = done;
+        const hipError_t e = mm_go<4, 4>(dtype, forward, a, s);
+        if (e != hipSuccess || p.small.nt == 0) return e;
+        // the other columns: the weight's rows from there on, or its columns
+        a.codes += forward ? done * (cols / 2) : done / 2;
+        a.scales += forward ? done * (cols / kGroup) : done / kGroup;
+        a.out = (char*)out + done * (out_kind == kOutFp32 ? 4 : 2);
+        a.ncol = ncol - done;
+    }
+    a.grid = p.small;
+    const hipError_t e = mm_go<2, 2>(dtype, forward, a, s);
+    if (e != hipSuccess || p.small.parts == 1) return e;
+    return launch_split_sum(part, p.small.parts, m * ncol, out, out_kind, s);
+}
+
+}  // namespace mx4k

@@ -28,13 +28,10 @@ namespace mx4k {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kThreads = 256;
 constexpr int kStep = 256;            // columns a step
 constexpr int kRowBytes = kStep / 2;
 constexpr int kGroups = kStep / kGroup;
-constexpr int kVmcnt0 = 0x0f70;       // s_waitcnt: vector memory only, none outstanding
 
 // cols >= kStep.
 struct Mm4Args {
@@ -54,9 +51,6 @@ __device__ __forceinline__ f32x16 mfma4(const u32x4& a, uint32_t sa, const u32x4
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
-template <int K>
-using Kind = std::integral_constant<int, K>;
-
 // A wave's tile: TM x TN tiles of 32 x 32; the workgroup's: 2 x 2 waves.
 template <int TM, int TN>
 struct Shape {
@@ -69,25 +63,6 @@ struct Buffer {
     u32x4 a[64 * TM * (kRowBytes / 16)], w[64 * TN * (kRowBytes / 16)];
     u32x2 as[64 * TM], ws[64 * TN];
 };
-
-// READS LDS reads and LOADS loads spread over N matrix instructions (the reads over
-// the first three quarters, the next sub-step begins with what they bring): four
-// waves share the LDS and the address unit, and what is bunched waits there while
-// the matrix cores are idle.
-template <int N, int READS, int LOADS, int I = 0>
-__device__ __forceinline__ void spread()
-{
-    if constexpr (I < N) {
-        constexpr int kOver = N * 3 / 4, kTo = I + 1 < kOver ? I + 1 : kOver, kFrom = I < kOver ? I : kOver;
-        constexpr int kReads = kTo * READS / kOver - kFrom * READS / kOver, kLoads = (I + 1) * LOADS / N - I * LOADS / N;
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if constexpr (kReads > 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
-        if constexpr (kLoads > 0) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);
-        spread<N, READS, LOADS, I + 1>();
-    } else {
-        __builtin_amdgcn_sched_barrier(0);
-    }
-}
 
 template <int TM, int TN>
 __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
@@ -204,14 +179,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
         fetch(next, clamp(step + 1), Third{}, TwoThirds{});
         frags(now, 1, 1);
         MX4_MULTIPLY(0, 0);
-        spread<TM * TN, TM + TN, TwoThirds::value - Third::value>();
+        spread<TM * TN, TM + TN, 0, TwoThirds::value - Third::value>();
         fetch(next, clamp(step + 1), TwoThirds{}, All{});
         frags(now, 2, 0);
         MX4_MULTIPLY(1, 1);
-        spread<TM * TN, TM + TN, All::value - TwoThirds::value>();
+        spread<TM * TN, TM + TN, 0, All::value - TwoThirds::value>();
         frags(now, 3, 1);
         MX4_MULTIPLY(2, 0);
-        spread<TM * TN, TM + TN, 0>();
+        spread<TM * TN, TM + TN, 0, 0>();
         __builtin_amdgcn_s_waitcnt(kVmcnt0);
         store_scales(next, step + 1);
         __syncthreads();
@@ -219,7 +194,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
         fetch_scales(clamp(step + 2));
         fetch(now, clamp(step + 2), Zero{}, Third{});
         MX4_MULTIPLY(3, 1);
-        spread<TM * TN, 2 * (TM + TN), Third::value + 2>();
+        spread<TM * TN, 2 * (TM + TN), 0, Third::value + 2>();
     };
     fetch_scales(first);
     fetch(b0, first, Zero{}, All{});
@@ -237,44 +212,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     __builtin_amdgcn_s_waitcnt(kVmcnt0);   // nothing may come into LDS after the end
 #undef MX4_MULTIPLY
 
-    const bool split = g.grid.parts > 1, whole = m0 + S::kBM <= g.m;
-    char* out = split ? (char*)(g.part + (int64_t)part * g.m * g.ldo) : (char*)g.out;
-    const int kind = split ? (int)kOutFp32 : g.kind;
-    const int col = wn * (32 * TN) + TN * r;
-    if (n0 + col >= g.rows) return;
-    // lane (r, h): columns from `col` on of rows 8 a + 4 h + b of each 32
-    auto put = [&](auto k, auto all) {
-        constexpr int kBytes = k == kOutFp32 ? 4 : 2;
-        char* base = out + ((m0 + wm * (32 * TM)) * g.ldo + n0) * kBytes;   // uniform
-        const uint32_t at = (uint32_t)(4 * h * g.ldo + col) * kBytes;
-        const int64_t pitch_out = g.ldo * kBytes;
-        const int left = (int)(all || g.m - m0 > S::kBM ? S::kBM : g.m - m0) - wm * (32 * TM) - 4 * h;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            // one row of tiles at a time out of the accumulation registers: moved all at once the sums spill
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int k2 = i; k2 < TM; ++k2)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) __asm__ volatile("" : "+a"(acc[k2][j]));
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = i * 32 + 8 * (e >> 2) + (e & 3);
-                if (all || row < left) {
-                    MX4_GLOBAL char* p = (MX4_GLOBAL char*)base + row * pitch_out;
-                    if constexpr (TN == 4) put4<k>(p + at, f32x4{acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]});
-                    else put2<k>(p + at, f32x2{acc[i][0][e], acc[i][1][e]});
-                }
-            }
-        }
-    };
-    auto of_kind = [&](auto all) {
-        if (kind == kOutBf16) put(Kind<kOutBf16>{}, all);
-        else if (kind == kOutFp16) put(Kind<kOutFp16>{}, all);
-        else put(Kind<kOutFp32>{}, all);
-    };
-    if (whole) of_kind(std::true_type{});
-    else of_kind(std::false_type{});
+    store_tile<TM, TN>(acc, g.out, g.part, g.kind, g.grid, part, g.m, g.rows, g.ldo, m0, n0, wm, wn, r, h);
 }
 
 template <int TM, int TN>

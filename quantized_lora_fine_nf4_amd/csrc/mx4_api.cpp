@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int64_t kMaxN = int64_t(1) << 40, kMaxSide = int64_t(1) << 26, kMaxTokens = int64_t(1) << 25;
+constexpr int64_t kMaxN = int64_t(1) << 40, kMaxSide = int64_t(1) << 22, kMaxTokens = int64_t(1) << 25;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -22,6 +22,12 @@ size_t matmul_ws(int64_t rows, int64_t cols, bool forward, int64_t m);
 hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                          bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s);
 
+// Their tiled kernels (k_mx4_mm.hip), for all but few tokens; a function of the
+// reduction's length and the output's columns.
+size_t mm_tiled_ws(int64_t kred, int64_t ncol, int64_t m);
+hipError_t launch_mm_tiled(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                           bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s);
+
 // The same forward with x [m x cols] in the microscaled form too.
 size_t matmul4_ws(int64_t rows, int64_t cols, int64_t m);
 hipError_t launch_matmul4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,

@@ -1,7 +1,11 @@
-// mx4_tile.h -- what the tiled products share: the order of the output tiles and
-// the split of the reduction.
+// mx4_tile.h -- what the tiled products share: the order of the output tiles, the
+// split of the reduction, the order of instructions in a sub-step and the way out.
+// A workgroup is 2 x 2 waves of TM x TN tiles of 32 x 32.
 #pragma once
+#include <type_traits>
+
 #include "mx4_format.h"
+#include "mx4_sum.h"
 
 namespace mx4k {
 
@@ -29,6 +33,87 @@ __device__ __forceinline__ void tile_of(const TileGrid& g, int b, int& tm, int& 
     const int in = t - band * kBand * g.nt;
     tm = __builtin_amdgcn_readfirstlane(band * kBand + in % h);
     tn = __builtin_amdgcn_readfirstlane(in / h);
+}
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kThreads = 256;
+constexpr int kVmcnt0 = 0x0f70;   // s_waitcnt: vector memory only, none outstanding
+
+// READS LDS reads, VALU vector instructions and LOADS loads among N matrix
+// instructions.  The reads go to the first three quarters (half, with VALU), since
+// the next sub-step, or the VALU in the rest of this one, begins with what they
+// bring.  Four waves share the LDS and the address unit, and what is bunched waits
+// there while the matrix cores are idle.
+template <int N, int READS, int VALU, int LOADS, int I = 0>
+__device__ __forceinline__ void spread()
+{
+    if constexpr (I < N) {
+        constexpr int kOver = VALU ? N / 2 : N * 3 / 4, kTo = I + 1 < kOver ? I + 1 : kOver, kFrom = I < kOver ? I : kOver;
+        constexpr int kReads = kTo * READS / kOver - kFrom * READS / kOver;
+        constexpr int kLoads = (I + 1) * LOADS / N - I * LOADS / N;
+        constexpr int kBusy = N - kOver, kVTo = I + 1 - kOver, kVFrom = I - kOver;
+        constexpr int kValu = kVTo > 0 ? kVTo * VALU / kBusy - (kVFrom > 0 ? kVFrom * VALU / kBusy : 0) : 0;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if constexpr (kReads > 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+        if constexpr (kValu > 0) __builtin_amdgcn_sched_group_barrier(0x002, kValu, 0);
+        if constexpr (kLoads > 0) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);
+        spread<N, READS, VALU, LOADS, I + 1>();
+    } else {
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+template <int K>
+using Kind = std::integral_constant<int, K>;
+
+// A wave's sums to out, or to its part's partial (with more than one).  The
+// workgroup's tile begins at (m0, n0); wave (wm, wn), lane (r, h): columns TN r to
+// TN r + TN - 1 of the wave's, rows 8 a + 4 h + b of each 32.  ncol: out's columns,
+// ldo its row pitch (the partials' too).
+template <int TM, int TN>
+__device__ __forceinline__ void store_tile(f32x16 (&acc)[TM][TN], void* dst, float* partial, int dst_kind,
+                                           const TileGrid& grid, int part, int64_t m, int64_t ncol, int64_t ldo,
+                                           int64_t m0, int64_t n0, int wm, int wn, int r, int h)
+{
+    constexpr int kBM = 64 * TM;
+    const bool split = grid.parts > 1;
+    char* out = split ? (char*)(partial + (int64_t)part * m * ldo) : (char*)dst;
+    const int kind = split ? (int)kOutFp32 : dst_kind;
+    const int col = wn * (32 * TN) + TN * r;
+    if (n0 + col >= ncol) return;
+    auto put = [&](auto k, auto all) {
+        constexpr int kBytes = k == kOutFp32 ? 4 : 2;
+        char* base = out + ((m0 + wm * (32 * TM)) * ldo + n0) * kBytes;   // uniform
+        const uint32_t at = (uint32_t)(4 * h * ldo + col) * kBytes;
+        const int64_t pitch = ldo * kBytes;
+        const int left = (int)(all || m - m0 > kBM ? kBM : m - m0) - wm * (32 * TM) - 4 * h;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            // one row of tiles at a time out of the accumulation registers: moved all at once the sums spill
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k2 = i; k2 < TM; ++k2)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) __asm__ volatile("" : "+a"(acc[k2][j]));
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int row = i * 32 + 8 * (e >> 2) + (e & 3);
+                if (all || row < left) {
+                    MX4_GLOBAL char* p = (MX4_GLOBAL char*)base + row * pitch;
+                    if constexpr (TN == 4) put4<k>(p + at, f32x4{acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]});
+                    else put2<k>(p + at, f32x2{acc[i][0][e], acc[i][1][e]});
+                }
+            }
+        }
+    };
+    auto of_kind = [&](auto all) {
+        if (kind == kOutBf16) put(Kind<kOutBf16>{}, all);
+        else if (kind == kOutFp16) put(Kind<kOutFp16>{}, all);
+        else put(Kind<kOutFp32>{}, all);
+    };
+    if (m0 + kBM <= m) of_kind(std::true_type{});
+    else of_kind(std::false_type{});
 }
 
 }  // namespace mx4k
