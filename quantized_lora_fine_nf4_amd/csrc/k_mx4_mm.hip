@@ -3,23 +3,30 @@
 //
 // v_mfma_f32_32x32x16; a 256 x 256 output tile by four waves of 128 x 128, one per
 // SIMD.  A step is 64 of the reduction: x's rows (128 bytes each) and the weight's
-// codes go straight into one of two LDS buffers while the other is multiplied.  The
-// codes leave LDS as codes: each wave converts the fragments it multiplies, two
-// values an instruction, in the shadow of the matrix instructions; the weight is
-// never written anywhere in 16 bits.
+// codes go straight into one of three LDS buffers (one multiplied, one complete,
+// one on its way).  The codes leave LDS as codes: each wave converts the fragments
+// it multiplies, two values an instruction, in the shadow of the matrix
+// instructions; the weight is never written anywhere in 16 bits.
+//
+// A step has four sub-steps of 16.  While one is multiplied, the next one's weight
+// is converted, its x read, and the codes of the one after it.  The barrier stands
+// before the third, when the next step's buffer is first read.
 //
 // Forward: lane (r, h) reads row r's 16 bytes of block h of the step, one scale
 // under which its four dwords become the fragments of the four sub-steps
-// (reduction index 32 h + 8 f + j).  Backward the reduction runs over the weight's
-// rows, whose scales differ: lane (r, h) reads its TN columns of rows 32 h + 8 f + j,
-// j = 0 .. 7, converts each row's byte (two columns) under that row's scale, and
-// two rows' halves are put together as pairs of the fragments.
+// (reduction index 32 h + 8 f + j).  Weight row TN r + c of a wave's is row r of its
+// tile c, so that a lane ends with TN consecutive columns.
 //
-// Weight row (column, backward) TN r + c of a wave's part is row r of its tile c,
-// so that a lane ends with TN consecutive columns.  16-byte pieces of x's rows lie
-// permuted by the row's index, so that eight lanes that read eight rows touch all
-// banks.  x comes through a buffer descriptor that ends with it: rows past its end,
-// and pieces past a row's end (offset kFar), arrive as zeros.
+// Backward the reduction runs over the weight's rows, whose scales differ.  The
+// transposing read gives lane (r, h) the bytes (two columns) of rows 32 h + 8 f + j,
+// j = 0 .. 7, in one register pair; each byte is converted under its row's scale,
+// and the halves of two rows are put together as pairs of the fragments.  Of a
+// wave's 128 columns lane r = 8 q + i has 32 q + 2 i, + 1, + 16, + 17 (one scale
+// group); neighbours exchange a pair at the end and hold four in a row.
+//
+// 16-byte pieces lie permuted by their row's index, so that lanes that read eight
+// rows touch all banks.  x comes through a buffer descriptor that ends with it: rows
+// past its end, and pieces past a row's end (offset kFar), arrive as zeros.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -70,7 +77,7 @@ template <int DT, bool FWD, int TM, int TN>
 __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
 {
     typedef Buffer<TM, TN> Buf;
-    __shared__ Buf b0, b1;   // two objects, so that reads of one need not wait for what comes into the other
+    __shared__ Buf b0, b1, b2;   // objects of their own, so that reads of one need not wait for what comes into another
     constexpr int kBM = 64 * TM, kBN = 64 * TN;
     constexpr int kA = 2 * TM, kW = TN / 2;   // 16-byte pieces per thread and step
     int tm, tn, part;
@@ -91,7 +98,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
     const int piece = (t & 7) ^ ((t >> 3) & 7);
     const uint32_t ao = (uint32_t)(t >> 3) * xpitch + 16 * piece;
     auto fetch_x = [&](Buf& b, int step, auto from, auto to) {
-        const bool in = step < last && step * kStep + 8 * piece < g.kred;
+        const bool in = (step < last) & (step * kStep + 8 * piece < g.kred);
         const uint32_t at = in ? ao + (uint32_t)step * (2 * kStep) : kFar;
 #pragma unroll
         for (int i = from; i < to; ++i)
@@ -99,7 +106,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
                                                      at + (uint32_t)i * (32 * xpitch), 0, 0, 0);
     };
     // codes.  Forward: two pieces a row, LDS row t / 2 + 128 i, slot (t & 1) holds piece (t & 1) ^ (row / 4 & 1).
-    // Backward: 2 TN pieces a row, row t / (2 TN) of the step (and 32 below with TN = 4).
+    // Backward: 2 TN pieces a row, row t / (2 TN) of the step (and 32 below with TN = 4), permuted by row % (2 TN).
     const MX4_GLOBAL uint8_t* wp = (const MX4_GLOBAL uint8_t*)g.codes;
     int64_t wo[kW];
 #pragma unroll
@@ -109,7 +116,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
             const int64_t n = n0 + l / (32 * TN) * (32 * TN) + TN * (l % 32) + l / 32 % TN;
             wo[i] = (n < g.ncol ? n : g.ncol - 1) * wpitch;
         } else {
-            const int64_t c = n0 + 32 * (t % (2 * TN));
+            const int64_t c = n0 + 32 * ((t % (2 * TN)) ^ (t / (2 * TN) % (2 * TN)));
             wo[i] = (c < g.ncol ? c : n0) / 2;
         }
     }
@@ -150,10 +157,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
         for (int i = 0; i < kW; ++i) {
             // past the end: 0 and not NaN, against zeros of x
             if constexpr (FWD) {
-                const bool in = step < last && 2 * step + (t & 1) < spitch;
+                const bool in = (step < last) & (2 * step + (t & 1) < spitch);
                 b.s[t + 256 * i] = (uint8_t)(in ? rs[i] : 0u);
             } else {
-                const bool in = step < last && step * kStep + (t >> 2) < g.kred;
+                const bool in = (step < last) & (step * kStep + (t >> 2) < g.kred);
                 b.s[((t & 3) + 4 * i) * 64 + (t >> 2)] = (uint8_t)(in ? rs[i] : 0u);
             }
         }
@@ -166,50 +173,53 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
 #pragma unroll
         for (int i = 0; i < TM; ++i) fa[to][i] = b.a[(wm * TM + i) * 256 + at];
     };
-    // forward: a step's codes and scale arguments; backward: a sub-step's
-    u32x4 code[TN];
-    float scale[TN];
-    uint32_t raw[8];
-    u32x2 rawscale;
+    // forward: a step's codes and scale arguments (now and next); backward: a sub-step's (the next one's and the one
+    // after it)
+    u32x4 code[2][TN];
+    uint32_t scale[2][TN];
+    u32x2 raw[2][TN / 2], rawscale[2];
     auto read_step = [&](const Buf& b) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int l = (wn * TN + j) * 32 + r;
-            code[j] = b.w[l * 2 + (h ^ ((l >> 2) & 1))];
-            scale[j] = __builtin_bit_cast(float, (uint32_t)b.s[2 * l + h]);
+            code[1][j] = b.w[l * 2 + (h ^ ((l >> 2) & 1))];
+            scale[1][j] = b.s[2 * l + h];
         }
     };
-    auto read_sub = [&](const Buf& b, int f) {
+    // the transposing read: of 16 lanes, lanes 2 j and 2 j + 1 give eight bytes each of row j, lane i takes byte i of all
+    const int trow = (lane & 15) >> 1, thalf = lane & 1, tquad = (lane >> 4) & 1;
+    auto read_sub = [&](const Buf& b, int f, int to) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint8_t* p = (const uint8_t*)b.w + (32 * h + 8 * f + j) * (32 * TN) + wn * (16 * TN) + r * (TN / 2);
-            if constexpr (TN == 4) raw[j] = *(const uint16_t*)p;
-            else raw[j] = *p;
+        for (int k = 0; k < TN / 2; ++k) {
+            const int p = TN == 4 ? wn * 4 + 2 * tquad + thalf : wn * 2 + tquad, half = TN == 4 ? k : thalf;
+            const int row = 32 * h + 8 * f + trow;
+            const uint8_t* at = (const uint8_t*)b.w + row * (32 * TN) + 16 * (p ^ (row % (2 * TN))) + 8 * half;
+            typedef int i32x2 __attribute__((ext_vector_type(2)));
+            raw[to][k] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((MX4_LDS i32x2*)at));
         }
-        rawscale = *(const u32x2*)(b.s + (wn * TN + r * TN / 32) * 64 + 32 * h + 8 * f);
+        rawscale[to] = *(const u32x2*)(b.s + (wn * TN + r * TN / 32) * 64 + 32 * h + 8 * f);
     };
-    auto shift_scales = [&]() {
-#pragma unroll
-        for (int j = 0; j < TN; ++j) scale[j] = scale_arg(__builtin_bit_cast(uint32_t, scale[j]));
+    // the conversions look at the exponent field alone: a byte of packed scales needs a shift and no mask
+    auto byte_arg = [](uint32_t v, int b) {
+        return __builtin_bit_cast(float, b == 3 ? v >> 1 : v << (23 - 8 * b));
     };
-    auto decode = [&](int f, int to) {
-        if constexpr (FWD) {
+    auto decode_next = [&](int f, int which, int to) {   // forward: sub-step f of step `which`
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fw[to][j] = decode8<DT>(code[j][f], scale[j]);
-        } else {
-            float s[8];
+        for (int j = 0; j < TN; ++j) fw[to][j] = decode8<DT>(code[which][j][f], scale_arg(scale[which][j]));
+    };
+    auto decode_back = [&](int from, int to) {
+        const uint32_t s0 = rawscale[from][0], s1 = rawscale[from][1];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] = scale_arg((rawscale[j >> 2] >> (8 * (j & 3))) & 255);
+        for (int k = 0; k < TN / 2; ++k) {
+            const uint32_t c0 = raw[from][k][0], c1 = raw[from][k][1];
+            const uint32_t v[8] = {decode2<DT, 0>(c0, byte_arg(s0, 0)), decode2<DT, 1>(c0, byte_arg(s0, 1)),
+                                   decode2<DT, 2>(c0, byte_arg(s0, 2)), decode2<DT, 3>(c0, byte_arg(s0, 3)),
+                                   decode2<DT, 0>(c1, byte_arg(s1, 0)), decode2<DT, 1>(c1, byte_arg(s1, 1)),
+                                   decode2<DT, 2>(c1, byte_arg(s1, 2)), decode2<DT, 3>(c1, byte_arg(s1, 3))};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t p = decode2<DT, 0>(raw[2 * j], s[2 * j]), q = decode2<DT, 0>(raw[2 * j + 1], s[2 * j + 1]);
-                fw[to][0][j] = low16(p, q);
-                fw[to][1][j] = high16(p, q);
-                if constexpr (TN == 4) {
-                    const uint32_t u = decode2<DT, 1>(raw[2 * j], s[2 * j]), v = decode2<DT, 1>(raw[2 * j + 1], s[2 * j + 1]);
-                    fw[to][2][j] = low16(u, v);
-                    fw[to][3][j] = high16(u, v);
-                }
+                fw[to][2 * k][j] = low16(v[2 * j], v[2 * j + 1]);
+                fw[to][2 * k + 1][j] = high16(v[2 * j], v[2 * j + 1]);
             }
         }
     };
@@ -219,71 +229,99 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] = mfma16<DT>(fa[from][i], fw[from][j], acc[i][j]);
     };
-    constexpr int kN = TM * TN;
-    constexpr int kReads = FWD ? TM : TM + 9, kValu = FWD ? 4 * TN : 8 * TN + 16;
-    typedef std::integral_constant<int, 0> Zero;
-    typedef std::integral_constant<int, kA / 2> Half;
+    constexpr int kN = TM * TN, kReads = FWD ? TM : TM + TN / 2 + 1, kValu = FWD ? 4 * TN : 8 * TN + 8;
+    typedef std::integral_constant<int, 0> P0;
+    typedef std::integral_constant<int, kA / 4> P1;
+    typedef std::integral_constant<int, kA * 5 / 8> P2;
     typedef std::integral_constant<int, kA> All;
 
-    // One step out of `now`: each sub-step reads and converts what the next one multiplies.  The step after it is on
-    // its way to `next`; steps past the last one are zeros under scales of 0.
-    auto body = [&](Buf& now, Buf& next, int step) {
-        fetch_x(next, step + 1, Half{}, All{});
+    // One step out of `now`; `next` is on its way until the barrier, `then` is asked for after it.  Steps past the last
+    // one are zeros under scales of 0.
+    auto body = [&](Buf& now, Buf& next, Buf& then, int step) {
+        fetch_x(next, step + 1, P2{}, All{});
         frags(now, 1, 1);
-        if constexpr (!FWD) read_sub(now, 1);
-        decode(1, 1);
+        if constexpr (FWD) {
+            decode_next(1, 0, 1);
+        } else {
+            read_sub(now, 2, 0);
+            decode_back(1, 1);
+        }
         multiply(0);
-        spread<kN, kReads, kValu, kA / 2>();
-        fetch_w(next, step + 1);
+        spread<kN, kReads, kValu, kA - P2::value>();
         frags(now, 2, 0);
-        if constexpr (!FWD) read_sub(now, 2);
-        decode(2, 0);
+        if constexpr (FWD) {
+            decode_next(2, 0, 0);
+        } else {
+            read_sub(now, 3, 1);
+            decode_back(0, 0);
+        }
         multiply(1);
-        spread<kN, kReads, kValu, kW>();
-        frags(now, 3, 1);
-        if constexpr (!FWD) read_sub(now, 3);
-        decode(3, 1);
-        multiply(0);
         spread<kN, kReads, kValu, 0>();
         __builtin_amdgcn_s_waitcnt(kVmcnt0);
         store_s(next, step + 1);
         __syncthreads();
         fetch_s(step + 2);
-        fetch_x(now, step + 2, Zero{}, Half{});
+        fetch_w(then, step + 2);
+        fetch_x(then, step + 2, P0{}, P1{});
+        frags(now, 3, 1);
+        if constexpr (FWD) {
+            decode_next(3, 0, 1);
+            read_step(next);
+        } else {
+            read_sub(next, 0, 0);
+            decode_back(1, 1);
+        }
+        multiply(0);
+        spread<kN, FWD ? TM + 2 * TN : kReads, kValu, 2 * kW + P1::value>();
+        fetch_x(then, step + 2, P1{}, P2{});
         frags(next, 0, 0);
         if constexpr (FWD) {
-            read_step(next);
-            shift_scales();
+            decode_next(0, 1, 0);
         } else {
-            read_sub(next, 0);
+            read_sub(next, 1, 1);
+            decode_back(0, 0);
         }
-        decode(0, 0);
         multiply(1);
-        spread<kN, FWD ? TM + 2 * TN : kReads, FWD ? 5 * TN : kValu, kA / 2 + kW>();
+        spread<kN, kReads, kValu, P2::value - P1::value>();
+        if constexpr (FWD) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                code[0][j] = code[1][j];
+                scale[0][j] = scale[1][j];
+            }
+        }
     };
 
     fetch_s(first);
-    fetch_x(b0, first, Zero{}, All{});
     fetch_w(b0, first);
+    fetch_x(b0, first, P0{}, All{});
     __builtin_amdgcn_s_waitcnt(kVmcnt0);
     store_s(b0, first);
     __syncthreads();
     fetch_s(first + 1);
-    fetch_x(b1, first + 1, Zero{}, Half{});
+    fetch_w(b1, first + 1);
+    fetch_x(b1, first + 1, P0{}, P2{});
     frags(b0, 0, 0);
     if constexpr (FWD) {
         read_step(b0);
-        shift_scales();
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            code[0][j] = code[1][j];
+            scale[0][j] = scale[1][j];
+        }
+        decode_next(0, 0, 0);
     } else {
-        read_sub(b0, 0);
+        read_sub(b0, 0, 0);
+        read_sub(b0, 1, 1);
+        decode_back(0, 0);
     }
-    decode(0, 0);
-    for (int step = first; step < last; step += 2) {
-        body(b0, b1, step);
-        body(b1, b0, step + 1);
+    for (int step = first; step < last; step += 3) {
+        body(b0, b1, b2, step);
+        body(b1, b2, b0, step + 1);
+        body(b2, b0, b1, step + 2);
     }
     __builtin_amdgcn_s_waitcnt(kVmcnt0);   // nothing may come into LDS after the end
-    store_tile<TM, TN>(acc, g.out, g.part, g.kind, g.grid, part, g.m, g.ncol, g.ldo, m0, n0, wm, wn, r, h);
+    store_tile<TM, TN, !FWD && TN == 4>(acc, g.out, g.part, g.kind, g.grid, part, g.m, g.ncol, g.ldo, m0, n0, wm, wn, r, h);
 }
 
 template <int TM, int TN>

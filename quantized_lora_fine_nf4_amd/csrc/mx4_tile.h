@@ -40,20 +40,17 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kThreads = 256;
 constexpr int kVmcnt0 = 0x0f70;   // s_waitcnt: vector memory only, none outstanding
 
-// READS LDS reads, VALU vector instructions and LOADS loads among N matrix
-// instructions.  The reads go to the first three quarters (half, with VALU), since
-// the next sub-step, or the VALU in the rest of this one, begins with what they
-// bring.  Four waves share the LDS and the address unit, and what is bunched waits
+// READS LDS reads, VALU vector instructions and LOADS loads spread over N matrix
+// instructions, the reads over the first three quarters: the next sub-step begins
+// with what they bring.  Four waves share the LDS and the address unit, and what is bunched waits
 // there while the matrix cores are idle.
 template <int N, int READS, int VALU, int LOADS, int I = 0>
 __device__ __forceinline__ void spread()
 {
     if constexpr (I < N) {
-        constexpr int kOver = VALU ? N / 2 : N * 3 / 4, kTo = I + 1 < kOver ? I + 1 : kOver, kFrom = I < kOver ? I : kOver;
+        constexpr int kOver = N * 3 / 4, kTo = I + 1 < kOver ? I + 1 : kOver, kFrom = I < kOver ? I : kOver;
         constexpr int kReads = kTo * READS / kOver - kFrom * READS / kOver;
-        constexpr int kLoads = (I + 1) * LOADS / N - I * LOADS / N;
-        constexpr int kBusy = N - kOver, kVTo = I + 1 - kOver, kVFrom = I - kOver;
-        constexpr int kValu = kVTo > 0 ? kVTo * VALU / kBusy - (kVFrom > 0 ? kVFrom * VALU / kBusy : 0) : 0;
+        constexpr int kLoads = (I + 1) * LOADS / N - I * LOADS / N, kValu = (I + 1) * VALU / N - I * VALU / N;
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         if constexpr (kReads > 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
         if constexpr (kValu > 0) __builtin_amdgcn_sched_group_barrier(0x002, kValu, 0);
@@ -67,11 +64,17 @@ __device__ __forceinline__ void spread()
 template <int K>
 using Kind = std::integral_constant<int, K>;
 
+// What the neighbour lane (r ^ 1) has.
+__device__ __forceinline__ uint32_t neighbour(uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xf, 0xf, true); }
+__device__ __forceinline__ float neighbour(float v) { return __builtin_bit_cast(float, neighbour(__builtin_bit_cast(uint32_t, v))); }
+
 // A wave's sums to out, or to its part's partial (with more than one).  The
 // workgroup's tile begins at (m0, n0); wave (wm, wn), lane (r, h): columns TN r to
-// TN r + TN - 1 of the wave's, rows 8 a + 4 h + b of each 32.  ncol: out's columns,
-// ldo its row pitch (the partials' too).
-template <int TM, int TN>
+// TN r + TN - 1 of the wave's, rows 8 a + 4 h + b of each 32.  PAIRS (TN 4): lane
+// r = 8 q + i has columns 32 q + 2 i, + 1, + 16, + 17 instead; an even lane gives its
+// upper pair for its neighbour's lower one.  ncol: out's columns, ldo its row pitch
+// (the partials' too).
+template <int TM, int TN, bool PAIRS = false>
 __device__ __forceinline__ void store_tile(f32x16 (&acc)[TM][TN], void* dst, float* partial, int dst_kind,
                                            const TileGrid& grid, int part, int64_t m, int64_t ncol, int64_t ldo,
                                            int64_t m0, int64_t n0, int wm, int wn, int r, int h)
@@ -80,8 +83,10 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[TM][TN], void* dst, flo
     const bool split = grid.parts > 1;
     char* out = split ? (char*)(partial + (int64_t)part * m * ldo) : (char*)dst;
     const int kind = split ? (int)kOutFp32 : dst_kind;
-    const int col = wn * (32 * TN) + TN * r;
-    if (n0 + col >= ncol) return;
+    const int odd = r & 1;
+    const int col = wn * (32 * TN) + (PAIRS ? 32 * (r >> 3) + 4 * ((r & 7) >> 1) + 16 * odd : TN * r);
+    if (!PAIRS && n0 + col >= ncol) return;
+    const bool in = n0 + col < ncol;   // with PAIRS the neighbour may need this lane
     auto put = [&](auto k, auto all) {
         constexpr int kBytes = k == kOutFp32 ? 4 : 2;
         char* base = out + ((m0 + wm * (32 * TM)) * ldo + n0) * kBytes;   // uniform
@@ -99,7 +104,13 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[TM][TN], void* dst, flo
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int row = i * 32 + 8 * (e >> 2) + (e & 3);
-                if (all || row < left) {
+                if constexpr (PAIRS) {
+                    const float c0 = acc[i][0][e], c1 = acc[i][1][e], c2 = acc[i][2][e], c3 = acc[i][3][e];
+                    const float w = odd ? c2 : c0, x = odd ? c3 : c1;
+                    const float y = neighbour(odd ? c0 : c2), z = neighbour(odd ? c1 : c3);
+                    if ((all || row < left) && in)
+                        put4<k>((MX4_GLOBAL char*)base + row * pitch + at, odd ? f32x4{y, z, w, x} : f32x4{w, x, y, z});
+                } else if (all || row < left) {
                     MX4_GLOBAL char* p = (MX4_GLOBAL char*)base + row * pitch;
                     if constexpr (TN == 4) put4<k>(p + at, f32x4{acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]});
                     else put2<k>(p + at, f32x2{acc[i][0][e], acc[i][1][e]});
