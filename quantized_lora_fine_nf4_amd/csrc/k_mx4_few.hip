@@ -13,11 +13,11 @@
 // are.  The waves' sums meet in LDS.
 //
 // Backward the reduction runs over the weight's rows, whose scales differ.  Lane
-// (r, g) reads eight columns (a dword) of rows 8 g .. 8 g + 7 of a 32-row slab; a
+// (r, g) reads eight or sixteen columns of rows 8 g .. 8 g + 7 of a 32-row slab; a
 // byte (two columns of one row) is converted under that row's scale, and the
 // halves of two rows' results are put together as the fragments' pairs.  Column
-// 8 r + c of a 128-column stripe is row r of tile c, so that a lane ends with
-// eight consecutive columns.
+// T r + c of a wave's 16 T is row r of tile c, so that a lane ends with T
+// consecutive columns.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -60,19 +60,20 @@ struct FewArgs {
     int64_t m, rows, cols;
     int kind;                        // of out
     int parts;
+    uint32_t token_tiles;            // workgroups along the tokens
 };
 
 __device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 
 constexpr int kWaves = 8;
 
-// DT 0, 1: x in bf16, fp16; 2: in codes.
-template <int DT, int kRT, int kMT>
+// DT 0, 1: x in bf16, fp16; 2: in codes.  kAhead steps of the weight in flight.
+template <int DT, int kRT, int kMT, int kAhead>
 __global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
 {
     __shared__ f32x4 sums[kWaves][kRT * kMT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * kRT), t0 = (int64_t)blockIdx.y * (16 * kMT);
+    const int64_t n0 = (int64_t)(blockIdx.x / a.token_tiles) * (16 * kRT), t0 = (int64_t)(blockIdx.x % a.token_tiles) * (16 * kMT);
     const int64_t blocks = a.cols / kGroup;
     const MX4_GLOBAL uint8_t *wc[kRT], *ws[kRT];
 #pragma unroll
@@ -89,38 +90,57 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
         xc[u] = (const MX4_GLOBAL uint8_t*)a.x + t * (DT == 2 ? a.cols / 2 : a.cols * 2);
         xs[u] = (const MX4_GLOBAL uint8_t*)a.xscales + t * blocks;
     }
+    // tokens past the last one: lanes that read nothing, columns that are not stored
+    const int here = (int)least(a.m - t0, 16 * kMT);
     f32x4 acc[kRT][kMT] = {};
-    for (int64_t blk = 4 * wave + g; blk - g < blocks; blk += 4 * kWaves) {
-        const bool in = blk < blocks;   // a block is whole or not there
-        u32x4 c[kRT];
-        uint32_t s[kRT];
+    u32x4 x[kMT][DT == 2 ? 1 : 4] = {};
+    uint32_t e[kMT] = {};
+    for (int64_t at = 4 * wave; at < blocks; at += 4 * kWaves * kAhead) {
+        u32x4 c[kAhead][kRT];
+        uint32_t s[kAhead][kRT];
 #pragma unroll
-        for (int i = 0; i < kRT; ++i) {
-            c[i] = in ? *(const MX4_GLOBAL u32x4*)(wc[i] + 16 * blk) : kZero;
-            s[i] = in ? ws[i][blk] : 0u;
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t blk = at + 4 * kWaves * k + g;
+            const bool in = blk < blocks;   // a block is whole or not there
+#pragma unroll
+            for (int i = 0; i < kRT; ++i) {
+                c[k][i] = in ? *(const MX4_GLOBAL u32x4*)(wc[i] + 16 * blk) : kZero;
+                s[k][i] = in ? ws[i][blk] : 0u;
+            }
         }
-        if constexpr (DT == 2) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t blk = at + 4 * kWaves * k + g;
+            if (blk - g >= blocks) break;
+            const bool in = blk < blocks;
 #pragma unroll
             for (int u = 0; u < kMT; ++u) {
-                const u32x4 d = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 16 * blk) : kZero;
-                const uint32_t e = in ? xs[u][blk] : 0u;
+                if constexpr (DT == 2) {
+                    if (16 * u + r < here) {
+                        x[u][0] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 16 * blk) : kZero;
+                        e[u] = in ? xs[u][blk] : 0u;
+                    }
+                } else {
+                    if (16 * u + r < here) {
 #pragma unroll
-                for (int i = 0; i < kRT; ++i) acc[i][u] = mfma4(c[i], s[i], d, e, acc[i][u]);
-            }
-        } else {
-            u32x4 x[kMT][4];
-#pragma unroll
-            for (int u = 0; u < kMT; ++u)
-#pragma unroll
-                for (int f = 0; f < 4; ++f) x[u][f] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 64 * blk + 16 * f) : kZero;
-#pragma unroll
-            for (int i = 0; i < kRT; ++i)
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const u32x4 w = decode8<DT>(c[i][f], scale_arg(s[i]));
-#pragma unroll
-                    for (int u = 0; u < kMT; ++u) acc[i][u] = mfma16<DT>(w, x[u][f], acc[i][u]);
+                        for (int f = 0; f < 4; ++f) x[u][f] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 64 * blk + 16 * f) : kZero;
+                    }
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < kRT; ++i) {
+                if constexpr (DT == 2) {
+#pragma unroll
+                    for (int u = 0; u < kMT; ++u) acc[i][u] = mfma4(c[k][i], s[k][i], x[u][0], e[u], acc[i][u]);
+                } else {
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        const u32x4 w = decode8<DT>(c[k][i][f], scale_arg(s[k][i]));
+#pragma unroll
+                        for (int u = 0; u < kMT; ++u) acc[i][u] = mfma16<DT>(w, x[u][f], acc[i][u]);
+                    }
+                }
+            }
         }
     }
 #pragma unroll
@@ -155,83 +175,119 @@ __device__ __forceinline__ void decode_columns(const uint32_t (&c)[8], const flo
     }
 }
 
-template <int DT, int kMT>
+// 64 kWords columns a wave: kWords dwords of each of eight rows a lane.
+template <int DT, int kMT, int kWords>
 __global__ __launch_bounds__(64 * kWaves) void k_few_back(FewArgs a)
 {
-    __shared__ f32x4 sums[kWaves / 2][8 * kMT][64];
+    constexpr int kTiles = 8 * kWords;
+    __shared__ f32x4 sums[kWaves / 2][kTiles * kMT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int64_t c0 = (int64_t)blockIdx.x * 128, t0 = (int64_t)blockIdx.y * (16 * kMT);
-    const int64_t col = least(c0 + 8 * r, a.cols - 8);
+    const int64_t c0 = (int64_t)(blockIdx.x / a.token_tiles) * (16 * kTiles), t0 = (int64_t)(blockIdx.x % a.token_tiles) * (16 * kMT);
+    const int64_t col = least(c0 + kTiles * r, a.cols - kTiles);
     const MX4_GLOBAL uint8_t* wc = (const MX4_GLOBAL uint8_t*)a.codes + col / 2;
     const MX4_GLOBAL uint8_t* ws = (const MX4_GLOBAL uint8_t*)a.scales + col / kGroup;
     const MX4_GLOBAL uint16_t* xr[kMT];
 #pragma unroll
     for (int u = 0; u < kMT; ++u) xr[u] = (const MX4_GLOBAL uint16_t*)a.x + least(t0 + 16 * u + r, a.m - 1) * a.rows;
-    f32x4 acc[kMT][8] = {};
+    const int here = (int)least(a.m - t0, 16 * kMT);
+    f32x4 acc[kMT][kTiles] = {};
+    u32x4 x[kMT] = {};
     const int64_t slabs = (a.rows + 31) / 32, stride = (int64_t)kWaves * a.parts;
-    for (int64_t slab = wave + (int64_t)kWaves * blockIdx.z; slab < slabs; slab += stride) {
+    for (int64_t slab = wave + (int64_t)kWaves * blockIdx.y; slab < slabs; slab += stride) {
         const int64_t n = 32 * slab + 8 * g;
         const bool in = n < a.rows;   // rows come in eights
-        uint32_t c[8];
-        float s[8];
+        uint32_t c[kWords][8], s[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            c[j] = in ? *(const MX4_GLOBAL uint32_t*)(wc + (n + j) * (a.cols / 2)) : 0u;
-            s[j] = scale_arg(in ? ws[(n + j) * (a.cols / kGroup)] : 0u);
+            const MX4_GLOBAL uint8_t* p = wc + (in ? n + j : 0) * (a.cols / 2);
+            if constexpr (kWords == 2) {
+                const u32x2 v = *(const MX4_GLOBAL u32x2*)p;
+                c[0][j] = v[0];
+                c[1][j] = v[1];
+            } else {
+                c[0][j] = *(const MX4_GLOBAL uint32_t*)p;
+            }
+            s[j] = ws[(in ? n + j : 0) * (a.cols / kGroup)];
         }
-        u32x4 x[kMT], w[8];
-#pragma unroll
-        for (int u = 0; u < kMT; ++u) x[u] = in ? *(const MX4_GLOBAL u32x4*)(xr[u] + n) : kZero;
-        decode_columns<DT, 0>(c, s, w[0], w[1]);
-        decode_columns<DT, 1>(c, s, w[2], w[3]);
-        decode_columns<DT, 2>(c, s, w[4], w[5]);
-        decode_columns<DT, 3>(c, s, w[6], w[7]);
 #pragma unroll
         for (int u = 0; u < kMT; ++u)
+            if (16 * u + r < here) x[u] = in ? *(const MX4_GLOBAL u32x4*)(xr[u] + n) : kZero;
+        float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[u][i] = mfma16<DT>(x[u], w[i], acc[u][i]);
+        for (int j = 0; j < 8; ++j) f[j] = scale_arg(in ? s[j] : 0u);   // rows past the end: finite, against zeros of x
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            u32x4 w[8];
+            decode_columns<DT, 0>(c[k], f, w[0], w[1]);
+            decode_columns<DT, 1>(c[k], f, w[2], w[3]);
+            decode_columns<DT, 2>(c[k], f, w[4], w[5]);
+            decode_columns<DT, 3>(c[k], f, w[6], w[7]);
+#pragma unroll
+            for (int u = 0; u < kMT; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[u][8 * k + i] = mfma16<DT>(x[u], w[i], acc[u][8 * k + i]);
+        }
     }
     // the upper half of the waves' sums to LDS and added by the lower half, until one is left
 #pragma unroll
     for (int half = kWaves / 2; half; half >>= 1) {
         if (wave >= half && wave < 2 * half) {
 #pragma unroll
-            for (int i = 0; i < 8 * kMT; ++i) sums[wave - half][i][lane] = acc[i >> 3][i & 7];
+            for (int i = 0; i < kTiles * kMT; ++i) sums[wave - half][i][lane] = acc[i / kTiles][i % kTiles];
         }
         __syncthreads();
         if (wave < half) {
 #pragma unroll
-            for (int i = 0; i < 8 * kMT; ++i) acc[i >> 3][i & 7] += sums[wave][i][lane];
+            for (int i = 0; i < kTiles * kMT; ++i) acc[i / kTiles][i % kTiles] += sums[wave][i][lane];
         }
         __syncthreads();
     }
-    if (wave != 0 || c0 + 8 * r >= a.cols) return;
-    void* out = a.parts > 1 ? (void*)(a.part + (int64_t)blockIdx.z * a.m * a.cols) : a.out;
+    if (wave != 0 || c0 + kTiles * r >= a.cols) return;
+    void* out = a.parts > 1 ? (void*)(a.part + (int64_t)blockIdx.y * a.m * a.cols) : a.out;
     const int kind = a.parts > 1 ? (int)kOutFp32 : a.kind;
-    // lane (r, g): tokens 4 g .. 4 g + 3, columns 8 r .. 8 r + 7
+    // lane (r, g): tokens 4 g .. 4 g + 3, columns kTiles r .. kTiles r + kTiles - 1
 #pragma unroll
     for (int u = 0; u < kMT; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t t = t0 + 16 * u + 4 * g + i;
-            if (t < a.m)
-                store8(out, kind, t * a.cols + col, f32x4{acc[u][0][i], acc[u][1][i], acc[u][2][i], acc[u][3][i]},
-                       f32x4{acc[u][4][i], acc[u][5][i], acc[u][6][i], acc[u][7][i]});
+            if (t < a.m) {
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) {
+                    const f32x4* v = acc[u] + 8 * k;
+                    store8(out, kind, t * a.cols + col + 8 * k, f32x4{v[0][i], v[1][i], v[2][i], v[3][i]},
+                           f32x4{v[4][i], v[5][i], v[6][i], v[7][i]});
+                }
+            }
         }
 }
 
-__global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits, int64_t n, void* out, int kind)
+__global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits, int64_t n, int width8, void* out,
+                                                   int64_t ldo, int kind)
 {
-    const int64_t at = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
-    if (at >= n) return;
-    const MX4_GLOBAL f32x4* p = (const MX4_GLOBAL f32x4*)(part + at);
-    f32x4 a = p[0], b = p[1];
-    for (int s = 1; s < splits; ++s) {
-        p += n / 4;
-        a += p[0];
-        b += p[1];
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (8 * i >= n) return;
+    const MX4_GLOBAL f32x4* p = (const MX4_GLOBAL f32x4*)(part + 8 * i);
+    f32x4 a = {0, 0, 0, 0}, b = a;
+    // four partials in flight: a call with few sums is bound by their latency
+    for (int s = 0; s < splits; s += 4) {
+        f32x4 v[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t at = (s + k < splits ? s + k : s) * (n / 4);
+            v[k][0] = p[at];
+            v[k][1] = p[at + 1];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (s + k < splits) {
+                a += v[k][0];
+                b += v[k][1];
+            }
+        }
     }
-    store8(out, kind, at, a, b);
+    const int64_t row = i / width8;
+    store8(out, kind, row * ldo + 8 * (i - row * width8), a, b);
 }
 
 bool mm_few(int64_t m) { return m <= 64; }
@@ -239,13 +295,18 @@ bool mm_few(int64_t m) { return m <= 64; }
 // Both operands in codes: k_few up to 64 tokens, and where a row is shorter than a step of the tiled kernel.
 bool mm4_few(int64_t cols, int64_t m) { return m <= 64 || cols < 256; }
 
+// Tiles of 16 tokens a workgroup, and how many workgroups they make.
 int token_tiles(int64_t m) { return m <= 16 ? 1 : m <= 32 ? 2 : 4; }
+uint32_t token_groups(int64_t m) { return (uint32_t)ceil_div(m, 16 * token_tiles(m)); }
+
+// Backward: columns of a wave.
+int back_columns(int64_t m) { return m <= 16 ? 256 : 128; }
 
 // Backward: parts of the reduction so that about 1,024 workgroups run, each
 // wave with two slabs at least.
 int back_parts(int64_t rows, int64_t cols, int64_t m)
 {
-    const int64_t groups = ceil_div(cols, 128) * ceil_div(m, 16 * token_tiles(m)), slabs = ceil_div(rows, 32);
+    const int64_t groups = ceil_div(cols, back_columns(m)) * ceil_div(m, 16 * token_tiles(m)), slabs = ceil_div(rows, 32);
     int64_t p = ceil_div(1024, groups);
     const int64_t most = ceil_div(slabs, 2 * kWaves);
     if (p > most) p = most;
@@ -256,10 +317,10 @@ template <int DT>
 hipError_t few_go(const FewArgs& a, hipStream_t s)
 {
     const int mt = token_tiles(a.m);
-    const dim3 grid((unsigned)ceil_div(a.rows, 32), (unsigned)ceil_div(a.m, 16 * mt));
-    if (mt == 1) k_few<DT, 2, 1><<<grid, 64 * kWaves, 0, s>>>(a);
-    else if (mt == 2) k_few<DT, 2, 2><<<grid, 64 * kWaves, 0, s>>>(a);
-    else k_few<DT, 2, 4><<<grid, 64 * kWaves, 0, s>>>(a);
+    const dim3 grid((unsigned)ceil_div(a.rows, 32) * a.token_tiles);
+    if (mt == 1) k_few<DT, 2, 1, 4><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (mt == 2) k_few<DT, 2, 2, 2><<<grid, 64 * kWaves, 0, s>>>(a);
+    else k_few<DT, 2, 4, 1><<<grid, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -267,18 +328,20 @@ template <int DT>
 hipError_t few_back_go(const FewArgs& a, hipStream_t s)
 {
     const int mt = token_tiles(a.m);
-    const dim3 grid((unsigned)ceil_div(a.cols, 128), (unsigned)ceil_div(a.m, 16 * mt), (unsigned)a.parts);
-    if (mt == 1) k_few_back<DT, 1><<<grid, 64 * kWaves, 0, s>>>(a);
-    else if (mt == 2) k_few_back<DT, 2><<<grid, 64 * kWaves, 0, s>>>(a);
-    else k_few_back<DT, 4><<<grid, 64 * kWaves, 0, s>>>(a);
+    const dim3 grid((unsigned)ceil_div(a.cols, back_columns(a.m)) * a.token_tiles, (unsigned)a.parts);
+    if (mt == 1) k_few_back<DT, 1, 2><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (mt == 2) k_few_back<DT, 2, 1><<<grid, 64 * kWaves, 0, s>>>(a);
+    else k_few_back<DT, 4, 1><<<grid, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_split_sum(const float* part, int splits, int64_t n, void* out, int out_kind, hipStream_t s)
+hipError_t launch_split_sum(const float* part, int splits, int64_t m, int64_t ncol, void* out, int64_t ldo, int out_kind,
+                            hipStream_t s)
 {
-    k_split_sum<<<(unsigned)ceil_div(n, 2048), 256, 0, s>>>(part, splits, n, out, out_kind);
+    const int64_t n = m * ncol;
+    k_split_sum<<<(unsigned)ceil_div(n, 2048), 256, 0, s>>>(part, splits, n, (int)(ncol / 8), out, ldo, out_kind);
     return hipGetLastError();
 }
 
@@ -294,12 +357,12 @@ hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales,
                          bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s)
 {
     if (!mm_few(m)) return launch_mm_tiled(dtype, codes, scales, rows, cols, forward, x, m, out, out_kind, part, s);
-    FewArgs a{codes, scales, x, nullptr, out, part, m, rows, cols, out_kind, 1};
+    FewArgs a{codes, scales, x, nullptr, out, part, m, rows, cols, out_kind, 1, token_groups(m)};
     if (forward) return dtype == 0 ? few_go<0>(a, s) : few_go<1>(a, s);
     a.parts = back_parts(rows, cols, m);
     const hipError_t e = dtype == 0 ? few_back_go<0>(a, s) : few_back_go<1>(a, s);
     if (e != hipSuccess || a.parts == 1) return e;
-    return launch_split_sum(part, a.parts, m * cols, out, out_kind, s);
+    return launch_split_sum(part, a.parts, m, cols, out, cols, out_kind, s);
 }
 
 size_t matmul4_ws(int64_t rows, int64_t cols, int64_t m) { return mm4_few(cols, m) ? 0 : mm4_tiled_ws(rows, cols, m); }
@@ -310,7 +373,7 @@ hipError_t launch_matmul4(const uint8_t* codes, const uint8_t* scales, int64_t r
 {
     if (!mm4_few(cols, m))
         return launch_mm4_tiled(codes, scales, rows, cols, xcodes, xscales, m, out, out_kind, part, s);
-    const FewArgs a{codes, scales, xcodes, xscales, out, nullptr, m, rows, cols, out_kind, 1};
+    const FewArgs a{codes, scales, xcodes, xscales, out, nullptr, m, rows, cols, out_kind, 1, token_groups(m)};
     return few_go<2>(a, s);
 }
 

@@ -48,7 +48,7 @@ struct MmArgs {
     const uint8_t *codes, *scales;    // W [rows x cols]
     const uint16_t* x;                // [m x kred]
     void* out;                        // [m x ncol], row pitch ldo
-    float* part;                      // parts > 1: fp32 [parts][m x ldo]
+    float* part;                      // parts > 1: fp32 [parts][m x ncol]
     int64_t m, ncol, ldo;
     int cols, kred, kind;
     TileGrid grid;
@@ -338,52 +338,22 @@ hipError_t mm_go(int dtype, bool forward, const MmArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-constexpr int kCus = 256;
+constexpr TileCosts kCosts = {1.62, 8.0, 0.87, 6.0};
 
-struct Plan {
-    TileGrid big, small;   // 256 x 256 tiles on the first columns, 128 x 128 on the others (nt 0: none)
-};
-
-Plan mm_plan(int64_t kred, int64_t ncol, int64_t m)
-{
-    const int steps = (int)ceil_div(kred, kStep);
-    Plan p = {};
-    const int64_t mt = ceil_div(m, 256), nt = ceil_div(ncol, 256);
-    if (mt * nt >= 200) {
-        const int64_t rounds = mt * nt / kCus, whole = rounds * kCus / mt;
-        const bool cut = rounds > 0 && whole > 0 && whole < nt && 4 * (mt * (nt - whole)) <= 3 * kCus;
-        const int64_t nb = cut ? whole : nt;
-        p.big = {(int)mt, (int)nb, 1, steps};
-        if (cut) p.small = {(int)ceil_div(m, 128), (int)ceil_div(ncol - 256 * nb, 128), 1, steps};
-        return p;
-    }
-    p.small = {(int)ceil_div(m, 128), (int)ceil_div(ncol, 128), 1, steps};
-    const int64_t tiles = (int64_t)p.small.mt * p.small.nt;
-    if (tiles < 256) {
-        int64_t parts = 512 / tiles;
-        if (parts > steps / 4) parts = steps / 4;
-        if (parts > 16) parts = 16;
-        if (parts > 1) {
-            p.small.per_part = (int)ceil_div(steps, parts);
-            p.small.parts = (int)ceil_div(steps, p.small.per_part);
-        }
-    }
-    return p;
-}
+TilePlan mm_plan(int64_t kred, int64_t ncol, int64_t m) { return tile_plan(m, ncol, (int)ceil_div(kred, kStep), kCosts); }
 
 }  // namespace
 
 size_t mm_tiled_ws(int64_t kred, int64_t ncol, int64_t m)
 {
-    const Plan p = mm_plan(kred, ncol, m);
-    return p.small.parts > 1 ? size_t(p.small.parts) * size_t(m) * size_t(ncol) * sizeof(float) : 0;
+    return plan_ws(mm_plan(kred, ncol, m), m, ncol);
 }
 
 hipError_t launch_mm_tiled(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                            bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s)
 {
     const int64_t kred = forward ? cols : rows, ncol = forward ? rows : cols;
-    const Plan p = mm_plan(kred, ncol, m);
+    const TilePlan p = mm_plan(kred, ncol, m);
     MmArgs a{codes, scales, static_cast<const uint16_t*>(x), out, part, m, ncol, ncol, (int)cols, (int)kred, out_kind, p.big};
     if (p.big.nt > 0) {
         const int64_t done = 256 * (int64_t)p.big.nt;
@@ -399,7 +369,7 @@ hipError_t launch_mm_tiled(int dtype, const uint8_t* codes, const uint8_t* scale
     a.grid = p.small;
     const hipError_t e = mm_go<2, 2>(dtype, forward, a, s);
     if (e != hipSuccess || p.small.parts == 1) return e;
-    return launch_split_sum(part, p.small.parts, m * ncol, out, out_kind, s);
+    return launch_split_sum(part, p.small.parts, m, a.ncol, a.out, ncol, out_kind, s);
 }
 
 }  // namespace mx4k

@@ -223,59 +223,22 @@ hipError_t mm4_go(Mm4Args a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Which tiles, and into how many parts the reduction goes.
-struct Plan {
-    TileGrid big;      // 256 x 256 tiles on the first big.nt * 256 columns (nt 0: none)
-    TileGrid small;    // 128 x 128 tiles on the others (nt 0: none)
-};
+constexpr TileCosts kCosts = {1.75, 7.0, 1.15, 6.0};
 
-constexpr int kCus = 256;
-
-// 200 tiles of 256 x 256 or more: whole rounds of them, one on each compute unit.
-// Tiles beyond the last whole round of at most three quarters of one run as four
-// small ones each, two on a compute unit (4096 x 13824 x 5120, 3.4 rounds: SMALL us
-// instead of 188).  Below 200 tiles small ones, with fewer than 256 of those the
-// reduction split.
-Plan mm4_plan(int64_t rows, int64_t cols, int64_t m)
-{
-    const int steps = (int)ceil_div(cols, kStep);
-    Plan p = {};
-    const int64_t mt = ceil_div(m, 256), nt = ceil_div(rows, 256);
-    if (mt * nt >= 200) {
-        const int64_t rounds = mt * nt / kCus, whole = rounds * kCus / mt;
-        const bool cut = rounds > 0 && whole > 0 && whole < nt && 4 * (mt * (nt - whole)) <= 3 * kCus;
-        const int64_t nb = cut ? whole : nt;
-        p.big = {(int)mt, (int)nb, 1, steps};
-        if (cut) p.small = {(int)ceil_div(m, 128), (int)ceil_div(rows - 256 * nb, 128), 1, steps};
-        return p;
-    }
-    p.small = {(int)ceil_div(m, 128), (int)ceil_div(rows, 128), 1, steps};
-    const int64_t tiles = (int64_t)p.small.mt * p.small.nt;
-    if (tiles < 256) {
-        int64_t parts = 512 / tiles;
-        if (parts > steps / 2) parts = steps / 2;
-        if (parts > 16) parts = 16;
-        if (parts > 1) {
-            p.small.per_part = (int)ceil_div(steps, parts);
-            p.small.parts = (int)ceil_div(steps, p.small.per_part);
-        }
-    }
-    return p;
-}
+TilePlan mm4_plan(int64_t rows, int64_t cols, int64_t m) { return tile_plan(m, rows, (int)ceil_div(cols, kStep), kCosts); }
 
 }  // namespace
 
 size_t mm4_tiled_ws(int64_t rows, int64_t cols, int64_t m)
 {
-    const Plan p = mm4_plan(rows, cols, m);
-    return p.small.parts > 1 ? size_t(p.small.parts) * size_t(m) * size_t(rows) * sizeof(float) : 0;
+    return plan_ws(mm4_plan(rows, cols, m), m, rows);
 }
 
 hipError_t launch_mm4_tiled(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                             const uint8_t* xcodes, const uint8_t* xscales, int64_t m, void* out, int out_kind,
                             float* part, hipStream_t s)
 {
-    const Plan p = mm4_plan(rows, cols, m);
+    const TilePlan p = mm4_plan(rows, cols, m);
     Mm4Args a{codes, scales, xcodes, xscales, out, part, m, rows, rows, (int)cols, out_kind, p.big};
     if (p.big.nt > 0) {
         const int64_t done = 256 * (int64_t)p.big.nt;
@@ -290,7 +253,7 @@ hipError_t launch_mm4_tiled(const uint8_t* codes, const uint8_t* scales, int64_t
     a.grid = p.small;
     const hipError_t e = mm4_go<2, 2>(a, s);
     if (e != hipSuccess || p.small.parts == 1) return e;
-    return launch_split_sum(part, p.small.parts, m * rows, out, out_kind, s);
+    return launch_split_sum(part, p.small.parts, m, a.rows, a.out, rows, out_kind, s);
 }
 
 }  // namespace mx4k

@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int64_t kMaxN = int64_t(1) << 40, kMaxSide = int64_t(1) << 22, kMaxTokens = int64_t(1) << 25;
+constexpr int64_t kMaxN = int64_t(1) << 40, kMaxSide = int64_t(1) << 22, kMaxTokens = int64_t(1) << 25, kMaxOut = int64_t(1) << 38;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -25,6 +25,8 @@ nf4_status check_product(int64_t rows, int64_t cols, int64_t m, int32_t dtype, i
 {
     if (dtype != NF4_BF16 && dtype != NF4_FP16) return NF4_E_UNSUPPORTED;
     if (rows <= 0 || rows >= kMaxSide || cols <= 0 || cols >= kMaxSide || m <= 0 || m > kMaxTokens) return NF4_E_ARG;
+    // more outputs than memory holds; the grids count their tiles in 32 bits
+    if (m * (rows > cols ? rows : cols) > kMaxOut) return NF4_E_ARG;
     if (rows > (kMaxN - 1) / cols || (out_fp32 != 0 && out_fp32 != 1)) return NF4_E_ARG;
     return rows % 8 || cols % 32 ? NF4_E_UNSUPPORTED : NF4_OK;
 }

@@ -40,8 +40,9 @@ hipError_t launch_mm4_tiled(const uint8_t* codes, const uint8_t* scales, int64_t
                             const uint8_t* xcodes, const uint8_t* xscales, int64_t m, void* out, int out_kind,
                             float* part, hipStream_t s);
 
-// The sum of `splits` fp32 partials of n values each (a multiple of 8) in split
-// order, to out (mx4_sum.h).
-hipError_t launch_split_sum(const float* part, int splits, int64_t n, void* out, int out_kind, hipStream_t s);
+// The sum of `splits` fp32 partials [m x ncol] (ncol a multiple of 8) in split
+// order, to out with row pitch ldo.
+hipError_t launch_split_sum(const float* part, int splits, int64_t m, int64_t ncol, void* out, int64_t ldo, int out_kind,
+                            hipStream_t s);
 
 }  // namespace mx4k

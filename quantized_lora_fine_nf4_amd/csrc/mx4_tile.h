@@ -17,6 +17,68 @@ struct TileGrid {
     int per_part;     // its steps per split
 };
 
+// How the output is cut: 256 x 256 tiles on the first 256 * big.nt columns, 128 x
+// 128 tiles on the others (nt 0: none there).
+struct TilePlan {
+    TileGrid big, small;
+};
+
+constexpr int kCus = 256;
+
+// Measured on this card, in us: a step of the reduction and what a tile costs
+// besides (its start and its stores), for a round of big tiles (one on each compute
+// unit) and of small ones (two on each, the same with one).
+struct TileCosts {
+    double big_step, big_tile, small_step, small_tile;
+};
+
+// The small tiles of m x ncol outputs: into how many parts their reduction goes and
+// what that costs, the partials at 5 TB/s and their sum's launch included.
+inline TileGrid small_plan(int64_t m, int64_t ncol, int steps, const TileCosts& c, double* cost)
+{
+    TileGrid best = {(int)ceil_div(m, 128), (int)ceil_div(ncol, 128), 1, steps};
+    const int64_t tiles = (int64_t)best.mt * best.nt;
+    *cost = ceil_div(tiles, 2 * kCus) * (steps * c.small_step + c.small_tile);
+    for (int p = 2; p <= 16 && p <= steps; ++p) {
+        const int per = (int)ceil_div(steps, p), parts = (int)ceil_div(steps, per);
+        const double us = ceil_div(tiles * parts, 2 * kCus) * (per * c.small_step + c.small_tile) + 6.0 +
+                          double(parts) * double(m) * double(ncol) * 8e-6 / 2.5;
+        if (us < *cost) {
+            *cost = us;
+            best.parts = parts;
+            best.per_part = per;
+        }
+    }
+    return best;
+}
+
+// The cheapest of: small tiles only, big ones only, whole rounds of big ones and
+// small ones on the columns that are left.
+inline TilePlan tile_plan(int64_t m, int64_t ncol, int steps, const TileCosts& c)
+{
+    TilePlan p = {};
+    double least;
+    p.small = small_plan(m, ncol, steps, c, &least);
+    const int64_t mt = ceil_div(m, 256), nt = ceil_div(ncol, 256), rounds = mt * nt / kCus, fit = rounds * kCus / mt;
+    const double round = steps * c.big_step + c.big_tile;
+    if (ceil_div(mt * nt, kCus) * round < least) {
+        least = ceil_div(mt * nt, kCus) * round;
+        p = TilePlan{{(int)mt, (int)nt, 1, steps}, {}};
+    }
+    if (fit > 0 && fit < nt) {
+        double rest;
+        const TileGrid small = small_plan(m, ncol - 256 * fit, steps, c, &rest);
+        if (rounds * round + rest < least) p = TilePlan{{(int)mt, (int)fit, 1, steps}, small};
+    }
+    return p;
+}
+
+// fp32 partials of the small tiles' columns, [parts][m][those columns].
+inline size_t plan_ws(const TilePlan& p, int64_t m, int64_t ncol)
+{
+    return p.small.parts > 1 ? size_t(p.small.parts) * size_t(m) * size_t(ncol - 256 * p.big.nt) * sizeof(float) : 0;
+}
+
 // Consecutive workgroups go to the eight XCDs in turn, each with an L2 of its
 // own: every XCD takes a contiguous run of an order in which kBand row tiles at a
 // time walk along the columns, so that the tiles that run together share rows of
@@ -72,15 +134,16 @@ __device__ __forceinline__ float neighbour(float v) { return __builtin_bit_cast(
 // workgroup's tile begins at (m0, n0); wave (wm, wn), lane (r, h): columns TN r to
 // TN r + TN - 1 of the wave's, rows 8 a + 4 h + b of each 32.  PAIRS (TN 4): lane
 // r = 8 q + i has columns 32 q + 2 i, + 1, + 16, + 17 instead; an even lane gives its
-// upper pair for its neighbour's lower one.  ncol: out's columns, ldo its row pitch
-// (the partials' too).
+// upper pair for its neighbour's lower one.  ncol: the columns of the call's region,
+// and a partial's row pitch; ldo: out's.
 template <int TM, int TN, bool PAIRS = false>
 __device__ __forceinline__ void store_tile(f32x16 (&acc)[TM][TN], void* dst, float* partial, int dst_kind,
-                                           const TileGrid& grid, int part, int64_t m, int64_t ncol, int64_t ldo,
+                                           const TileGrid& grid, int part, int64_t m, int64_t ncol, int64_t out_pitch,
                                            int64_t m0, int64_t n0, int wm, int wn, int r, int h)
 {
     constexpr int kBM = 64 * TM;
     const bool split = grid.parts > 1;
+    const int64_t ldo = split ? ncol : out_pitch;
     char* out = split ? (char*)(partial + (int64_t)part * m * ldo) : (char*)dst;
     const int kind = split ? (int)kOutFp32 : dst_kind;
     const int odd = r & 1;
