@@ -67,8 +67,8 @@ __device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? 
 
 constexpr int kWaves = 8;
 
-// DT 0, 1: x in bf16, fp16; 2: in codes.  kAhead steps of the weight in flight.
-template <int DT, int kRT, int kMT, int kAhead>
+// DT 0, 1: x in bf16, fp16; 2: in codes.
+template <int DT, int kRT, int kMT>
 __global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
 {
     __shared__ f32x4 sums[kWaves][kRT * kMT][64];
@@ -95,50 +95,38 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
     f32x4 acc[kRT][kMT] = {};
     u32x4 x[kMT][DT == 2 ? 1 : 4] = {};
     uint32_t e[kMT] = {};
-    for (int64_t at = 4 * wave; at < blocks; at += 4 * kWaves * kAhead) {
-        u32x4 c[kAhead][kRT];
-        uint32_t s[kAhead][kRT];
+    for (int64_t blk = 4 * wave + g; blk - g < blocks; blk += 4 * kWaves) {
+        const bool in = blk < blocks;   // a block is whole or not there
+        u32x4 c[kRT];
+        uint32_t s[kRT];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int64_t blk = at + 4 * kWaves * k + g;
-            const bool in = blk < blocks;   // a block is whole or not there
+        for (int i = 0; i < kRT; ++i) {
+            c[i] = in ? *(const MX4_GLOBAL u32x4*)(wc[i] + 16 * blk) : kZero;
+            s[i] = in ? ws[i][blk] : 0u;
+        }
 #pragma unroll
-            for (int i = 0; i < kRT; ++i) {
-                c[k][i] = in ? *(const MX4_GLOBAL u32x4*)(wc[i] + 16 * blk) : kZero;
-                s[k][i] = in ? ws[i][blk] : 0u;
+        for (int u = 0; u < kMT; ++u) {
+            if (16 * u + r < here) {
+                if constexpr (DT == 2) {
+                    x[u][0] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 16 * blk) : kZero;
+                    e[u] = in ? xs[u][blk] : 0u;
+                } else {
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) x[u][f] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 64 * blk + 16 * f) : kZero;
+                }
             }
         }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int64_t blk = at + 4 * kWaves * k + g;
-            if (blk - g >= blocks) break;
-            const bool in = blk < blocks;
+        for (int i = 0; i < kRT; ++i) {
+            if constexpr (DT == 2) {
 #pragma unroll
-            for (int u = 0; u < kMT; ++u) {
-                if constexpr (DT == 2) {
-                    if (16 * u + r < here) {
-                        x[u][0] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 16 * blk) : kZero;
-                        e[u] = in ? xs[u][blk] : 0u;
-                    }
-                } else {
-                    if (16 * u + r < here) {
+                for (int u = 0; u < kMT; ++u) acc[i][u] = mfma4(c[i], s[i], x[u][0], e[u], acc[i][u]);
+            } else {
 #pragma unroll
-                        for (int f = 0; f < 4; ++f) x[u][f] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 64 * blk + 16 * f) : kZero;
-                    }
-                }
-            }
+                for (int f = 0; f < 4; ++f) {
+                    const u32x4 w = decode8<DT>(c[i][f], scale_arg(s[i]));
 #pragma unroll
-            for (int i = 0; i < kRT; ++i) {
-                if constexpr (DT == 2) {
-#pragma unroll
-                    for (int u = 0; u < kMT; ++u) acc[i][u] = mfma4(c[k][i], s[k][i], x[u][0], e[u], acc[i][u]);
-                } else {
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const u32x4 w = decode8<DT>(c[k][i][f], scale_arg(s[k][i]));
-#pragma unroll
-                        for (int u = 0; u < kMT; ++u) acc[i][u] = mfma16<DT>(w, x[u][f], acc[i][u]);
-                    }
+                    for (int u = 0; u < kMT; ++u) acc[i][u] = mfma16<DT>(w, x[u][f], acc[i][u]);
                 }
             }
         }
@@ -157,6 +145,79 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
         const int64_t t = t0 + 16 * (tile % kMT) + (l & 15), n = n0 + 16 * (tile / kMT) + 4 * (l >> 4);
         if (t < a.m && n < a.rows) store4(a.out, a.kind, t * a.rows + n, v);
     }
+}
+
+// One token, forward.  A matrix instruction's lanes lie along the rows, so that
+// each of a load's quads touches four lines; here kWidth waves read four whole rows,
+// 16 bytes a lane, and a lane keeps its 32 values of x in fp32 for the four (13824 x
+// 5120 11.5 us, k_few 13.4; 5120 x 13824 with one wave 16.5, with two 10.2).
+template <int DT, int kWidth>
+__global__ __launch_bounds__(64 * kWidth) void k_one(FewArgs a)
+{
+    constexpr int kRows = 4;
+    __shared__ float other[kRows];
+    const int t = threadIdx.x;
+    const int64_t n0 = (int64_t)blockIdx.x * kRows, blocks = a.cols / kGroup;
+    const MX4_GLOBAL uint8_t *wc[kRows], *ws[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        wc[i] = (const MX4_GLOBAL uint8_t*)a.codes + (n0 + i) * 16 * blocks;   // rows come in eights
+        ws[i] = (const MX4_GLOBAL uint8_t*)a.scales + (n0 + i) * blocks;
+    }
+    float sum[kRows] = {};
+    for (int64_t first = 0; first < blocks; first += 64 * kWidth) {
+        const bool in = first + t < blocks;
+        const int64_t blk = in ? first + t : first;
+        float x[32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const u32x4 v = ((const MX4_GLOBAL u32x4*)a.x)[4 * blk + q];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f32x2 p = unpack2<DT>(in ? v[j] : 0u);
+                x[8 * q + 2 * j] = p.x;
+                x[8 * q + 2 * j + 1] = p.y;
+            }
+        }
+        u32x4 c[kRows];
+        uint32_t s[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            c[i] = *(const MX4_GLOBAL u32x4*)(wc[i] + 16 * blk);
+            s[i] = ws[i][blk];
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const float arg = scale_arg(in ? s[i] : 0u);   // past the end: finite, times 0
+            float even = 0, odd = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f32x2 p[4];
+                decode8_fp32<DT>(c[i][q], arg, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    even = __builtin_fmaf(p[j].x, x[8 * q + 2 * j], even);
+                    odd = __builtin_fmaf(p[j].y, x[8 * q + 2 * j + 1], odd);
+                }
+            }
+            sum[i] += even + odd;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) sum[i] += __shfl_xor(sum[i], o);
+    }
+    if constexpr (kWidth == 2) {
+        if (t == 64) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) other[i] = sum[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) sum[i] += other[i];
+    }
+    if (t == 0) store4(a.out, a.kind, n0, f32x4{sum[0], sum[1], sum[2], sum[3]});
 }
 
 // The low and the high halves of two dwords, put together.
@@ -290,14 +351,44 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
     store8(out, kind, row * ldo + 8 * (i - row * width8), a, b);
 }
 
-bool mm_few(int64_t m) { return m <= 64; }
+// k_few's time: about 4 us, and 30 ns for each load instruction of a compute unit
+// (64 lanes on 64 lines).  kRT x kMT tiles of 16 x 16 a wave, as many as leave 160
+// workgroups (4096 x 4096, 4 tokens: 1 x 1 5.7 us, 2 x 1 7.5; 13824 x 5120, 16
+// tokens: 4 x 1 16.1, 2 x 1 20.5, 1 x 1 29.6).
+struct FewPlan {
+    int rt, mt;
+    double us;
+};
 
-// Both operands in codes: k_few up to 64 tokens, and where a row is shorter than a step of the tiled kernel.
-bool mm4_few(int64_t cols, int64_t m) { return m <= 64 || cols < 256; }
+FewPlan few_plan(int64_t rows, int64_t cols, int64_t m, bool codes)
+{
+    FewPlan best = {};
+    for (int rt = 4; rt; rt >>= 1)
+        for (int mt = 4; mt; mt >>= 1) {
+            if (mt > 1 && 8 * mt >= m) continue;   // half of it would be empty
+            const double groups = double(ceil_div(rows, 16 * rt)) * double(ceil_div(m, 16 * mt));
+            if ((groups < 160 && rt * mt > 1) || rt * mt <= best.rt * best.mt) continue;
+            const double full = m < 16 ? m / 16.0 : 1.0;   // lanes of x that read
+            const double loads = double(ceil_div(cols, 128)) * (2 * rt + (codes ? 2 : 4) * mt * full);
+            best = {rt, mt, 4.0 + (groups > 256 ? groups / 256 : 1) * loads * 0.03};
+        }
+    return best;
+}
 
-// Tiles of 16 tokens a workgroup, and how many workgroups they make.
+// Against the tiled kernels' estimate.  Those take at least 256 columns with both operands in codes.
+bool mm_few(int64_t rows, int64_t cols, int64_t m, bool forward)
+{
+    if (!forward) return m <= 64;
+    return m == 1 || (m <= 64 && few_plan(rows, cols, m, false).us < mm_tiled_us(cols, rows, m));
+}
+bool mm4_few(int64_t rows, int64_t cols, int64_t m)
+{
+    return cols < 256 || (m <= 64 && few_plan(rows, cols, m, true).us < mm4_tiled_us(rows, cols, m));
+}
+
+// Tiles of 16 tokens a workgroup takes backward, and how many workgroups they make.
 int token_tiles(int64_t m) { return m <= 16 ? 1 : m <= 32 ? 2 : 4; }
-uint32_t token_groups(int64_t m) { return (uint32_t)ceil_div(m, 16 * token_tiles(m)); }
+uint32_t token_groups(int64_t m, int tiles) { return (uint32_t)ceil_div(m, 16 * tiles); }
 
 // Backward: columns of a wave.
 int back_columns(int64_t m) { return m <= 16 ? 256 : 128; }
@@ -313,15 +404,31 @@ int back_parts(int64_t rows, int64_t cols, int64_t m)
     return (int)(p < 1 ? 1 : p > 16 ? 16 : p);
 }
 
-template <int DT>
-hipError_t few_go(const FewArgs& a, hipStream_t s)
+template <int DT, int kRT>
+hipError_t few_tokens(const FewArgs& a, int mt, hipStream_t s)
 {
-    const int mt = token_tiles(a.m);
-    const dim3 grid((unsigned)ceil_div(a.rows, 32) * a.token_tiles);
-    if (mt == 1) k_few<DT, 2, 1, 4><<<grid, 64 * kWaves, 0, s>>>(a);
-    else if (mt == 2) k_few<DT, 2, 2, 2><<<grid, 64 * kWaves, 0, s>>>(a);
-    else k_few<DT, 2, 4, 1><<<grid, 64 * kWaves, 0, s>>>(a);
+    const dim3 grid((unsigned)ceil_div(a.rows, 16 * kRT) * a.token_tiles);
+    if (mt == 1) k_few<DT, kRT, 1><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (mt == 2) k_few<DT, kRT, 2><<<grid, 64 * kWaves, 0, s>>>(a);
+    else k_few<DT, kRT, 4><<<grid, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <int DT>
+hipError_t few_go(FewArgs a, hipStream_t s)
+{
+    if (DT != 2 && a.m == 1) {
+        if constexpr (DT != 2) {
+            // two waves where a row is more than four segments of one
+            if (a.cols > 8192) k_one<DT, 2><<<(unsigned)(a.rows / 4), 128, 0, s>>>(a);
+            else k_one<DT, 1><<<(unsigned)(a.rows / 4), 64, 0, s>>>(a);
+        }
+        return hipGetLastError();
+    }
+    const FewPlan p = few_plan(a.rows, a.cols, a.m, DT == 2);
+    a.token_tiles = token_groups(a.m, p.mt);
+    if (p.rt == 4) return few_tokens<DT, 4>(a, p.mt, s);
+    return p.rt == 2 ? few_tokens<DT, 2>(a, p.mt, s) : few_tokens<DT, 1>(a, p.mt, s);
 }
 
 template <int DT>
@@ -347,7 +454,7 @@ hipError_t launch_split_sum(const float* part, int splits, int64_t m, int64_t nc
 
 size_t matmul_ws(int64_t rows, int64_t cols, bool forward, int64_t m)
 {
-    if (!mm_few(m)) return forward ? mm_tiled_ws(cols, rows, m) : mm_tiled_ws(rows, cols, m);
+    if (!mm_few(rows, cols, m, forward)) return forward ? mm_tiled_ws(cols, rows, m) : mm_tiled_ws(rows, cols, m);
     if (forward) return 0;
     const int parts = back_parts(rows, cols, m);
     return parts > 1 ? size_t(parts) * size_t(m) * size_t(cols) * sizeof(float) : 0;
@@ -356,8 +463,8 @@ size_t matmul_ws(int64_t rows, int64_t cols, bool forward, int64_t m)
 hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                          bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s)
 {
-    if (!mm_few(m)) return launch_mm_tiled(dtype, codes, scales, rows, cols, forward, x, m, out, out_kind, part, s);
-    FewArgs a{codes, scales, x, nullptr, out, part, m, rows, cols, out_kind, 1, token_groups(m)};
+    if (!mm_few(rows, cols, m, forward)) return launch_mm_tiled(dtype, codes, scales, rows, cols, forward, x, m, out, out_kind, part, s);
+    FewArgs a{codes, scales, x, nullptr, out, part, m, rows, cols, out_kind, 1, token_groups(m, token_tiles(m))};
     if (forward) return dtype == 0 ? few_go<0>(a, s) : few_go<1>(a, s);
     a.parts = back_parts(rows, cols, m);
     const hipError_t e = dtype == 0 ? few_back_go<0>(a, s) : few_back_go<1>(a, s);
@@ -365,15 +472,15 @@ hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales,
     return launch_split_sum(part, a.parts, m, cols, out, cols, out_kind, s);
 }
 
-size_t matmul4_ws(int64_t rows, int64_t cols, int64_t m) { return mm4_few(cols, m) ? 0 : mm4_tiled_ws(rows, cols, m); }
+size_t matmul4_ws(int64_t rows, int64_t cols, int64_t m) { return mm4_few(rows, cols, m) ? 0 : mm4_tiled_ws(rows, cols, m); }
 
 hipError_t launch_matmul4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                           const uint8_t* xcodes, const uint8_t* xscales, int64_t m, void* out, int out_kind,
                           float* part, hipStream_t s)
 {
-    if (!mm4_few(cols, m))
+    if (!mm4_few(rows, cols, m))
         return launch_mm4_tiled(codes, scales, rows, cols, xcodes, xscales, m, out, out_kind, part, s);
-    const FewArgs a{codes, scales, xcodes, xscales, out, nullptr, m, rows, cols, out_kind, 1, token_groups(m)};
+    const FewArgs a{codes, scales, xcodes, xscales, out, nullptr, m, rows, cols, out_kind, 1, 1};
     return few_go<2>(a, s);
 }
 

@@ -344,6 +344,13 @@ TilePlan mm_plan(int64_t kred, int64_t ncol, int64_t m) { return tile_plan(m, nc
 
 }  // namespace
 
+double mm_tiled_us(int64_t kred, int64_t ncol, int64_t m)
+{
+    double us;
+    tile_plan(m, ncol, (int)ceil_div(kred, kStep), kCosts, &us);
+    return us;
+}
+
 size_t mm_tiled_ws(int64_t kred, int64_t ncol, int64_t m)
 {
     return plan_ws(mm_plan(kred, ncol, m), m, ncol);

@@ -229,6 +229,13 @@ TilePlan mm4_plan(int64_t rows, int64_t cols, int64_t m) { return tile_plan(m, r
 
 }  // namespace
 
+double mm4_tiled_us(int64_t rows, int64_t cols, int64_t m)
+{
+    double us;
+    tile_plan(m, rows, (int)ceil_div(cols, kStep), kCosts, &us);
+    return us;
+}
+
 size_t mm4_tiled_ws(int64_t rows, int64_t cols, int64_t m)
 {
     return plan_ws(mm4_plan(rows, cols, m), m, rows);

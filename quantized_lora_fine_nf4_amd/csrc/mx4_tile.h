@@ -54,7 +54,7 @@ inline TileGrid small_plan(int64_t m, int64_t ncol, int steps, const TileCosts& 
 
 // The cheapest of: small tiles only, big ones only, whole rounds of big ones and
 // small ones on the columns that are left.
-inline TilePlan tile_plan(int64_t m, int64_t ncol, int steps, const TileCosts& c)
+inline TilePlan tile_plan(int64_t m, int64_t ncol, int steps, const TileCosts& c, double* us = nullptr)
 {
     TilePlan p = {};
     double least;
@@ -68,8 +68,12 @@ inline TilePlan tile_plan(int64_t m, int64_t ncol, int steps, const TileCosts& c
     if (fit > 0 && fit < nt) {
         double rest;
         const TileGrid small = small_plan(m, ncol - 256 * fit, steps, c, &rest);
-        if (rounds * round + rest < least) p = TilePlan{{(int)mt, (int)fit, 1, steps}, small};
+        if (rounds * round + rest < least) {
+            least = rounds * round + rest;
+            p = TilePlan{{(int)mt, (int)fit, 1, steps}, small};
+        }
     }
+    if (us) *us = least;
     return p;
 }
 
