@@ -5,12 +5,12 @@
 //   forward   out[t, n] = sum_k x[t, k] W[n, k]
 //   backward  out[t, k] = sum_n x[t, n] W[n, k]
 //
-// Forward: a wave takes kRT x 16 weight rows and every kWaves-th step of 128
-// columns.  Lane (r, g) holds row r's 32 codes of block g: one load, one scale.
-// In 16 bits they make four fragments of v_mfma_f32_16x16x32 (the reduction index
-// of element j of fragment f in group g is 32 g + 8 f + j; x is read to match);
-// with x in 4 bits too, they are the operand of v_mfma_scale_f32_16x16x128 as they
-// are.  The waves' sums meet in LDS.
+// Forward: a wave takes kRT x 16 weight rows and every kWaves-th run of 512
+// columns.  Lane (r, g) holds four blocks of 32 of row r, block 4 g + j in the j-th
+// of four steps: one load each and one for their four scales.  In 16 bits a block
+// makes four fragments of v_mfma_f32_16x16x32 (x is read to match: any order of the
+// reduction will do that is the same on both sides); with x in 4 bits too, it is the
+// operand of v_mfma_scale_f32_16x16x128 as it is.  The waves' sums meet in LDS.
 //
 // Backward the reduction runs over the weight's rows, whose scales differ.  Lane
 // (r, g) reads eight or sixteen columns of rows 8 g .. 8 g + 7 of a 32-row slab; a
@@ -20,6 +20,8 @@
 // consecutive columns.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "mx4_format.h"
 #include "mx4_launch.h"
@@ -44,11 +46,12 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f3
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+template <int S>
 __device__ __forceinline__ f32x4 mfma4(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb, const f32x4& c)
 {
     const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
     const i32x8 y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)sa, 0, (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
 struct FewArgs {
@@ -66,6 +69,18 @@ struct FewArgs {
 __device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 
 constexpr int kWaves = 8;
+
+// Four scales of a row in one dword; past its end zeros.
+__device__ __forceinline__ uint32_t load_scales(const MX4_GLOBAL uint8_t* p, int have)
+{
+    uint32_t v = 0;
+    if (have == 4) {
+        __builtin_memcpy(&v, (const uint8_t*)p, 4);
+    } else {
+        for (int i = 0; i < have; ++i) v |= (uint32_t)p[i] << (8 * i);
+    }
+    return v;
+}
 
 // DT 0, 1: x in bf16, fp16; 2: in codes.
 template <int DT, int kRT, int kMT>
@@ -95,41 +110,57 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
     f32x4 acc[kRT][kMT] = {};
     u32x4 x[kMT][DT == 2 ? 1 : 4] = {};
     uint32_t e[kMT] = {};
-    for (int64_t blk = 4 * wave + g; blk - g < blocks; blk += 4 * kWaves) {
-        const bool in = blk < blocks;   // a block is whole or not there
-        u32x4 c[kRT];
+    for (int64_t at = 16 * wave; at < blocks; at += 16 * kWaves) {
+        const int64_t blk = at + 4 * g;                      // this lane's four
+        const int have = (int)least(blocks - blk, 4);
         uint32_t s[kRT];
 #pragma unroll
-        for (int i = 0; i < kRT; ++i) {
-            c[i] = in ? *(const MX4_GLOBAL u32x4*)(wc[i] + 16 * blk) : kZero;
-            s[i] = in ? ws[i][blk] : 0u;
-        }
+        for (int i = 0; i < kRT; ++i) s[i] = load_scales(ws[i] + blk, have);
+        if constexpr (DT == 2) {
 #pragma unroll
-        for (int u = 0; u < kMT; ++u) {
-            if (16 * u + r < here) {
+            for (int u = 0; u < kMT; ++u)
+                if (16 * u + r < here) e[u] = load_scales(xs[u] + blk, have);
+        }
+        u32x4 c[4][kRT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < kRT; ++i) c[j][i] = j < have ? *(const MX4_GLOBAL u32x4*)(wc[i] + 16 * (blk + j)) : kZero;
+        auto part = [&](auto which) {
+            constexpr int j = which;
+            const bool in = j < have;
+#pragma unroll
+            for (int u = 0; u < kMT; ++u) {
+                if (16 * u + r < here) {
+                    if constexpr (DT == 2) {
+                        x[u][0] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 16 * (blk + j)) : kZero;
+                    } else {
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            x[u][f] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 64 * (blk + j) + 16 * f) : kZero;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kRT; ++i) {
                 if constexpr (DT == 2) {
-                    x[u][0] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 16 * blk) : kZero;
-                    e[u] = in ? xs[u][blk] : 0u;
+#pragma unroll
+                    for (int u = 0; u < kMT; ++u) acc[i][u] = mfma4<j>(c[j][i], s[i], x[u][0], e[u], acc[i][u]);
                 } else {
+                    const float arg = byte_arg<j>(s[i]);
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) x[u][f] = in ? *(const MX4_GLOBAL u32x4*)(xc[u] + 64 * blk + 16 * f) : kZero;
+                    for (int f = 0; f < 4; ++f) {
+                        const u32x4 w = decode8<DT>(c[j][i][f], arg);
+#pragma unroll
+                        for (int u = 0; u < kMT; ++u) acc[i][u] = mfma16<DT>(w, x[u][f], acc[i][u]);
+                    }
                 }
             }
-        }
-#pragma unroll
-        for (int i = 0; i < kRT; ++i) {
-            if constexpr (DT == 2) {
-#pragma unroll
-                for (int u = 0; u < kMT; ++u) acc[i][u] = mfma4(c[i], s[i], x[u][0], e[u], acc[i][u]);
-            } else {
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const u32x4 w = decode8<DT>(c[i][f], scale_arg(s[i]));
-#pragma unroll
-                    for (int u = 0; u < kMT; ++u) acc[i][u] = mfma16<DT>(w, x[u][f], acc[i][u]);
-                }
-            }
-        }
+        };
+        part(std::integral_constant<int, 0>{});
+        part(std::integral_constant<int, 1>{});
+        part(std::integral_constant<int, 2>{});
+        part(std::integral_constant<int, 3>{});
     }
 #pragma unroll
     for (int i = 0; i < kRT; ++i)

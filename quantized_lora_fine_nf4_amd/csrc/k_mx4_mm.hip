@@ -199,10 +199,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
         }
         rawscale[to] = *(const u32x2*)(b.s + (wn * TN + r * TN / 32) * 64 + 32 * h + 8 * f);
     };
-    // the conversions look at the exponent field alone: a byte of packed scales needs a shift and no mask
-    auto byte_arg = [](uint32_t v, int b) {
-        return __builtin_bit_cast(float, b == 3 ? v >> 1 : v << (23 - 8 * b));
-    };
     auto decode_next = [&](int f, int which, int to) {   // forward: sub-step f of step `which`
 #pragma unroll
         for (int j = 0; j < TN; ++j) fw[to][j] = decode8<DT>(code[which][j][f], scale_arg(scale[which][j]));
@@ -212,10 +208,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
 #pragma unroll
         for (int k = 0; k < TN / 2; ++k) {
             const uint32_t c0 = raw[from][k][0], c1 = raw[from][k][1];
-            const uint32_t v[8] = {decode2<DT, 0>(c0, byte_arg(s0, 0)), decode2<DT, 1>(c0, byte_arg(s0, 1)),
-                                   decode2<DT, 2>(c0, byte_arg(s0, 2)), decode2<DT, 3>(c0, byte_arg(s0, 3)),
-                                   decode2<DT, 0>(c1, byte_arg(s1, 0)), decode2<DT, 1>(c1, byte_arg(s1, 1)),
-                                   decode2<DT, 2>(c1, byte_arg(s1, 2)), decode2<DT, 3>(c1, byte_arg(s1, 3))};
+            const uint32_t v[8] = {decode2<DT, 0>(c0, byte_arg<0>(s0)), decode2<DT, 1>(c0, byte_arg<1>(s0)),
+                                   decode2<DT, 2>(c0, byte_arg<2>(s0)), decode2<DT, 3>(c0, byte_arg<3>(s0)),
+                                   decode2<DT, 0>(c1, byte_arg<0>(s1)), decode2<DT, 1>(c1, byte_arg<1>(s1)),
+                                   decode2<DT, 2>(c1, byte_arg<2>(s1)), decode2<DT, 3>(c1, byte_arg<3>(s1))};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 fw[to][2 * k][j] = low16(v[2 * j], v[2 * j + 1]);

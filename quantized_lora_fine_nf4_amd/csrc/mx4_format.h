@@ -6,7 +6,8 @@
 // gfx950 converts from and to these codes itself: the conversions take the
 // scale as an fp32 whose exponent field is s.  Every finite 16-bit input under 15
 // scales from 0 to 254 and every code under every scale was compared with the
-// definition: equal, ties to even, 6 beyond the range, s = 0 as 2^-127, 255 as NaN.
+// definition: equal, ties to even, 6 beyond the range, s = 0 as 2^-127, 255 as NaN;
+// sign and mantissa of the scale's fp32 do not matter.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -21,6 +22,14 @@ constexpr int kGroup = 32;   // elements per scale
 
 // The fp32 that the conversions read as scale s.
 __device__ __forceinline__ float scale_arg(uint32_t s) { return __builtin_bit_cast(float, s << 23); }
+
+// The same from byte B of four packed scales: the conversions look at the exponent
+// field alone, so a shift will do and no mask is needed.
+template <int B>
+__device__ __forceinline__ float byte_arg(uint32_t s)
+{
+    return __builtin_bit_cast(float, B == 3 ? s >> 1 : s << (23 - 8 * B));
+}
 
 // The two codes of byte `B` of a dword to two 16-bit values of type DT (0 bf16,
 // 1 fp16), each code's value times 2^(s - 127) rounded once.
