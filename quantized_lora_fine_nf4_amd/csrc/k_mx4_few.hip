@@ -178,77 +178,85 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
     }
 }
 
-// One token, forward.  A matrix instruction's lanes lie along the rows, so that
-// each of a load's quads touches four lines; here kWidth waves read four whole rows,
-// 16 bytes a lane, and a lane keeps its 32 values of x in fp32 for the four (13824 x
-// 5120 11.5 us, k_few 13.4; 5120 x 13824 with one wave 16.5, with two 10.2).
-template <int DT, int kWidth>
-__global__ __launch_bounds__(64 * kWidth) void k_one(FewArgs a)
+// Up to 16 tokens, forward.  The 16 rows of a matrix instruction's first operand are
+// four weight rows times four neighbouring blocks b, those of the second four tokens
+// times the same four blocks; of the products only those of equal b count, the
+// diagonals, and the quad's four are added at the end.  So four neighbouring lanes
+// read 64 bytes in a row, where k_few's sixteen rows cost a line for each lane.  A
+// run is 512 columns (lane (a, b, g): row a, block 4 g + b); kRT x 4 rows and kTG x 4
+// tokens a wave.  Seven tokens through 5120 x 13824, both operands in codes: 8.1 us,
+// k_few 15.4; two through 13824 x 5120 in 16 bits 9.9, k_few 13.8.
+template <int DT, int kRT, int kTG, int kThinWaves>
+__global__ __launch_bounds__(64 * kThinWaves) void k_thin(FewArgs a)
 {
-    constexpr int kRows = 4;
-    __shared__ float other[kRows];
-    const int t = threadIdx.x;
-    const int64_t n0 = (int64_t)blockIdx.x * kRows, blocks = a.cols / kGroup;
-    const MX4_GLOBAL uint8_t *wc[kRows], *ws[kRows];
+    __shared__ float sums[kThinWaves][kRT][kTG][16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, quad = (lane & 15) >> 2, b = lane & 3, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * (4 * kRT), blocks = a.cols / kGroup;
+    const MX4_GLOBAL uint8_t *wc[kRT], *ws[kRT], *xc[kTG], *xs[kTG];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        wc[i] = (const MX4_GLOBAL uint8_t*)a.codes + (n0 + i) * 16 * blocks;   // rows come in eights
-        ws[i] = (const MX4_GLOBAL uint8_t*)a.scales + (n0 + i) * blocks;
+    for (int i = 0; i < kRT; ++i) {
+        const int64_t n = least(n0 + 4 * i + quad, a.rows - 1);
+        wc[i] = (const MX4_GLOBAL uint8_t*)a.codes + n * (a.cols / 2);
+        ws[i] = (const MX4_GLOBAL uint8_t*)a.scales + n * blocks;
     }
-    float sum[kRows] = {};
-    for (int64_t first = 0; first < blocks; first += 64 * kWidth) {
-        const bool in = first + t < blocks;
-        const int64_t blk = in ? first + t : first;
-        float x[32];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const u32x4 v = ((const MX4_GLOBAL u32x4*)a.x)[4 * blk + q];
+    for (int u = 0; u < kTG; ++u) {
+        const int64_t t = least(4 * u + quad, a.m - 1);
+        xc[u] = (const MX4_GLOBAL uint8_t*)a.x + t * (DT == 2 ? a.cols / 2 : a.cols * 2);
+        xs[u] = (const MX4_GLOBAL uint8_t*)a.xscales + t * blocks;
+    }
+    f32x4 acc[kRT][kTG] = {};
+    for (int64_t at = 16 * wave; at < blocks; at += 16 * kThinWaves) {
+        const bool in = at + 4 * g + b < blocks;
+        const int64_t blk = in ? at + 4 * g + b : 0;
+        u32x4 c[kRT];
+        uint32_t s[kRT];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x2 p = unpack2<DT>(in ? v[j] : 0u);
-                x[8 * q + 2 * j] = p.x;
-                x[8 * q + 2 * j + 1] = p.y;
-            }
-        }
-        u32x4 c[kRows];
-        uint32_t s[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
+        for (int i = 0; i < kRT; ++i) {
             c[i] = *(const MX4_GLOBAL u32x4*)(wc[i] + 16 * blk);
             s[i] = ws[i][blk];
         }
+        // blocks past the row's end: x 0 and the weight finite
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const float arg = scale_arg(in ? s[i] : 0u);   // past the end: finite, times 0
-            float even = 0, odd = 0;
+        for (int i = 0; i < kRT; ++i) s[i] = in ? s[i] : 0u;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                f32x2 p[4];
-                decode8_fp32<DT>(c[i][q], arg, p);
+        for (int u = 0; u < kTG; ++u) {
+            const bool mine = in && 4 * u + quad < a.m;
+            if constexpr (DT == 2) {
+                const u32x4 x = mine ? *(const MX4_GLOBAL u32x4*)(xc[u] + 16 * blk) : kZero;
+                const uint32_t e = mine ? xs[u][blk] : 0u;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    even = __builtin_fmaf(p[j].x, x[8 * q + 2 * j], even);
-                    odd = __builtin_fmaf(p[j].y, x[8 * q + 2 * j + 1], odd);
+                for (int i = 0; i < kRT; ++i) acc[i][u] = mfma4<0>(c[i], s[i], x, e, acc[i][u]);
+            } else {
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const u32x4 x = mine ? *(const MX4_GLOBAL u32x4*)(xc[u] + 64 * blk + 16 * f) : kZero;
+#pragma unroll
+                    for (int i = 0; i < kRT; ++i)
+                        acc[i][u] = mfma16<DT>(decode8<DT>(c[i][f], scale_arg(s[i])), x, acc[i][u]);
                 }
             }
-            sum[i] += even + odd;
         }
     }
+    // lane (r, g) of the result: row g, blocks 0 .. 3 in the four registers; column r = token quad, block b
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < kRT; ++i)
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) sum[i] += __shfl_xor(sum[i], o);
-    }
-    if constexpr (kWidth == 2) {
-        if (t == 64) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) other[i] = sum[i];
+        for (int u = 0; u < kTG; ++u) {
+            const float c0 = acc[i][u][0], c1 = acc[i][u][1], c2 = acc[i][u][2], c3 = acc[i][u][3];
+            float v = b == 0 ? c0 : b == 1 ? c1 : b == 2 ? c2 : c3;
+            v += __shfl_xor(v, 1);
+            v += __shfl_xor(v, 2);
+            if (b == 0) sums[wave][i][u][4 * quad + g] = v;
         }
-        __syncthreads();
+    __syncthreads();
+    for (int e = threadIdx.x; e < kRT * kTG * 4; e += 64 * kThinWaves) {
+        const int i = e % kRT, t = e / kRT;   // token t, rows n0 + 4 i ..
+        f32x4 v = *(const f32x4*)&sums[0][i][t / 4][4 * (t % 4)];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) sum[i] += other[i];
+        for (int w = 1; w < kThinWaves; ++w) v += *(const f32x4*)&sums[w][i][t / 4][4 * (t % 4)];
+        if (t < a.m && n0 + 4 * i < a.rows) store4(a.out, a.kind, t * a.rows + n0 + 4 * i, v);
     }
-    if (t == 0) store4(a.out, a.kind, n0, f32x4{sum[0], sum[1], sum[2], sum[3]});
 }
 
 // The low and the high halves of two dwords, put together.
@@ -406,15 +414,18 @@ FewPlan few_plan(int64_t rows, int64_t cols, int64_t m, bool codes)
     return best;
 }
 
+// k_thin's tokens: with x in 16 bits a token's values are four times those of its codes.
+bool thin(int64_t m, bool codes) { return m <= (codes ? 16 : 8); }
+
 // Against the tiled kernels' estimate.  Those take at least 256 columns with both operands in codes.
 bool mm_few(int64_t rows, int64_t cols, int64_t m, bool forward)
 {
     if (!forward) return m <= 64;
-    return m == 1 || (m <= 64 && few_plan(rows, cols, m, false).us < mm_tiled_us(cols, rows, m));
+    return thin(m, false) || (m <= 64 && few_plan(rows, cols, m, false).us < mm_tiled_us(cols, rows, m));
 }
 bool mm4_few(int64_t rows, int64_t cols, int64_t m)
 {
-    return cols < 256 || (m <= 64 && few_plan(rows, cols, m, true).us < mm4_tiled_us(rows, cols, m));
+    return cols < 256 || thin(m, true) || (m <= 64 && few_plan(rows, cols, m, true).us < mm4_tiled_us(rows, cols, m));
 }
 
 // Tiles of 16 tokens a workgroup takes backward, and how many workgroups they make.
@@ -445,16 +456,24 @@ hipError_t few_tokens(const FewArgs& a, int mt, hipStream_t s)
     return hipGetLastError();
 }
 
+template <int DT, int kRT, int kTG, int kThinWaves>
+hipError_t thin_go(const FewArgs& a, hipStream_t s)
+{
+    k_thin<DT, kRT, kTG, kThinWaves><<<(unsigned)ceil_div(a.rows, 4 * kRT), 64 * kThinWaves, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <int DT>
 hipError_t few_go(FewArgs a, hipStream_t s)
 {
-    if (DT != 2 && a.m == 1) {
-        if constexpr (DT != 2) {
-            // two waves where a row is more than four segments of one
-            if (a.cols > 8192) k_one<DT, 2><<<(unsigned)(a.rows / 4), 128, 0, s>>>(a);
-            else k_one<DT, 1><<<(unsigned)(a.rows / 4), 64, 0, s>>>(a);
-        }
-        return hipGetLastError();
+    if (thin(a.m, DT == 2)) {
+        const int64_t runs = ceil_div(a.cols, 512);
+        if (a.m <= 4) return thin_go<DT, 2, 1, 4>(a, s);
+        if constexpr (DT == 2) return a.m <= 8 ? thin_go<DT, 2, 2, 4>(a, s) : thin_go<DT, 2, 4, 4>(a, s);
+        // 16 bits, five to eight tokens: two waves where four would share the runs unevenly (8 tokens through 13824 x
+        // 5120, 10 runs: 13.6 us, with four 16.2; through 11008 x 4096, 8 runs: 11.0 and 8.9)
+        if (10 * ceil_div(runs, 4) * 4 > 11 * runs) return thin_go<DT, 4, 2, 2>(a, s);
+        return thin_go<DT, 4, 2, 4>(a, s);
     }
     const FewPlan p = few_plan(a.rows, a.cols, a.m, DT == 2);
     a.token_tiles = token_groups(a.m, p.mt);

@@ -48,26 +48,6 @@ __device__ __forceinline__ u32x4 decode8(uint32_t codes, float scale)
                  decode2<DT, 3>(codes, scale)};
 }
 
-// Eight codes to the values of type DT in fp32.  A bf16 holds every one of them (it
-// has fp32's exponents, and two bits are enough), so fp32 is reached directly; fp16
-// rounds first.
-template <int DT>
-__device__ __forceinline__ void decode8_fp32(uint32_t codes, float scale, f32x2 (&p)[4])
-{
-    if constexpr (DT == 0) {
-        p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 0);
-        p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 1);
-        p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 2);
-        p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 3);
-    } else {
-        const u32x4 w = decode8<DT>(codes, scale);
-        p[0] = unpack2<DT>(w[0]);
-        p[1] = unpack2<DT>(w[1]);
-        p[2] = unpack2<DT>(w[2]);
-        p[3] = unpack2<DT>(w[3]);
-    }
-}
-
 // Two 16-bit values over 2^(s - 127) to their nearest codes, into byte B of `codes`.
 template <int DT, int B>
 __device__ __forceinline__ uint32_t encode2(uint32_t codes, uint32_t x, float scale)
