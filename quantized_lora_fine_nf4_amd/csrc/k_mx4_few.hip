@@ -420,7 +420,9 @@ bool thin(int64_t m, bool codes) { return m <= (codes ? 16 : 8); }
 // Against the tiled kernels' estimate.  Those take at least 256 columns with both operands in codes.
 bool mm_few(int64_t rows, int64_t cols, int64_t m, bool forward)
 {
-    if (!forward) return m <= 64;
+    // backward against the tiled kernels: 16 tokens through 13824 x 5120 20.8 us (23.9), 32 30.4 (25.3); 32 through
+    // 4096 x 4096 13.2 (16.2), 48 17.0 (15.3)
+    if (!forward) return m <= (rows * cols <= int64_t(1) << 25 ? 32 : 16);
     return thin(m, false) || (m <= 64 && few_plan(rows, cols, m, false).us < mm_tiled_us(cols, rows, m));
 }
 bool mm4_few(int64_t rows, int64_t cols, int64_t m)
@@ -429,7 +431,7 @@ bool mm4_few(int64_t rows, int64_t cols, int64_t m)
 }
 
 // Tiles of 16 tokens a workgroup takes backward, and how many workgroups they make.
-int token_tiles(int64_t m) { return m <= 16 ? 1 : m <= 32 ? 2 : 4; }
+int token_tiles(int64_t m) { return m <= 16 ? 1 : 2; }
 uint32_t token_groups(int64_t m, int tiles) { return (uint32_t)ceil_div(m, 16 * tiles); }
 
 // Backward: columns of a wave.
@@ -487,8 +489,7 @@ hipError_t few_back_go(const FewArgs& a, hipStream_t s)
     const int mt = token_tiles(a.m);
     const dim3 grid((unsigned)ceil_div(a.cols, back_columns(a.m)) * a.token_tiles, (unsigned)a.parts);
     if (mt == 1) k_few_back<DT, 1, 2><<<grid, 64 * kWaves, 0, s>>>(a);
-    else if (mt == 2) k_few_back<DT, 2, 1><<<grid, 64 * kWaves, 0, s>>>(a);
-    else k_few_back<DT, 4, 1><<<grid, 64 * kWaves, 0, s>>>(a);
+    else k_few_back<DT, 2, 1><<<grid, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
 }
 
