@@ -531,8 +531,16 @@ hipError_t launch_matmul4(const uint8_t* codes, const uint8_t* scales, int64_t r
 {
     if (!mm4_few(rows, cols, m))
         return launch_mm4_tiled(codes, scales, rows, cols, xcodes, xscales, m, out, out_kind, part, s);
-    const FewArgs a{codes, scales, xcodes, xscales, out, nullptr, m, rows, cols, out_kind, 1, 1};
-    return few_go<2>(a, s);
+    // narrow weights come here with any number of tokens: what keeps a launch under 2^32 threads at once
+    const int64_t most = (int64_t(1) << 34) / rows;
+    for (int64_t t = 0; t < m; t += most) {
+        const FewArgs a{codes, scales, xcodes + t * (cols / 2), xscales + t * (cols / kGroup),
+                        (char*)out + t * rows * (out_kind == kOutFp32 ? 4 : 2), nullptr, m - t < most ? m - t : most,
+                        rows, cols, out_kind, 1, 1};
+        const hipError_t e = few_go<2>(a, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace mx4k

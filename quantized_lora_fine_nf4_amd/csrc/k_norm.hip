@@ -179,43 +179,44 @@ __global__ __launch_bounds__(1024) void k_norm_long(NormArgs a)
 {
     __shared__ float buf[2][16];
     const int n8 = a.n >> 3;
-    const int64_t row = blockIdx.x;
     const float inv = 1.0f / (float)a.n;
     // with a residual the sum is written first and read back by the same thread
     const uint16_t* h = RES ? a.total : a.x;
-    float sum = 0;
-    for (int p = threadIdx.x; p < n8; p += 1024) {
-        u32x4 v = load16(a.x, row * a.n + 8 * (int64_t)p);
-        if constexpr (RES) {
-            v = add8<DT>(v, load16(a.residual, row * a.n + 8 * (int64_t)p));
-            *((GLOBAL u32x4*)(a.total + row * a.n + 8 * (int64_t)p)) = v;
+    for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
+        float sum = 0;
+        for (int p = threadIdx.x; p < n8; p += 1024) {
+            u32x4 v = load16(a.x, row * a.n + 8 * (int64_t)p);
+            if constexpr (RES) {
+                v = add8<DT>(v, load16(a.residual, row * a.n + 8 * (int64_t)p));
+                *((GLOBAL u32x4*)(a.total + row * a.n + 8 * (int64_t)p)) = v;
+            }
+            float f[8];
+            unpack8<DT>(v, f);
+            sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
         }
-        float f[8];
-        unpack8<DT>(v, f);
-        sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-    }
-    const float mean = row_sum<1024>(sum, buf[0]) * inv;
-    float sq = 0;
-    for (int p = threadIdx.x; p < n8; p += 1024) {
-        float f[8];
-        unpack8<DT>(load16(h, row * a.n + 8 * (int64_t)p), f);
+        const float mean = row_sum<1024>(sum, buf[0]) * inv;
+        float sq = 0;
+        for (int p = threadIdx.x; p < n8; p += 1024) {
+            float f[8];
+            unpack8<DT>(load16(h, row * a.n + 8 * (int64_t)p), f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            f[j] -= mean;
-            sq = __builtin_fmaf(f[j], f[j], sq);
+            for (int j = 0; j < 8; ++j) {
+                f[j] -= mean;
+                sq = __builtin_fmaf(f[j], f[j], sq);
+            }
         }
-    }
-    const float rstd = 1.0f / __builtin_sqrtf(row_sum<1024>(sq, buf[1]) * inv + a.eps);
-    for (int p = threadIdx.x; p < n8; p += 1024) {
-        float f[8], g[8], c[8];
-        unpack8<DT>(load16(h, row * a.n + 8 * (int64_t)p), f);
-        unpack8<DT>(load16(a.weight, 8 * (int64_t)p), g);
-        unpack8<DT>(load16(a.bias, 8 * (int64_t)p), c);
+        const float rstd = 1.0f / __builtin_sqrtf(row_sum<1024>(sq, buf[1]) * inv + a.eps);
+        for (int p = threadIdx.x; p < n8; p += 1024) {
+            float f[8], g[8], c[8];
+            unpack8<DT>(load16(h, row * a.n + 8 * (int64_t)p), f);
+            unpack8<DT>(load16(a.weight, 8 * (int64_t)p), g);
+            unpack8<DT>(load16(a.bias, 8 * (int64_t)p), c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf((f[j] - mean) * rstd, g[j], c[j]);
-        *((GLOBAL u32x4*)(a.out + row * a.n + 8 * (int64_t)p)) = pack8<DT>(f);
+            for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf((f[j] - mean) * rstd, g[j], c[j]);
+            *((GLOBAL u32x4*)(a.out + row * a.n + 8 * (int64_t)p)) = pack8<DT>(f);
+        }
+        if (threadIdx.x == 0) *((GLOBAL f32x2*)(a.stats + 2 * row)) = f32x2{mean, rstd};
     }
-    if (threadIdx.x == 0) *((GLOBAL f32x2*)(a.stats + 2 * row)) = f32x2{mean, rstd};
 }
 
 // ---- gradient
@@ -352,35 +353,38 @@ __global__ __launch_bounds__(1024) void k_norm_grad_long(NormGradArgs a)
 {
     __shared__ float buf[2][16];
     const int n8 = a.n >> 3;
-    const int64_t at = (int64_t)blockIdx.x * a.n;
-    const f32x2 st = *((const GLOBAL f32x2*)(a.stats + 2 * (int64_t)blockIdx.x));
-    const float mean = st.x, rstd = st.y, inv = 1.0f / (float)a.n;
-    float s0 = 0, s1 = 0;
-    for (int p = threadIdx.x; p < n8; p += 1024) {
-        float f[8], e[8], g[8];
-        unpack8<DT>(load16(a.x, at + 8 * (int64_t)p), f);
-        unpack8<DT>(load16(a.dy, at + 8 * (int64_t)p), e);
-        unpack8<DT>(load16(a.weight, 8 * (int64_t)p), g);
+    const float inv = 1.0f / (float)a.n;
+    for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
+        const int64_t at = row * a.n;
+        const f32x2 st = *((const GLOBAL f32x2*)(a.stats + 2 * row));
+        const float mean = st.x, rstd = st.y;
+        float s0 = 0, s1 = 0;
+        for (int p = threadIdx.x; p < n8; p += 1024) {
+            float f[8], e[8], g[8];
+            unpack8<DT>(load16(a.x, at + 8 * (int64_t)p), f);
+            unpack8<DT>(load16(a.dy, at + 8 * (int64_t)p), e);
+            unpack8<DT>(load16(a.weight, 8 * (int64_t)p), g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float t = e[j] * g[j];
-            s0 += t;
-            s1 = __builtin_fmaf(t, (f[j] - mean) * rstd, s1);
+            for (int j = 0; j < 8; ++j) {
+                const float t = e[j] * g[j];
+                s0 += t;
+                s1 = __builtin_fmaf(t, (f[j] - mean) * rstd, s1);
+            }
         }
-    }
-    const float m0 = row_sum<1024>(s0, buf[0]) * inv, m1 = row_sum<1024>(s1, buf[1]) * inv;
-    for (int p = threadIdx.x; p < n8; p += 1024) {
-        float f[8], e[8], g[8], q[8];
-        unpack8<DT>(load16(a.x, at + 8 * (int64_t)p), f);
-        unpack8<DT>(load16(a.dy, at + 8 * (int64_t)p), e);
-        unpack8<DT>(load16(a.weight, 8 * (int64_t)p), g);
-        if constexpr (RES) unpack8<DT>(load16(a.residual, at + 8 * (int64_t)p), q);
+        const float m0 = row_sum<1024>(s0, buf[0]) * inv, m1 = row_sum<1024>(s1, buf[1]) * inv;
+        for (int p = threadIdx.x; p < n8; p += 1024) {
+            float f[8], e[8], g[8], q[8];
+            unpack8<DT>(load16(a.x, at + 8 * (int64_t)p), f);
+            unpack8<DT>(load16(a.dy, at + 8 * (int64_t)p), e);
+            unpack8<DT>(load16(a.weight, 8 * (int64_t)p), g);
+            if constexpr (RES) unpack8<DT>(load16(a.residual, at + 8 * (int64_t)p), q);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            f[j] = (e[j] * g[j] - m0 - (f[j] - mean) * rstd * m1) * rstd;
-            if constexpr (RES) f[j] += q[j];
+            for (int j = 0; j < 8; ++j) {
+                f[j] = (e[j] * g[j] - m0 - (f[j] - mean) * rstd * m1) * rstd;
+                if constexpr (RES) f[j] += q[j];
+            }
+            *((GLOBAL u32x4*)(a.dx + at + 8 * (int64_t)p)) = pack8<DT>(f);
         }
-        *((GLOBAL u32x4*)(a.dx + at + 8 * (int64_t)p)) = pack8<DT>(f);
     }
 }
 
@@ -434,6 +438,9 @@ __global__ __launch_bounds__(512) void k_norm_sum(const float* part, int blocks,
 // Rows up to this many values stay in registers (forward, gradient).
 constexpr int kMaxNorm = 24576, kMaxGrad = 16384;
 
+// Workgroups of the kernels for longer ones: a row each, up to a grid's limit.
+unsigned long_blocks(int64_t m) { return (unsigned)(m < 65536 ? m : 65536); }
+
 template <int DT, bool RES, int kLanes, int kPieces>
 hipError_t norm_go(const NormArgs& a, hipStream_t s)
 {
@@ -459,7 +466,7 @@ hipError_t norm_any(const NormArgs& a, hipStream_t s)
     if (a.n <= 2048) return norm_pieces<DT, RES, 64>(a, s);
     if (a.n <= 8192) return norm_pieces<DT, RES, 256>(a, s);
     if (a.n <= kMaxNorm) return norm_pieces<DT, RES, 1024>(a, s);
-    k_norm_long<DT, RES><<<(unsigned)a.m, 1024, 0, s>>>(a);
+    k_norm_long<DT, RES><<<long_blocks(a.m), 1024, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -491,7 +498,7 @@ hipError_t grad_any(const NormGradArgs& a, hipStream_t s)
     if (a.n > kMaxGrad) {
         k_norm_columns<DT><<<dim3((unsigned)((a.n / 8 + 255) / 256), (unsigned)blocks), 256, 0, s>>>(a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        k_norm_grad_long<DT, RES><<<(unsigned)a.m, 1024, 0, s>>>(a);
+        k_norm_grad_long<DT, RES><<<long_blocks(a.m), 1024, 0, s>>>(a);
         e = hipGetLastError();
     } else if (a.n <= 2048) {
         e = grad_pieces<DT, RES, 64>(a, blocks, s);

@@ -33,7 +33,8 @@ struct TileCosts {
 };
 
 // The small tiles of m x ncol outputs: into how many parts their reduction goes and
-// what that costs, the partials at 5 TB/s and their sum's launch included.
+// what that costs, with 6 us for the sum's launch and the partials written and read
+// at 2.5 TB/s.
 inline TileGrid small_plan(int64_t m, int64_t ncol, int steps, const TileCosts& c, double* cost)
 {
     TileGrid best = {(int)ceil_div(m, 128), (int)ceil_div(ncol, 128), 1, steps};

@@ -343,3 +343,33 @@ def test_captured_and_on_another_stream():
         step(s, *ins[3][:4], codes, scales, ins[3][4])
     side.synchronize()
     assert all(torch.equal(s[name], w) for name, w in zip(names, want[3]))
+
+
+def test_long_rows_more_than_a_grid():
+    """More rows past the registers than workgroups: the same bits as those rows alone."""
+    m, n = 65536 + 5, 24584
+    print_case("nf4_layer_norm, nf4_layer_norm_grad", m, n)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(m, n, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    dy = torch.empty_like(x).normal_(generator=g)
+    weight, bias = (torch.randn(n, generator=g, device="cuda").to(x.dtype) for _ in range(2))
+    out, stats = torch.empty_like(x), torch.empty(m, 2, device="cuda")
+    q.nf4_layer_norm(x, weight, bias, out, stats)
+    dw, db = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    dx = torch.empty_like(x)
+    space = torch.empty(q.nf4_layer_norm_grad_workspace_bytes(m, n), dtype=torch.uint8, device="cuda")
+    q.nf4_layer_norm_grad(dy, x, weight, stats, dx, dw, db, space)
+    k = 7
+    out2, stats2, dx2 = torch.empty(k, n, dtype=x.dtype, device="cuda"), torch.empty(k, 2, device="cuda"), torch.empty(k, n, dtype=x.dtype, device="cuda")
+    q.nf4_layer_norm(x[-k:].contiguous(), weight, bias, out2, stats2)
+    space = torch.empty(q.nf4_layer_norm_grad_workspace_bytes(k, n), dtype=torch.uint8, device="cuda")
+    q.nf4_layer_norm_grad(dy[-k:].contiguous(), x[-k:].contiguous(), weight, stats2, dx2, torch.empty_like(dw), torch.empty_like(db),
+                          space if space.numel() else None)
+    assert torch.equal(out[-k:], out2) and torch.equal(stats[-k:], stats2) and torch.equal(dx[-k:], dx2)
+    # a sum of m terms in any order: within m u of the magnitudes' sum
+    want = torch.zeros(n, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    for i in range(0, m, 8192):
+        want += dy[i:i + 8192].double().sum(0)
+        size += dy[i:i + 8192].double().abs().sum(0)
+    assert ((db.double() - want).abs() <= m * U32 * size).all()
