@@ -25,25 +25,36 @@ struct TilePlan {
 
 constexpr int kCus = 256;
 
-// Measured on this card, in us: a step of the reduction and what a tile costs
-// besides (its start and its stores), for a round of big tiles (one on each compute
-// unit) and of small ones (two on each, the same with one).
+// Measured on this card, in us: a step of the reduction, and what a tile costs
+// besides (its start and its stores), for large tiles (one on each compute unit), for
+// small ones with one on each compute unit and for small ones with two.
 struct TileCosts {
-    double big_step, big_tile, small_step, small_tile;
+    double big_step, big_tile, one_step, one_tile, two_step, two_tile;
 };
 
+// So many small tiles of so many steps: rounds of two on each compute unit and a rest.
+// Between one and two on each it grows with their number, a quarter of the way at once.
+inline double small_us(int64_t tiles, int steps, const TileCosts& c)
+{
+    const double one = steps * c.one_step + c.one_tile, two = steps * c.two_step + c.two_tile;
+    const int64_t rounds = tiles / (2 * kCus), rest = tiles % (2 * kCus);
+    if (rest == 0) return rounds * two;
+    if (rest <= kCus) return rounds * two + one;
+    const double over = double(rest - kCus) / kCus;
+    return rounds * two + one + (two - one) * (over > 0.25 ? over : 0.25);
+}
+
 // The small tiles of m x ncol outputs: into how many parts their reduction goes and
-// what that costs, with 6 us for the sum's launch and the partials written and read
-// at 2.5 TB/s.
+// what that costs, with 2.3 us for the sum's launch and the partials' 8 bytes (written
+// and read) at 6.5 TB/s.
 inline TileGrid small_plan(int64_t m, int64_t ncol, int steps, const TileCosts& c, double* cost)
 {
     TileGrid best = {(int)ceil_div(m, 128), (int)ceil_div(ncol, 128), 1, steps};
     const int64_t tiles = (int64_t)best.mt * best.nt;
-    *cost = ceil_div(tiles, 2 * kCus) * (steps * c.small_step + c.small_tile);
+    *cost = small_us(tiles, steps, c);
     for (int p = 2; p <= 16 && p <= steps; ++p) {
         const int per = (int)ceil_div(steps, p), parts = (int)ceil_div(steps, per);
-        const double us = ceil_div(tiles * parts, 2 * kCus) * (per * c.small_step + c.small_tile) + 6.0 +
-                          double(parts) * double(m) * double(ncol) * 8e-6 / 2.5;
+        const double us = small_us(tiles * parts, per, c) + 2.3 + double(parts) * double(m) * double(ncol) * 8e-6 / 6.5;
         if (us < *cost) {
             *cost = us;
             best.parts = parts;
