@@ -202,6 +202,30 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_plain = None
+
+
+class _NoCalls:
+    """In the place of the _calls module where it cannot be used: every call is Python's to make."""
+    layer_norm = layer_norm_grad = quantize = dequantize = matmul = matmul4 = staticmethod(lambda *a: None)
+
+
+def _load_calls():
+    """The module that makes plain calls without Python's checks (csrc/py_calls.cpp), once."""
+    global _plain
+    import torch
+    L = lib()
+    try:
+        from . import _calls as native
+        at = [ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "nf4_layer_norm", "nf4_layer_norm_grad", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_matmul4")]
+        native.setup(*at, torch._C._cuda_getCurrentRawStream)
+    except (ImportError, AttributeError):
+        native = _NoCalls
+    _plain = native
+    return native
+
+
 def fmt(dtype: int = NF4_BF16, dq: bool = True) -> nf4_format:
     return nf4_format(int(dtype), BLOCK, DQ_GROUP if dq else 0)
 
@@ -564,12 +588,19 @@ def nf4_lora_grad_workspace_bytes(m: int, n: int, rank: int) -> int:
 
 
 # ---- the layer norm -------------------------------------------------------
+#
+# A plain call of these and of the microscaled ones (contiguous tensors of the right
+# shapes and types on the current device, its current stream) is made by _calls;
+# what that leaves alone is checked and made, or refused, here.
 
 def nf4_layer_norm(x, weight, bias, out, stats, eps: float = 1e-5, residual=None, total=None, stream=None) -> None:
     """out = (h - mean) rstd weight + bias over the last axis, h = x, or total = x +
     residual rounded to their type (residual and total: both or neither).  x,
     residual, out, total [m, n], weight and bias [n], bfloat16 or float16; stats
     float32 [m, 2], written with each token's mean and rstd."""
+    st = (_plain or _load_calls()).layer_norm(x, weight, bias, out, stats, eps, residual, total, stream)
+    if st is not None:
+        return _check(st, "nf4_layer_norm")
     import torch
     w = "nf4_layer_norm"
     dt, dev, t16 = _dtype16(x, w), x.get_device(), x.dtype
@@ -592,6 +623,9 @@ def nf4_layer_norm_grad(dy, x, weight, stats, dx, dweight, dbias, ws=None, resid
     normalised (total, with a residual), stats: nf4_layer_norm's; dx may be dy, x or
     residual.  ws: device tensor of nf4_layer_norm_grad_workspace_bytes(m, n) bytes,
     or None when that is 0."""
+    st = (_plain or _load_calls()).layer_norm_grad(dy, x, weight, stats, dx, dweight, dbias, ws, residual, stream)
+    if st is not None:
+        return _check(st, "nf4_layer_norm_grad")
     import torch
     w = "nf4_layer_norm_grad"
     dt, dev, t16 = _dtype16(dy, w), dy.get_device(), dy.dtype
@@ -638,6 +672,9 @@ def mx4_quantize(x, codes, scales, err=None, ws=None, stream=None) -> None:
     (float64 [1]), the sum of squared differences to their values: a score for
     aqlora_select.  ws: device tensor of mx4_quantize_workspace_bytes(rows, cols)
     bytes with err, or None when that is 0."""
+    st = (_plain or _load_calls()).quantize(x, codes, scales, err, ws, stream)
+    if st is not None:
+        return _check(st, "mx4_quantize")
     import torch
     w = "mx4_quantize"
     dt, dev = _dtype16(x, w), x.get_device()
@@ -650,6 +687,9 @@ def mx4_quantize(x, codes, scales, err=None, ws=None, stream=None) -> None:
 
 def mx4_dequantize(codes, scales, out, stream=None) -> None:
     """out [rows, cols] (bfloat16 or float16) = the values of codes and scales."""
+    st = (_plain or _load_calls()).dequantize(codes, scales, out, stream)
+    if st is not None:
+        return _check(st, "mx4_dequantize")
     w = "mx4_dequantize"
     dt, dev = _dtype16(out, w), out.get_device()
     cp, sp, rows, cols = _mx4_pair(codes, scales, _MX4_W, w, dev)
@@ -667,6 +707,9 @@ def mx4_matmul(codes, scales, x, out, ws=None, backward: bool = False, stream=No
     rows]), W [rows, cols] by its codes and scales.  x bfloat16 or float16, out that
     type or float32.  ws: device tensor of mx4_matmul_workspace_bytes(rows, cols,
     backward, m) bytes, or None when that is 0."""
+    st = (_plain or _load_calls()).matmul(codes, scales, x, out, ws, backward, stream)
+    if st is not None:
+        return _check(st, "mx4_matmul")
     w = "mx4_matmul"
     dt, dev, t16 = _dtype16(x, w), x.get_device(), x.dtype
     cp, sp, rows, cols = _mx4_pair(codes, scales, _MX4_W, w, dev)
@@ -683,6 +726,9 @@ def mx4_matmul4(codes, scales, xcodes, xscales, out, ws=None, stream=None) -> No
     """out [m, rows] = x W^T with W [rows, cols] and x [m, cols] both by codes and
     scales; out bfloat16, float16 or float32.  ws: device tensor of
     mx4_matmul4_workspace_bytes(rows, cols, m) bytes, or None when that is 0."""
+    st = (_plain or _load_calls()).matmul4(codes, scales, xcodes, xscales, out, ws, stream)
+    if st is not None:
+        return _check(st, "mx4_matmul4")
     import torch
     w = "mx4_matmul4"
     dev = codes.get_device()

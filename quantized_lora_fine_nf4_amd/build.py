@@ -18,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_PATH = os.path.join(PKG, "libnf4.so")
 CPU_LIB_PATH = os.path.join(PKG, "libnf4cpu.so")
+CALLS_PATH = os.path.join(PKG, "_calls.so")
 CPU_SOURCES = [os.path.join("cpu", "nf4_cpu.cpp")]
 SOURCES = ["k_gemm.hip", "k_linear_back.hip", "k_linear.hip", "k_codec.hip", "k_lora.hip", "k_variants.hip",
            "k_norm.hip", "k_mx4_mm.hip", "k_mx4_mm4.hip", "k_mx4_few.hip", "k_mx4.hip", "k_select.hip",
@@ -59,6 +60,31 @@ def build_cpu(verbose: bool = False) -> str:
     return CPU_LIB_PATH
 
 
+def calls_command(out: str = CALLS_PATH) -> list:
+    """The Python calls' plain case (a CPython module against torch's C++ tensors)."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-Wno-attributes",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(t, "include"),
+            "-isystem", sysconfig.get_paths()["include"], "-o", out, os.path.join(CSRC, "py_calls.cpp"),
+            "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{os.path.join(t, 'lib')}"]
+
+
+def build_calls(verbose: bool = False) -> str:
+    tmp = CALLS_PATH + ".tmp"
+    cmd = calls_command(tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed ({r.returncode}):\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
+    return CALLS_PATH
+
+
 def _hipcc(cmd: list, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -87,3 +113,4 @@ def build(verbose: bool = False) -> str:
 if __name__ == "__main__":
     print(build(verbose=True))
     print(build_cpu(verbose=True))
+    print(build_calls(verbose=True))

@@ -373,3 +373,108 @@ def test_long_rows_more_than_a_grid():
         want += dy[i:i + 8192].double().sum(0)
         size += dy[i:i + 8192].double().abs().sum(0)
     assert ((db.double() - want).abs() <= m * U32 * size).all()
+
+
+# ---- plain calls, and those that are not ------------------------------------
+
+def all_calls(dtype, m=5, n=256, rows=64, seed=0):
+    """Each call with good arguments, by name: (function, arguments by name, what it writes)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def r(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+    def e(*shape, t=dtype):
+        return torch.zeros(*shape, dtype=t, device="cuda")
+
+    def u8(nbytes):
+        return e(nbytes, t=torch.uint8) if nbytes else None
+    w = r(rows, n)
+    c, s = e(rows, n // 2, t=torch.uint8), e(rows, n // 32, t=torch.uint8)
+    q.mx4_quantize(w, c, s)
+    x, dy = r(m, n), r(m, rows)
+    xc, xs = e(m, n // 2, t=torch.uint8), e(m, n // 32, t=torch.uint8)
+    q.mx4_quantize(x, xc, xs)
+    stats = e(m, 2, t=torch.float32)
+    q.nf4_layer_norm(x, r(n), r(n), e(m, n), stats)
+    f32 = torch.float32
+    return {
+        "norm": (q.nf4_layer_norm, dict(x=x, weight=r(n), bias=r(n), out=e(m, n), stats=e(m, 2, t=f32), residual=r(m, n),
+                                        total=e(m, n)), ("out", "stats", "total")),
+        "norm grad": (q.nf4_layer_norm_grad, dict(dy=r(m, n), x=x, weight=r(n), stats=stats, dx=e(m, n), dweight=e(n, t=f32),
+                                                  dbias=e(n, t=f32), residual=r(m, n),
+                                                  ws=u8(q.nf4_layer_norm_grad_workspace_bytes(m, n))), ("dx", "dweight", "dbias")),
+        "quantize": (q.mx4_quantize, dict(x=w, codes=e(*c.shape, t=torch.uint8), scales=e(*s.shape, t=torch.uint8),
+                                          err=e(1, t=torch.float64), ws=u8(q.mx4_quantize_workspace_bytes(rows, n))),
+                     ("codes", "scales", "err")),
+        "dequantize": (q.mx4_dequantize, dict(codes=c, scales=s, out=e(rows, n)), ("out",)),
+        "matmul": (q.mx4_matmul, dict(codes=c, scales=s, x=x, out=e(m, rows), ws=u8(q.mx4_matmul_workspace_bytes(rows, n, False, m))),
+                   ("out",)),
+        "matmul back": (q.mx4_matmul, dict(codes=c, scales=s, x=dy, out=e(m, n, t=f32), backward=True,
+                                           ws=u8(q.mx4_matmul_workspace_bytes(rows, n, True, m))), ("out",)),
+        "matmul4": (q.mx4_matmul4, dict(codes=c, scales=s, xcodes=xc, xscales=xs, out=e(m, rows),
+                                        ws=u8(q.mx4_matmul4_workspace_bytes(rows, n, m))), ("out",)),
+    }
+
+
+CALLS = ("norm", "norm grad", "quantize", "dequantize", "matmul", "matmul back", "matmul4")
+
+
+def test_plain_calls_are_made_by_the_compiled_module(monkeypatch):
+    """With it and with Python's own checks the same bits, on the current stream and on a given one."""
+    native = q._load_calls()
+    assert native is not q._NoCalls, "the compiled module is missing"
+    for dtype in DT:
+        for name in CALLS:
+            print_case("plain call", name, dtype)
+            got = []
+            for plain, stream in ((native, None), (q._NoCalls, None), (native, torch.cuda.Stream())):
+                monkeypatch.setattr(q, "_plain", plain)
+                fn, kw, outs = all_calls(dtype)[name]
+                torch.cuda.synchronize()
+                fn(**kw, stream=stream)
+                torch.cuda.synchronize()
+                got.append([kw[k].clone() for k in outs])
+            for other in got[1:]:
+                assert all(torch.equal(a, b) for a, b in zip(got[0], other)), name
+            # what it takes as plain it makes: a status and not None
+            monkeypatch.setattr(q, "_plain", native)
+            if name == "dequantize":
+                fn, kw, _ = all_calls(dtype)[name]
+                assert native.dequantize(kw["codes"], kw["scales"], kw["out"], None) == q.NF4_OK
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_what_does_not_fit_is_refused(name):
+    """Each tensor in turn: another shape, another type, on the CPU, every other element, an address off by one element.
+    Nothing is written."""
+    for key in all_calls(torch.bfloat16)[name][1]:
+        for what in ("shape", "type", "cpu", "strides", "address"):
+            fn, kw, outs = all_calls(torch.bfloat16)[name]
+            t = kw[key]
+            if not isinstance(t, torch.Tensor):
+                continue
+            if key == "ws" and what in ("shape", "type") or t.numel() < 2 and what == "strides":
+                continue
+            print_case("refused", name, key, what)
+            if what == "shape":
+                kw[key] = torch.cat([t, t])
+            elif what == "type":
+                kw[key] = t.to(torch.float64 if t.dtype != torch.float64 else torch.float32)
+            elif what == "cpu":
+                kw[key] = t.cpu()
+            elif what == "strides":
+                kw[key] = torch.cat([t.reshape(-1), t.reshape(-1)])[::2].view(t.shape) if t.dim() == 1 else t.t().contiguous().t()
+            else:
+                if key in ("scales", "xscales", "err", "stats"):
+                    continue   # one element on is aligned as it has to be
+                kw[key] = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+            if what == "strides" and kw[key].is_contiguous():
+                continue
+            for k in outs:
+                kw[k].fill_(7)
+            before = [kw[k].clone() for k in outs]
+            with pytest.raises(q.NF4Error):
+                fn(**kw)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, kw[k]) for a, k in zip(before, outs))
