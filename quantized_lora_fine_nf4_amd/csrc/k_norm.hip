@@ -222,14 +222,14 @@ __global__ __launch_bounds__(1024) void k_norm_long(NormArgs a)
 // ---- gradient
 
 // kThreads / kLanes rows at a time; each thread sums its columns of dweight and
-// dbias over the rows that it takes, the row groups of the workgroup add theirs
-// up through LDS in group order, and the workgroup writes one partial.
+// dbias over the rows that it takes, the row groups' sums meet in LDS and are added
+// in group order, and the workgroup writes one partial.
 template <int DT, bool RES, int kLanes, int kPieces>
 __global__ __launch_bounds__(512) void k_norm_grad(NormGradArgs a)
 {
     constexpr int kThreads = 512, kRows = kThreads / kLanes;
     __shared__ float buf[4][kThreads / 64];
-    __shared__ float acc[kRows > 1 ? 16 * kLanes * kPieces : 1];
+    __shared__ f32x4 acc[kRows > 1 ? kRows : 1][2][kRows > 1 ? 2 * kLanes * kPieces : 1];
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes, n8 = a.n >> 3;
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t row = (int64_t)blockIdx.x * kRows + group;
@@ -311,39 +311,40 @@ __global__ __launch_bounds__(512) void k_norm_grad(NormGradArgs a)
     const bool direct = gridDim.x == 1;
     float* to_w = direct ? a.dweight : a.part + (int64_t)blockIdx.x * 2 * a.n;
     float* to_b = direct ? a.dbias : to_w + a.n;
-    for (int k = 0; k < kRows; ++k) {
-        if (group == k) {
+    if constexpr (kRows == 1) {
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int p = lane + i * kLanes;
-                if (p < n8) {
-                    if constexpr (kRows > 1) {
-                        float* s = acc + 4 * lane + 16 * kLanes * i;   // four floats a lane: no bank conflicts
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = lane + i * kLanes;
+            if (p < n8) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float* sw = s + (j >> 2) * (4 * kLanes) + (j & 3);
-                            float* sb = sw + 8 * kLanes;
-                            if (k > 0) {
-                                dw[i][j] += *sw;
-                                db[i][j] += *sb;
-                            }
-                            *sw = dw[i][j];
-                            *sb = db[i][j];
-                        }
-                    }
-                    if (k == kRows - 1) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            *((GLOBAL f32x4*)(to_w + 8 * p + 4 * h)) =
-                                f32x4{dw[i][4 * h], dw[i][4 * h + 1], dw[i][4 * h + 2], dw[i][4 * h + 3]};
-                            *((GLOBAL f32x4*)(to_b + 8 * p + 4 * h)) =
-                                f32x4{db[i][4 * h], db[i][4 * h + 1], db[i][4 * h + 2], db[i][4 * h + 3]};
-                        }
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    *((GLOBAL f32x4*)(to_w + 8 * p + 4 * h)) =
+                        f32x4{dw[i][4 * h], dw[i][4 * h + 1], dw[i][4 * h + 2], dw[i][4 * h + 3]};
+                    *((GLOBAL f32x4*)(to_b + 8 * p + 4 * h)) =
+                        f32x4{db[i][4 * h], db[i][4 * h + 1], db[i][4 * h + 2], db[i][4 * h + 3]};
                 }
             }
         }
-        if constexpr (kRows > 1) __syncthreads();
+    } else {
+        // quads of a group's 2 x 8 kLanes kPieces sums, a lane's four kLanes apart: no bank conflicts
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                acc[group][0][(2 * i + h) * kLanes + lane] =
+                    f32x4{dw[i][4 * h], dw[i][4 * h + 1], dw[i][4 * h + 2], dw[i][4 * h + 3]};
+                acc[group][1][(2 * i + h) * kLanes + lane] =
+                    f32x4{db[i][4 * h], db[i][4 * h + 1], db[i][4 * h + 2], db[i][4 * h + 3]};
+            }
+        __syncthreads();
+        for (int e = threadIdx.x; e < 4 * kLanes * kPieces; e += kThreads) {
+            const int which = e / (2 * kLanes * kPieces), at = e % (2 * kLanes * kPieces), l = at % kLanes;
+            const int p = l + at / (2 * kLanes) * kLanes, h = at / kLanes % 2;
+            f32x4 t = acc[0][which][at];
+#pragma unroll
+            for (int k = 1; k < kRows; ++k) t += acc[k][which][at];
+            if (p < n8) *((GLOBAL f32x4*)((which ? to_b : to_w) + 8 * p + 4 * h)) = t;
+        }
     }
 }
 
@@ -521,7 +522,11 @@ int norm_grad_blocks(int64_t m, int64_t n)
         return (int)(b < 64 ? b : 64);
     }
     const int lanes = grad_lanes(n), rows = 512 / lanes;
-    const int64_t b = (m + rows - 1) / rows;
+    const int64_t b = (m + rows - 1) / rows, pieces = (n / 8 + lanes - 1) / lanes;
+    // one workgroup's rounds take about half a us for each piece of a thread's; more than one need the sums' launch (16
+    // rows of 2048 in two rounds 6.7 us, 24 in three 8.7; with a workgroup for every eight 7.8; 32 rows of 512 in four
+    // rounds 4.9, 64 in eight 7.3; with a workgroup for every eight 6.0)
+    if (b <= 5 && b * pieces <= 8) return 1;
     return (int)(b < 256 ? b : 256);
 }
 
