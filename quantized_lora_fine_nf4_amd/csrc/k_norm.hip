@@ -471,8 +471,9 @@ hipError_t norm_any(const NormArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Threads of a row and rows a workgroup takes at a time, by the row's length.
-int grad_lanes(int64_t n) { return n <= 2048 ? 64 : n <= 8192 ? 256 : 512; }
+// Threads of a row, by its length: one wave up to three pieces a thread (8192 x 1536 19.8 us, with 256 threads 22.9; 2000 x
+// 2048 13.3 and 12.2).
+int grad_lanes(int64_t n) { return n <= 1536 ? 64 : n <= 8192 ? 256 : 512; }
 
 template <int DT, bool RES, int kLanes, int kPieces>
 hipError_t grad_go(const NormGradArgs& a, int blocks, hipStream_t s)
@@ -487,8 +488,8 @@ hipError_t grad_pieces(const NormGradArgs& a, int blocks, hipStream_t s)
     const int pieces = (a.n / 8 + kLanes - 1) / kLanes;
     if (pieces == 1) return grad_go<DT, RES, kLanes, 1>(a, blocks, s);
     if (pieces == 2) return grad_go<DT, RES, kLanes, 2>(a, blocks, s);
-    if (pieces == 3) return grad_go<DT, RES, kLanes, 3>(a, blocks, s);
-    return grad_go<DT, RES, kLanes, 4>(a, blocks, s);
+    if constexpr (kLanes == 64) return grad_go<DT, RES, kLanes, 3>(a, blocks, s);
+    else return pieces == 3 ? grad_go<DT, RES, kLanes, 3>(a, blocks, s) : grad_go<DT, RES, kLanes, 4>(a, blocks, s);
 }
 
 template <int DT, bool RES>
@@ -501,7 +502,7 @@ hipError_t grad_any(const NormGradArgs& a, hipStream_t s)
         if ((e = hipGetLastError()) != hipSuccess) return e;
         k_norm_grad_long<DT, RES><<<long_blocks(a.m), 1024, 0, s>>>(a);
         e = hipGetLastError();
-    } else if (a.n <= 2048) {
+    } else if (a.n <= 1536) {
         e = grad_pieces<DT, RES, 64>(a, blocks, s);
     } else if (a.n <= 8192) {
         e = grad_pieces<DT, RES, 256>(a, blocks, s);
@@ -523,11 +524,14 @@ int norm_grad_blocks(int64_t m, int64_t n)
     }
     const int lanes = grad_lanes(n), rows = 512 / lanes;
     const int64_t b = (m + rows - 1) / rows, pieces = (n / 8 + lanes - 1) / lanes;
-    // one workgroup's rounds take about half a us for each piece of a thread's; more than one need the sums' launch (16
-    // rows of 2048 in two rounds 6.7 us, 24 in three 8.7; with a workgroup for every eight 7.8; 32 rows of 512 in four
-    // rounds 4.9, 64 in eight 7.3; with a workgroup for every eight 6.0)
+    // one workgroup's rounds take about half a us for each piece of a thread's; more workgroups need the sums' launch (8
+    // rows of 2048 5.5 us in four rounds, 7.6 with a workgroup for every two; 32 rows of 512 4.9 in four and 64 7.3 in
+    // eight, with a workgroup for every eight 6.0)
     if (b <= 5 && b * pieces <= 8) return 1;
-    return (int)(b < 256 ? b : 256);
+    // past 64 two rounds each and half the partials (333 x 2048 7.9 us, with one round 8.5; 300 x 16384 18.2 and 21.5)
+    const int64_t half = (b + 1) / 2;
+    if (b > 64) return (int)(half < 64 ? 64 : half < 256 ? half : 256);
+    return (int)b;
 }
 
 hipError_t launch_layer_norm(int dtype, const NormArgs& a, hipStream_t s)
