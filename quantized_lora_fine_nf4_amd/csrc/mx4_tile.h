@@ -33,7 +33,7 @@ struct TileCosts {
 };
 
 // So many small tiles of so many steps: rounds of two on each compute unit and a rest.
-// Between one and two on each it grows with their number, a quarter of the way at once.
+// Between one and two on each it grows with their number, 0.4 of the way at once.
 inline double small_us(int64_t tiles, int steps, const TileCosts& c)
 {
     const double one = steps * c.one_step + c.one_tile, two = steps * c.two_step + c.two_tile;
@@ -41,7 +41,7 @@ inline double small_us(int64_t tiles, int steps, const TileCosts& c)
     if (rest == 0) return rounds * two;
     if (rest <= kCus) return rounds * two + one;
     const double over = double(rest - kCus) / kCus;
-    return rounds * two + one + (two - one) * (over > 0.25 ? over : 0.25);
+    return rounds * two + one + (two - one) * (over > 0.4 ? over : 0.4);
 }
 
 // The small tiles of m x ncol outputs: into how many parts their reduction goes and
