@@ -11,8 +11,8 @@
 //
 // A step is 256 columns: 128 bytes of codes and 8 scales of each row.  The codes go
 // straight to one of two LDS buffers (global_load_lds) while the other one is
-// multiplied.  The 16-byte pieces of a row are permuted by its index, so that eight
-// lanes that read eight rows touch all banks.  Weight row TN r + c of a wave's columns is row r of
+// multiplied.  The 16-byte pieces of a row are permuted by half its index, so that
+// a read's lanes touch all 64 banks (two rows).  Weight row TN r + c of a wave's columns is row r of
 // its tile c: a lane ends with TN consecutive columns.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -107,9 +107,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     const MX4_GLOBAL uint8_t* asp = (const MX4_GLOBAL uint8_t*)g.xscales + m0 * spitch + aso;
     const MX4_GLOBAL uint8_t* wsp = (const MX4_GLOBAL uint8_t*)g.scales + n0 * spitch + wso;
 
-    // the codes of a step: wave instructions of eight rows each; piece p of row i lies at p ^ (i & 7), and this
+    // the codes of a step: wave instructions of eight rows each; piece p of row i lies at p ^ (i / 2 & 7), and this
     // thread fetches what belongs into slot t % 8 of rows t / 8 + 32 i
-    const int slot = t & 7, piece = slot ^ ((t >> 3) & 7);
+    const int slot = t & 7, piece = slot ^ ((t >> 4) & 7);
     auto fetch = [&](Buffer<TM, TN>& b, int step, auto from, auto to) {
         const int left = spitch - step * kGroups;
         // a piece past the row's end: the step's first one, under scales of 0
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     const uint32_t pick = h ? 0x07050301u : 0x06040200u;   // this half's scales of the four sub-steps
     u32x2 na[TM], nw[TN];
     auto frags = [&](const Buffer<TM, TN>& b, int s, int to) {
-        const int at = r * 8 + ((2 * s + h) ^ (r & 7));
+        const int at = r * 8 + ((2 * s + h) ^ ((r >> 1) & 7));
         // in the order of their use
         fa[to][0] = b.a[wm * TM * 256 + at];
 #pragma unroll
