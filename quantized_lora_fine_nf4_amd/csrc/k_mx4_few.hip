@@ -390,9 +390,10 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
     store8(out, kind, row * ldo + 8 * (i - row * width8), a, b);
 }
 
-// k_few's time: about 4 us, and 30 ns for each load instruction of a compute unit
-// (64 lanes on 64 lines).  kRT x kMT tiles of 16 x 16 a wave, as many as leave 160
-// workgroups (4096 x 4096, 4 tokens: 1 x 1 5.7 us, 2 x 1 7.5; 13824 x 5120, 16
+// k_few's time in us: for each round of a workgroup on every compute unit 1.5, 0.15 for
+// each of a wave's tiles and 30 ns (22 with x in codes) for each load instruction of its
+// waves (64 lanes on 64 lines).  kRT x kMT tiles of 16 x 16 a wave,
+// the cheapest (4096 x 4096, 4 tokens: 1 x 1 5.7, 2 x 1 7.5; 13824 x 5120, 16
 // tokens: 4 x 1 16.1, 2 x 1 20.5, 1 x 1 29.6).
 struct FewPlan {
     int rt, mt;
@@ -405,11 +406,11 @@ FewPlan few_plan(int64_t rows, int64_t cols, int64_t m, bool codes)
     for (int rt = 4; rt; rt >>= 1)
         for (int mt = 4; mt; mt >>= 1) {
             if (mt > 1 && 8 * mt >= m) continue;   // half of it would be empty
-            const double groups = double(ceil_div(rows, 16 * rt)) * double(ceil_div(m, 16 * mt));
-            if ((groups < 160 && rt * mt > 1) || rt * mt <= best.rt * best.mt) continue;
+            const double rounds = double(ceil_div(ceil_div(rows, 16 * rt) * ceil_div(m, 16 * mt), kCus));
             const double full = m < 16 ? m / 16.0 : 1.0;   // lanes of x that read
             const double loads = double(ceil_div(cols, 128)) * (2 * rt + (codes ? 2 : 4) * mt * full);
-            best = {rt, mt, 4.0 + (groups > 256 ? groups / 256 : 1) * loads * 0.03};
+            const double us = 1.0 + rounds * (1.5 + 0.15 * rt * mt + loads * (codes ? 0.022 : 0.03));
+            if (best.rt == 0 || us < best.us) best = {rt, mt, us};
         }
     return best;
 }
@@ -417,35 +418,49 @@ FewPlan few_plan(int64_t rows, int64_t cols, int64_t m, bool codes)
 // k_thin's tokens: with x in 16 bits a token's values are four times those of its codes.
 bool thin(int64_t m, bool codes) { return m <= (codes ? 16 : 8); }
 
-// Against the tiled kernels' estimate.  Those take at least 256 columns with both operands in codes.
-bool mm_few(int64_t rows, int64_t cols, int64_t m, bool forward)
-{
-    // backward against the tiled kernels: 16 tokens through 13824 x 5120 20.8 us (23.9), 32 30.4 (25.3); 32 through
-    // 4096 x 4096 13.2 (16.2), 48 17.0 (15.3)
-    if (!forward) return m <= (rows * cols <= int64_t(1) << 25 ? 32 : 16);
-    return thin(m, false) || (m <= 64 && few_plan(rows, cols, m, false).us < mm_tiled_us(cols, rows, m));
-}
-bool mm4_few(int64_t rows, int64_t cols, int64_t m)
-{
-    return cols < 256 || thin(m, true) || (m <= 64 && few_plan(rows, cols, m, true).us < mm4_tiled_us(rows, cols, m));
-}
-
-// Tiles of 16 tokens a workgroup takes backward, and how many workgroups they make.
+// Backward: tiles of 16 tokens a workgroup takes, how many workgroups they make, and a wave's columns.
 int token_tiles(int64_t m) { return m <= 16 ? 1 : 2; }
-uint32_t token_groups(int64_t m, int tiles) { return (uint32_t)ceil_div(m, 16 * tiles); }
-
-// Backward: columns of a wave.
+uint32_t token_groups(int64_t m) { return (uint32_t)ceil_div(m, 16 * token_tiles(m)); }
 int back_columns(int64_t m) { return m <= 16 ? 256 : 128; }
 
-// Backward: parts of the reduction so that about 1,024 workgroups run, each
-// wave with two slabs at least.
+// Parts of the reduction so that about 1,024 workgroups run, each wave with two
+// slabs at least.
 int back_parts(int64_t rows, int64_t cols, int64_t m)
 {
-    const int64_t groups = ceil_div(cols, back_columns(m)) * ceil_div(m, 16 * token_tiles(m)), slabs = ceil_div(rows, 32);
+    const int64_t groups = ceil_div(cols, back_columns(m)) * token_groups(m), slabs = ceil_div(rows, 32);
     int64_t p = ceil_div(1024, groups);
     const int64_t most = ceil_div(slabs, 2 * kWaves);
     if (p > most) p = most;
     return (int)(p < 1 ? 1 : p > 16 ? 16 : p);
+}
+
+// k_few_back's time in us: the launch, 1.2 for a round's sums over the waves, 0.34 for
+// each slab of a wave on a compute unit but 1.4 for one after another of the same
+// wave, and the split's sum.
+double back_us(int64_t rows, int64_t cols, int64_t m)
+{
+    const int64_t groups = ceil_div(cols, back_columns(m)) * token_groups(m), slabs = ceil_div(rows, 32);
+    const int parts = back_parts(rows, cols, m);
+    const double one = 1.4 * double(ceil_div(slabs, (int64_t)kWaves * parts)), all = 0.34 * double(groups) * double(slabs) / kCus;
+    return 2.5 + 1.2 * double(ceil_div(groups * parts, kCus)) + (one > all ? one : all) +
+           (parts > 1 ? 3.0 + double(parts) * double(m) * double(cols) * 8e-6 / 6.0 : 0.0);
+}
+
+// Whether these kernels take a product, or the tiled ones: by the estimates, up to as many tokens as their grids are
+// made for (both in 16 bits: 100 tokens through 1024 x 1024 4.0 us, tiled 10.1; 64 through 4096 x 4096 14.0 and 15.1,
+// through 13824 x 5120 32.1 and 28.3; backward 300 through 512 x 512 6.6 and 8.7, 64 through 4096 x 4096 18.8 and
+// 14.3).  The tiled kernel of two operands in codes takes rows of 256 at least.
+constexpr int64_t kFewTokens = 4096;
+
+bool mm_few(int64_t rows, int64_t cols, int64_t m, bool forward)
+{
+    if (m > kFewTokens) return false;
+    if (!forward) return m <= 16 || back_us(rows, cols, m) < mm_tiled_us(rows, cols, m);
+    return thin(m, false) || few_plan(rows, cols, m, false).us < mm_tiled_us(cols, rows, m);
+}
+bool mm4_few(int64_t rows, int64_t cols, int64_t m)
+{
+    return cols < 256 || thin(m, true) || (m <= kFewTokens && few_plan(rows, cols, m, true).us < mm4_tiled_us(rows, cols, m));
 }
 
 template <int DT, int kRT>
@@ -478,7 +493,7 @@ hipError_t few_go(FewArgs a, hipStream_t s)
         return thin_go<DT, 4, 2, 4>(a, s);
     }
     const FewPlan p = few_plan(a.rows, a.cols, a.m, DT == 2);
-    a.token_tiles = token_groups(a.m, p.mt);
+    a.token_tiles = (uint32_t)ceil_div(a.m, 16 * p.mt);
     if (p.rt == 4) return few_tokens<DT, 4>(a, p.mt, s);
     return p.rt == 2 ? few_tokens<DT, 2>(a, p.mt, s) : few_tokens<DT, 1>(a, p.mt, s);
 }
@@ -515,7 +530,7 @@ hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales,
                          bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s)
 {
     if (!mm_few(rows, cols, m, forward)) return launch_mm_tiled(dtype, codes, scales, rows, cols, forward, x, m, out, out_kind, part, s);
-    FewArgs a{codes, scales, x, nullptr, out, part, m, rows, cols, out_kind, 1, token_groups(m, token_tiles(m))};
+    FewArgs a{codes, scales, x, nullptr, out, part, m, rows, cols, out_kind, 1, token_groups(m)};
     if (forward) return dtype == 0 ? few_go<0>(a, s) : few_go<1>(a, s);
     a.parts = back_parts(rows, cols, m);
     const hipError_t e = dtype == 0 ? few_back_go<0>(a, s) : few_back_go<1>(a, s);

@@ -338,7 +338,7 @@ hipError_t mm_go(int dtype, bool forward, const MmArgs& a, hipStream_t s)
 
 // 4096 tokens through 4096 x 1024 .. 13824 take 38.8 .. 353 us, 128 through 13824 x 5120 in 1, 2, 4 parts 57.3, 38.4 and
 // 33.2, 256 through 4096 x 11008 in 4, 5, 6, 8 parts 41.2, 39.7, 36.8 and 40.3.
-constexpr TileCosts kCosts = {1.58, 12.0, 0.64, 4.5, 0.98, 7.0};
+constexpr TileCosts kCosts = {1.58, 12.0, 0.67, 3.2, 0.98, 7.0};
 
 TilePlan mm_plan(int64_t kred, int64_t ncol, int64_t m) { return tile_plan(m, ncol, (int)ceil_div(kred, kStep), kCosts); }
 

@@ -225,7 +225,7 @@ hipError_t mm4_go(Mm4Args a, hipStream_t s)
 
 // 4096 tokens through 4096 x 1024 .. 13824 take 22.0 .. 113 us, 333 through 2048 x 8192 in 1, 2, 4, 8 parts 28.5, 20.6,
 // 16.3 and 18.7.
-constexpr TileCosts kCosts = {1.80, 14.0, 0.80, 4.7, 1.50, 7.0};
+constexpr TileCosts kCosts = {1.80, 14.0, 0.90, 3.2, 1.50, 7.0};
 
 TilePlan mm4_plan(int64_t rows, int64_t cols, int64_t m) { return tile_plan(m, rows, (int)ceil_div(cols, kStep), kCosts); }
 

@@ -45,8 +45,8 @@ inline double small_us(int64_t tiles, int steps, const TileCosts& c)
 }
 
 // The small tiles of m x ncol outputs: into how many parts their reduction goes and
-// what that costs, with 2.3 us for the sum's launch and the partials' 8 bytes (written
-// and read) at 6.5 TB/s.
+// what that costs, with 4.3 us for the sum and the partials' 8 bytes (written and read)
+// at 6 TB/s (they stay in the caches).
 inline TileGrid small_plan(int64_t m, int64_t ncol, int steps, const TileCosts& c, double* cost)
 {
     TileGrid best = {(int)ceil_div(m, 128), (int)ceil_div(ncol, 128), 1, steps};
@@ -54,7 +54,7 @@ inline TileGrid small_plan(int64_t m, int64_t ncol, int steps, const TileCosts& 
     *cost = small_us(tiles, steps, c);
     for (int p = 2; p <= 16 && p <= steps; ++p) {
         const int per = (int)ceil_div(steps, p), parts = (int)ceil_div(steps, per);
-        const double us = small_us(tiles * parts, per, c) + 2.3 + double(parts) * double(m) * double(ncol) * 8e-6 / 6.5;
+        const double us = small_us(tiles * parts, per, c) + 4.3 + double(parts) * double(m) * double(ncol) * 8e-6 / 6.0;
         if (us < *cost) {
             *cost = us;
             best.parts = parts;
