@@ -21,6 +21,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <type_traits>
 
 #include "mx4_format.h"
@@ -83,10 +84,10 @@ __device__ __forceinline__ uint32_t load_scales(const MX4_GLOBAL uint8_t* p, int
 }
 
 // DT 0, 1: x in bf16, fp16; 2: in codes.
-template <int DT, int kRT, int kMT>
-__global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
+template <int DT, int kRT, int kMT, int kW>
+__global__ __launch_bounds__(64 * kW) void k_few(FewArgs a)
 {
-    __shared__ f32x4 sums[kWaves][kRT * kMT][64];
+    __shared__ f32x4 sums[kW > 1 ? kW : 1][kW > 1 ? kRT * kMT : 1][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)(blockIdx.x / a.token_tiles) * (16 * kRT), t0 = (int64_t)(blockIdx.x % a.token_tiles) * (16 * kMT);
     const int64_t blocks = a.cols / kGroup;
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
     f32x4 acc[kRT][kMT] = {};
     u32x4 x[kMT][DT == 2 ? 1 : 4] = {};
     uint32_t e[kMT] = {};
-    for (int64_t at = 16 * wave; at < blocks; at += 16 * kWaves) {
+    for (int64_t at = 16 * wave; at < blocks; at += 16 * kW) {
         const int64_t blk = at + 4 * g;                      // this lane's four
         const int have = (int)least(blocks - blk, 4);
         uint32_t s[kRT];
@@ -162,19 +163,29 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(FewArgs a)
         part(std::integral_constant<int, 2>{});
         part(std::integral_constant<int, 3>{});
     }
-#pragma unroll
-    for (int i = 0; i < kRT; ++i)
-#pragma unroll
-        for (int u = 0; u < kMT; ++u) sums[wave][i * kMT + u][lane] = acc[i][u];
-    __syncthreads();
     // lane (r, g) of a tile: token r, weight rows 4 g .. 4 g + 3
-    for (int e = threadIdx.x; e < kRT * kMT * 64; e += 64 * kWaves) {
-        const int tile = e >> 6, l = e & 63;
-        f32x4 v = sums[0][tile][l];
+    if constexpr (kW == 1) {
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += sums[w][tile][l];
-        const int64_t t = t0 + 16 * (tile % kMT) + (l & 15), n = n0 + 16 * (tile / kMT) + 4 * (l >> 4);
-        if (t < a.m && n < a.rows) store4(a.out, a.kind, t * a.rows + n, v);
+        for (int i = 0; i < kRT; ++i)
+#pragma unroll
+            for (int u = 0; u < kMT; ++u) {
+                const int64_t t = t0 + 16 * u + r, n = n0 + 16 * i + 4 * g;
+                if (t < a.m && n < a.rows) store4(a.out, a.kind, t * a.rows + n, acc[i][u]);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRT; ++i)
+#pragma unroll
+            for (int u = 0; u < kMT; ++u) sums[wave][i * kMT + u][lane] = acc[i][u];
+        __syncthreads();
+        for (int e = threadIdx.x; e < kRT * kMT * 64; e += 64 * kW) {
+            const int tile = e >> 6, l = e & 63;
+            f32x4 v = sums[0][tile][l];
+#pragma unroll
+            for (int w = 1; w < kW; ++w) v += sums[w][tile][l];
+            const int64_t t = t0 + 16 * (tile % kMT) + (l & 15), n = n0 + 16 * (tile / kMT) + 4 * (l >> 4);
+            if (t < a.m && n < a.rows) store4(a.out, a.kind, t * a.rows + n, v);
+        }
     }
 }
 
@@ -395,6 +406,9 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
 // waves (64 lanes on 64 lines).  kRT x kMT tiles of 16 x 16 a wave,
 // the cheapest (4096 x 4096, 4 tokens: 1 x 1 5.7, 2 x 1 7.5; 13824 x 5120, 16
 // tokens: 4 x 1 16.1, 2 x 1 20.5, 1 x 1 29.6).
+// Rows of one run need one wave, and many of those fit a compute unit at once.
+constexpr int64_t kOneWave = 512;
+
 struct FewPlan {
     int rt, mt;
     double us;
@@ -406,10 +420,12 @@ FewPlan few_plan(int64_t rows, int64_t cols, int64_t m, bool codes)
     for (int rt = 4; rt; rt >>= 1)
         for (int mt = 4; mt; mt >>= 1) {
             if (mt > 1 && 8 * mt >= m) continue;   // half of it would be empty
-            const double rounds = double(ceil_div(ceil_div(rows, 16 * rt) * ceil_div(m, 16 * mt), kCus));
+            const double groups = double(ceil_div(rows, 16 * rt)) * double(ceil_div(m, 16 * mt));
             const double full = m < 16 ? m / 16.0 : 1.0;   // lanes of x that read
             const double loads = double(ceil_div(cols, 128)) * (2 * rt + (codes ? 2 : 4) * mt * full);
-            const double us = 1.0 + rounds * (1.5 + 0.15 * rt * mt + loads * (codes ? 0.022 : 0.03));
+            const double each = 0.15 * rt * mt, load = loads * (codes ? 0.022 : 0.03);
+            const double us = cols <= kOneWave ? 2.5 + each + (groups > kCus ? groups / kCus : 1.0) * load
+                                               : 1.0 + std::ceil(groups / kCus) * (1.5 + each + load);
             if (best.rt == 0 || us < best.us) best = {rt, mt, us};
         }
     return best;
@@ -463,14 +479,21 @@ bool mm4_few(int64_t rows, int64_t cols, int64_t m)
     return cols < 256 || thin(m, true) || (m <= kFewTokens && few_plan(rows, cols, m, true).us < mm4_tiled_us(rows, cols, m));
 }
 
-template <int DT, int kRT>
+template <int DT, int kRT, int kW>
 hipError_t few_tokens(const FewArgs& a, int mt, hipStream_t s)
 {
     const dim3 grid((unsigned)ceil_div(a.rows, 16 * kRT) * a.token_tiles);
-    if (mt == 1) k_few<DT, kRT, 1><<<grid, 64 * kWaves, 0, s>>>(a);
-    else if (mt == 2) k_few<DT, kRT, 2><<<grid, 64 * kWaves, 0, s>>>(a);
-    else k_few<DT, kRT, 4><<<grid, 64 * kWaves, 0, s>>>(a);
+    if (mt == 1) k_few<DT, kRT, 1, kW><<<grid, 64 * kW, 0, s>>>(a);
+    else if (mt == 2) k_few<DT, kRT, 2, kW><<<grid, 64 * kW, 0, s>>>(a);
+    else k_few<DT, kRT, 4, kW><<<grid, 64 * kW, 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <int DT, int kW>
+hipError_t few_rows(const FewArgs& a, const FewPlan& p, hipStream_t s)
+{
+    if (p.rt == 4) return few_tokens<DT, 4, kW>(a, p.mt, s);
+    return p.rt == 2 ? few_tokens<DT, 2, kW>(a, p.mt, s) : few_tokens<DT, 1, kW>(a, p.mt, s);
 }
 
 template <int DT, int kRT, int kTG, int kThinWaves>
@@ -494,8 +517,7 @@ hipError_t few_go(FewArgs a, hipStream_t s)
     }
     const FewPlan p = few_plan(a.rows, a.cols, a.m, DT == 2);
     a.token_tiles = (uint32_t)ceil_div(a.m, 16 * p.mt);
-    if (p.rt == 4) return few_tokens<DT, 4>(a, p.mt, s);
-    return p.rt == 2 ? few_tokens<DT, 2>(a, p.mt, s) : few_tokens<DT, 1>(a, p.mt, s);
+    return a.cols <= kOneWave ? few_rows<DT, 1>(a, p, s) : few_rows<DT, kWaves>(a, p, s);
 }
 
 template <int DT>

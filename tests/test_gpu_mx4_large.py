@@ -139,6 +139,35 @@ def test_every_number_of_few_tokens(rows, cols):
         assert untouched(buf)
 
 
+@pytest.mark.parametrize("m,rows,cols", [(700, 1000, 1504), (1500, 520, 480), (4096, 72, 512), (4097, 72, 512), (300, 3000, 96),
+                                         (333, 88, 2528), (1001, 2000, 64), (200, 1000, 2016), (130, 8, 32)])
+def test_many_tokens_through_small_weights(m, rows, cols):
+    """Where the few-token kernels take many tokens too: waves that share the columns, and one wave for all of them."""
+    g = gen(m + cols)
+    codes, scales = matrix(rows, cols, g)
+    scales[rows // 2, 0] = 255
+    v = values(codes, scales)
+    w = v.float().to(FP16).double()
+    ok = torch.arange(rows, device="cuda") != rows // 2
+    print_case("many tokens, small weight", m, rows, cols)
+    for out_dtype in (FP16, FP32):
+        x = torch.randn(m, cols, generator=g, device="cuda").to(FP16)
+        buf, out = guarded(m, rows, out_dtype)
+        matmul(codes, scales, x, out)
+        check(out[:, ok], x.double(), w[ok].t().contiguous(), ("forward", out_dtype))
+        assert torch.isnan(out[:, rows // 2]).all() and untouched(buf)
+        xc, xs = matrix(m, cols, g, 122, 129)
+        buf, out = guarded(m, rows, out_dtype)
+        matmul4(codes, scales, xc, xs, out)
+        check(out[:, ok], values(xc, xs), v[ok].t().contiguous(), ("codes", out_dtype))
+        assert torch.isnan(out[:, rows // 2]).all() and untouched(buf)
+        y = torch.randn(m, rows, generator=g, device="cuda").to(FP16)
+        buf, out = guarded(m, cols, out_dtype)
+        matmul(codes, scales, y, out, True)
+        check(out[:, 32:], y.double(), w[:, 32:].nan_to_num(), ("backward", out_dtype)) if cols > 32 else None
+        assert torch.isnan(out[:, :32]).all() and untouched(buf)
+
+
 @pytest.mark.parametrize("m", [600, 4000])
 def test_large_tiles_keep_what_is_not_finite(m):
     """The first piece of the last, ragged step holds what a piece past the row's end reads in its place; a neighbour
