@@ -286,12 +286,14 @@ __device__ __forceinline__ void decode_columns(const uint32_t (&c)[8], const flo
     }
 }
 
-// 64 kWords columns a wave: kWords dwords of each of eight rows a lane.
-template <int DT, int kMT, int kWords>
+// 128 kWords columns a wave: kWords dwords of each of eight rows a lane.  The waves'
+// sums meet in LDS, in kPhases parts that each take turns there.
+template <int DT, int kMT, int kWords, int kPhases>
 __global__ __launch_bounds__(64 * kWaves) void k_few_back(FewArgs a)
 {
-    constexpr int kTiles = 8 * kWords;
-    __shared__ f32x4 sums[kWaves / 2][kTiles * kMT][64];
+    constexpr int kTiles = 8 * kWords, kShare = kTiles * kMT / kPhases, kPairs = kShare / 2;
+    static_assert(64 * kPairs * kPhases == 64 * kWaves, "a pair of tiles' lane for each thread");
+    __shared__ f32x4 sums[kWaves][kShare][65];   // 65: lanes that read neighbouring tiles touch other banks
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     const int64_t c0 = (int64_t)(blockIdx.x / a.token_tiles) * (16 * kTiles), t0 = (int64_t)(blockIdx.x % a.token_tiles) * (16 * kMT);
     const int64_t col = least(c0 + kTiles * r, a.cols - kTiles);
@@ -339,38 +341,35 @@ __global__ __launch_bounds__(64 * kWaves) void k_few_back(FewArgs a)
                 for (int i = 0; i < 8; ++i) acc[u][8 * k + i] = mfma16<DT>(x[u], w[i], acc[u][8 * k + i]);
         }
     }
-    // the upper half of the waves' sums to LDS and added by the lower half, until one is left
+    // a thread adds up two neighbouring tiles of one lane: two columns of four tokens
+    const int phase = threadIdx.x / (64 * kPairs), pair = threadIdx.x % kPairs, from = threadIdx.x / kPairs % 64;
+    f32x4 v0, v1;
 #pragma unroll
-    for (int half = kWaves / 2; half; half >>= 1) {
-        if (wave >= half && wave < 2 * half) {
+    for (int ph = 0; ph < kPhases; ++ph) {
+        if (ph > 0) __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kTiles * kMT; ++i) sums[wave - half][i][lane] = acc[i / kTiles][i % kTiles];
-        }
+        for (int i = 0; i < kShare; ++i) sums[wave][i][lane] = acc[(ph * kShare + i) / kTiles][(ph * kShare + i) % kTiles];
         __syncthreads();
-        if (wave < half) {
+        if (phase == ph) {
+            v0 = sums[0][2 * pair][from];
+            v1 = sums[0][2 * pair + 1][from];
 #pragma unroll
-            for (int i = 0; i < kTiles * kMT; ++i) acc[i / kTiles][i % kTiles] += sums[wave][i][lane];
-        }
-        __syncthreads();
-    }
-    if (wave != 0 || c0 + kTiles * r >= a.cols) return;
-    void* out = a.parts > 1 ? (void*)(a.part + (int64_t)blockIdx.y * a.m * a.cols) : a.out;
-    const int kind = a.parts > 1 ? (int)kOutFp32 : a.kind;
-    // lane (r, g): tokens 4 g .. 4 g + 3, columns kTiles r .. kTiles r + kTiles - 1
-#pragma unroll
-    for (int u = 0; u < kMT; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t t = t0 + 16 * u + 4 * g + i;
-            if (t < a.m) {
-#pragma unroll
-                for (int k = 0; k < kWords; ++k) {
-                    const f32x4* v = acc[u] + 8 * k;
-                    store8(out, kind, t * a.cols + col + 8 * k, f32x4{v[0][i], v[1][i], v[2][i], v[3][i]},
-                           f32x4{v[4][i], v[5][i], v[6][i], v[7][i]});
-                }
+            for (int w = 1; w < kWaves; ++w) {
+                v0 += sums[w][2 * pair][from];
+                v1 += sums[w][2 * pair + 1][from];
             }
         }
+    }
+    const int tile = phase * kShare + 2 * pair;
+    const int64_t c = c0 + kTiles * (from & 15) + tile % kTiles;
+    if (c >= a.cols) return;
+    void* out = a.parts > 1 ? (void*)(a.part + (int64_t)blockIdx.y * a.m * a.cols) : a.out;
+    const int kind = a.parts > 1 ? (int)kOutFp32 : a.kind;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t t = t0 + 16 * (tile / kTiles) + 4 * (from >> 4) + i;
+        if (t < a.m) store2(out, kind, t * a.cols + c, f32x2{v0[i], v1[i]});
+    }
 }
 
 __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits, int64_t n, int width8, void* out,
@@ -439,27 +438,29 @@ int token_tiles(int64_t m) { return m <= 16 ? 1 : 2; }
 uint32_t token_groups(int64_t m) { return (uint32_t)ceil_div(m, 16 * token_tiles(m)); }
 int back_columns(int64_t m) { return m <= 16 ? 256 : 128; }
 
-// Parts of the reduction so that about 1,024 workgroups run, each wave with two
-// slabs at least.
-int back_parts(int64_t rows, int64_t cols, int64_t m)
+// k_few_back's parts of the reduction and its time in us: the launch, 0.5 for each
+// round's sums over the waves, 0.34 for each slab of a wave on a compute unit but 1.2
+// for one after another of the same wave, and the split's sum.  One part, or as many
+// as make about 1,024 workgroups with two slabs a wave at least.
+struct BackPlan {
+    int parts;
+    double us;
+};
+
+BackPlan back_plan(int64_t rows, int64_t cols, int64_t m)
 {
     const int64_t groups = ceil_div(cols, back_columns(m)) * token_groups(m), slabs = ceil_div(rows, 32);
+    auto us = [&](int64_t parts) {
+        const double one = 1.2 * double(ceil_div(slabs, kWaves * parts)), all = 0.34 * double(groups) * double(slabs) / kCus;
+        return 2.5 + 0.5 * double(ceil_div(groups * parts, kCus)) + (one > all ? one : all) +
+               (parts > 1 ? 3.0 + double(parts) * double(m) * double(cols) * 8e-6 / 6.0 : 0.0);
+    };
     int64_t p = ceil_div(1024, groups);
     const int64_t most = ceil_div(slabs, 2 * kWaves);
-    if (p > most) p = most;
-    return (int)(p < 1 ? 1 : p > 16 ? 16 : p);
-}
-
-// k_few_back's time in us: the launch, 1.2 for a round's sums over the waves, 0.34 for
-// each slab of a wave on a compute unit but 1.4 for one after another of the same
-// wave, and the split's sum.
-double back_us(int64_t rows, int64_t cols, int64_t m)
-{
-    const int64_t groups = ceil_div(cols, back_columns(m)) * token_groups(m), slabs = ceil_div(rows, 32);
-    const int parts = back_parts(rows, cols, m);
-    const double one = 1.4 * double(ceil_div(slabs, (int64_t)kWaves * parts)), all = 0.34 * double(groups) * double(slabs) / kCus;
-    return 2.5 + 1.2 * double(ceil_div(groups * parts, kCus)) + (one > all ? one : all) +
-           (parts > 1 ? 3.0 + double(parts) * double(m) * double(cols) * 8e-6 / 6.0 : 0.0);
+    p = p > most ? most : p;
+    p = p > 16 ? 16 : p;
+    const double whole = us(1), split = us(p);
+    return p < 2 || whole <= split ? BackPlan{1, whole} : BackPlan{(int)p, split};
 }
 
 // Whether these kernels take a product, or the tiled ones: by the estimates, up to as many tokens as their grids are
@@ -471,7 +472,7 @@ constexpr int64_t kFewTokens = 4096;
 bool mm_few(int64_t rows, int64_t cols, int64_t m, bool forward)
 {
     if (m > kFewTokens) return false;
-    if (!forward) return m <= 16 || back_us(rows, cols, m) < mm_tiled_us(rows, cols, m);
+    if (!forward) return m <= 16 || back_plan(rows, cols, m).us < mm_tiled_us(rows, cols, m);
     return thin(m, false) || few_plan(rows, cols, m, false).us < mm_tiled_us(cols, rows, m);
 }
 bool mm4_few(int64_t rows, int64_t cols, int64_t m)
@@ -525,8 +526,10 @@ hipError_t few_back_go(const FewArgs& a, hipStream_t s)
 {
     const int mt = token_tiles(a.m);
     const dim3 grid((unsigned)ceil_div(a.cols, back_columns(a.m)) * a.token_tiles, (unsigned)a.parts);
-    if (mt == 1) k_few_back<DT, 1, 2><<<grid, 64 * kWaves, 0, s>>>(a);
-    else k_few_back<DT, 2, 1><<<grid, 64 * kWaves, 0, s>>>(a);
+    // in one phase the sums take most of a compute unit's LDS
+    const bool alone = (int64_t)grid.x * grid.y <= kCus;
+    if (mt == 1) alone ? k_few_back<DT, 1, 2, 1><<<grid, 64 * kWaves, 0, s>>>(a) : k_few_back<DT, 1, 2, 2><<<grid, 64 * kWaves, 0, s>>>(a);
+    else alone ? k_few_back<DT, 2, 1, 1><<<grid, 64 * kWaves, 0, s>>>(a) : k_few_back<DT, 2, 1, 2><<<grid, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -544,7 +547,7 @@ size_t matmul_ws(int64_t rows, int64_t cols, bool forward, int64_t m)
 {
     if (!mm_few(rows, cols, m, forward)) return forward ? mm_tiled_ws(cols, rows, m) : mm_tiled_ws(rows, cols, m);
     if (forward) return 0;
-    const int parts = back_parts(rows, cols, m);
+    const int parts = back_plan(rows, cols, m).parts;
     return parts > 1 ? size_t(parts) * size_t(m) * size_t(cols) * sizeof(float) : 0;
 }
 
@@ -554,7 +557,7 @@ hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales,
     if (!mm_few(rows, cols, m, forward)) return launch_mm_tiled(dtype, codes, scales, rows, cols, forward, x, m, out, out_kind, part, s);
     FewArgs a{codes, scales, x, nullptr, out, part, m, rows, cols, out_kind, 1, token_groups(m)};
     if (forward) return dtype == 0 ? few_go<0>(a, s) : few_go<1>(a, s);
-    a.parts = back_parts(rows, cols, m);
+    a.parts = back_plan(rows, cols, m).parts;
     const hipError_t e = dtype == 0 ? few_back_go<0>(a, s) : few_back_go<1>(a, s);
     if (e != hipSuccess || a.parts == 1) return e;
     return launch_split_sum(part, a.parts, m, cols, out, cols, out_kind, s);

@@ -42,6 +42,14 @@ __device__ __forceinline__ void put8(MX4_GLOBAL char* p, const f32x4& a, const f
 }
 
 // The same with the type known at run time only, at element `at` of out.
+__device__ __forceinline__ void store2(void* out, int kind, int64_t at, const f32x2& v)
+{
+    MX4_GLOBAL char* p = (MX4_GLOBAL char*)out;
+    if (kind == kOutFp32) put2<kOutFp32>(p + 4 * at, v);
+    else if (kind == kOutBf16) put2<kOutBf16>(p + 2 * at, v);
+    else put2<kOutFp16>(p + 2 * at, v);
+}
+
 __device__ __forceinline__ void store4(void* out, int kind, int64_t at, const f32x4& v)
 {
     MX4_GLOBAL char* p = (MX4_GLOBAL char*)out;
