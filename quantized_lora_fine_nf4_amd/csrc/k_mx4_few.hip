@@ -508,6 +508,13 @@ template <int DT>
 hipError_t few_go(FewArgs a, hipStream_t s)
 {
     if (thin(a.m, DT == 2)) {
+        // few rows: four of them a workgroup and eight waves (a token through 64 x 6912 3.2 us, eight rows and four waves
+        // 4.0; six tokens 4.2, sixteen rows and two 9.4; through 1024 x 4096 3.9 and 5.0, but through 4096 x 4096 6.5 and 5.7)
+        if (a.rows <= 2048) {
+            if (a.m <= 4) return thin_go<DT, 1, 1, 8>(a, s);
+            if constexpr (DT == 2) return a.m <= 8 ? thin_go<DT, 1, 2, 8>(a, s) : thin_go<DT, 1, 4, 8>(a, s);
+            return thin_go<DT, 1, 2, 8>(a, s);
+        }
         const int64_t runs = ceil_div(a.cols, 512);
         if (a.m <= 4) return thin_go<DT, 2, 1, 4>(a, s);
         if constexpr (DT == 2) return a.m <= 8 ? thin_go<DT, 2, 2, 4>(a, s) : thin_go<DT, 2, 4, 4>(a, s);
