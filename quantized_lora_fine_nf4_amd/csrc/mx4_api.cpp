@@ -5,7 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include "mx4_launch.h"
-#include "nf4_internal.h"
+#include "nf4_launch.h"
 
 namespace {
 

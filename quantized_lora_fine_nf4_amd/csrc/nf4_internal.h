@@ -29,7 +29,4 @@ static_assert(sizeof(LayerDesc) == 64, "layer table entry is 64 bytes");
 
 __host__ __device__ inline int64_t tiles_of(int64_t n) { return (n + kTileElems - 1) >> kTileShift; }
 
-// Keeps e as this thread's nf4_last_hip_error and returns NF4_E_HIP.
-int32_t hip_failed(hipError_t e);
-
 }  // namespace nf4k

@@ -8,6 +8,9 @@
 
 namespace nf4k {
 
+// Keeps e as this thread's nf4_last_hip_error and returns NF4_E_HIP.
+int32_t hip_failed(hipError_t e);
+
 // Fused blockwise quantisation (+ int8 double quantisation when dq) and, when
 // err_partial != nullptr, in-register dequantisation and the fp64 squared
 // error, written as kPartsPerTile partials per tile to err_partial; with
