@@ -54,12 +54,12 @@ nf4_status mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t r
  * x row-major in dtype, W's values rounded to dtype (as mx4_dequantize), sums
  * fp32 on the matrix cores; out row-major, fp32 (out_fp32 = 1) or dtype rounded
  * once.  rows a multiple of 8 and cols of 32 (else NF4_E_UNSUPPORTED), each
- * below 2^22; 1 <= m <= 2^25; m times the larger side at most 2^38.  x, codes and out 16-byte aligned; out must not
- * overlap the operands.  ws: mx4_matmul_workspace_bytes(rows, cols, backward, m),
- * 256-byte aligned, may be NULL where that is 0.  With few output tiles the
- * reduction is split and the parts are added in a fixed order.  A value that is
- * not finite acts as in fp32 arithmetic, in its own row and column of the result
- * only. */
+ * below 2^22; 1 <= m <= 2^25; m times the larger side at most 2^38.  x, codes
+ * and out 16-byte aligned; out must not overlap the operands.  ws:
+ * mx4_matmul_workspace_bytes(rows, cols, backward, m), 256-byte aligned, may be
+ * NULL where that is 0.  With few output tiles the reduction is split and the
+ * parts are added in a fixed order.  A value that is not finite acts as in fp32
+ * arithmetic, in its own row and column of the result only. */
 nf4_status mx4_matmul(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                       int32_t dtype, int32_t backward, const void* x, int64_t m, void* out,
                       int32_t out_fp32, void* ws, size_t ws_bytes, hipStream_t stream);

@@ -18,6 +18,12 @@
 // halves of two rows' results are put together as the fragments' pairs.  Column
 // T r + c of a wave's 16 T is row r of tile c, so that a lane ends with T
 // consecutive columns.
+//
+// One token through 13824 x 5120 in bf16 takes 9.0 us (4.2 TB/s of codes), backward
+// 19.4, where the conversion of each byte under its own row's scale counts and the
+// parts' sum takes 4.
+// With small weights these kernels need no second launch where the tiled ones split
+// their reduction, and take many tokens too.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -465,7 +471,7 @@ BackPlan back_plan(int64_t rows, int64_t cols, int64_t m)
 
 // Whether these kernels take a product, or the tiled ones: by the estimates, up to as many tokens as their grids are
 // made for (both in 16 bits: 100 tokens through 1024 x 1024 4.0 us, tiled 10.1; 64 through 4096 x 4096 14.0 and 15.1,
-// through 13824 x 5120 32.1 and 28.3; backward 300 through 512 x 512 6.6 and 8.7, 64 through 4096 x 4096 18.8 and
+// through 13824 x 5120 32.1 and 28.3; backward 300 through 512 x 512 5.3 and 8.7, 64 through 4096 x 4096 18.8 and
 // 14.3).  The tiled kernel of two operands in codes takes rows of 256 at least.
 constexpr int64_t kFewTokens = 4096;
 
@@ -535,8 +541,10 @@ hipError_t few_back_go(const FewArgs& a, hipStream_t s)
     const dim3 grid((unsigned)ceil_div(a.cols, back_columns(a.m)) * a.token_tiles, (unsigned)a.parts);
     // in one phase the sums take most of a compute unit's LDS
     const bool alone = (int64_t)grid.x * grid.y <= kCus;
-    if (mt == 1) alone ? k_few_back<DT, 1, 2, 1><<<grid, 64 * kWaves, 0, s>>>(a) : k_few_back<DT, 1, 2, 2><<<grid, 64 * kWaves, 0, s>>>(a);
-    else alone ? k_few_back<DT, 2, 1, 1><<<grid, 64 * kWaves, 0, s>>>(a) : k_few_back<DT, 2, 1, 2><<<grid, 64 * kWaves, 0, s>>>(a);
+    if (mt == 1 && alone) k_few_back<DT, 1, 2, 1><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (mt == 1) k_few_back<DT, 1, 2, 2><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (alone) k_few_back<DT, 2, 1, 1><<<grid, 64 * kWaves, 0, s>>>(a);
+    else k_few_back<DT, 2, 1, 2><<<grid, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
 }
 

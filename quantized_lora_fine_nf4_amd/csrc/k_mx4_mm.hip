@@ -27,7 +27,15 @@
 // 16-byte pieces lie permuted by half their row's index, so that a read's lanes
 // touch all 64 banks (two rows of 128 bytes).  Reads alone run 1.9 times as fast as
 // with a permutation by the index itself; the products, which other things bound,
-// take the same time.  x comes through a buffer descriptor that ends with it: rows
+// take the same time.
+//
+// 4096 tokens through 13824 x 5120 in bf16 take 473 us forward and 457 backward (1.22
+// and 1.27 PF; the library's product alone, of a weight in 16 bits, 487 and 628), 8192 x
+// 8192 x 8192 808 and 777.  The matrix cores are busy two thirds of the time: one wave a
+// SIMD waits at each step's barrier and at a tile's ends (12 us a round).  With operands
+// of zeros 8192 x 8192 x 8192 takes 622 us: the rest is the clock that the power leaves.
+// Eight waves of 128 x 64 took 3% longer, codes fetched four steps at once through
+// registers 3% too.  x comes through a buffer descriptor that ends with it: rows
 // past its end, and pieces past a row's end (offset kFar), arrive as zeros.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

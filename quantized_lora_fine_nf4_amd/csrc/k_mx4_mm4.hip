@@ -4,16 +4,21 @@
 // v_mfma_scale_f32_32x32x64 takes 32 codes (16 bytes, one group) and one scale
 // byte a lane, as they lie in memory: nothing is converted.  It does four times
 // the operations of the 16-bit instructions per cycle, so the operands' way to it
-// is what bounds the kernel: a 256 x 256 output tile by four waves of 128 x 128
-// (one per SIMD, 256 accumulator registers each) needs 192 KB through LDS for
-// 2,048 matrix cycles, 1,536 of the LDS's.  Eight waves of 128 x 64 would need
-// 256 KB, as many cycles as the matrix cores.
+// counts: a 256 x 256 output tile by four waves of 128 x 128 (one per SIMD, 256
+// accumulator registers each) reads 128 KB from LDS a step and 64 KB come into it, for
+// 2,048 matrix cycles.  Eight waves of 128 x 64 would read half as much again.
+//
+// 8192 x 8192 x 8192 takes 263 to 280 us (3.9 to 4.2 PF); with operands of zeros 205, so a
+// quarter of it is the clock that the power leaves.  A round of tiles through 5120
+// columns takes 47 us: 3.0 until the first step is there, 39 for the 20 steps, 3.5 for
+// the stores and 1.3 until the next tile.  Those ends are why 4096 tokens through
+// 13824 x 5120 (3.4 rounds, 183 us) reach 3.2 PF.
 //
 // A step is 256 columns: 128 bytes of codes and 8 scales of each row.  The codes go
 // straight to one of two LDS buffers (global_load_lds) while the other one is
 // multiplied.  The 16-byte pieces of a row are permuted by half its index, so that
-// a read's lanes touch all 64 banks (two rows).  Weight row TN r + c of a wave's columns is row r of
-// its tile c: a lane ends with TN consecutive columns.
+// a read's lanes touch all 64 banks (two rows).  Weight row TN r + c of a wave's
+// columns is row r of its tile c: a lane ends with TN consecutive columns.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
