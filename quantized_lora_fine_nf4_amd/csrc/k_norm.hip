@@ -429,8 +429,17 @@ __global__ __launch_bounds__(512) void k_norm_sum(const float* part, int blocks,
     const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
     const int64_t at = (int64_t)blockIdx.x * 64 + 4 * lane, width = 2 * (int64_t)n;
     f32x4 t = {0, 0, 0, 0};
-    if (at < width)
-        for (int b = group; b < blocks; b += 32) t += *((const GLOBAL f32x4*)(part + b * width + at));
+    if (at < width) {
+        // four loads on their way: a few of them one after another is all a small sum's time
+        for (int b = group; b < blocks; b += 128) {
+            f32x4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = *((const GLOBAL f32x4*)(part + (b + 32 * k < blocks ? b + 32 * k : b) * width + at));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (b + 32 * k < blocks) t += v[k];
+        }
+    }
     s[group][lane] = t;
     __syncthreads();
     if (group == 0 && at < width) {
