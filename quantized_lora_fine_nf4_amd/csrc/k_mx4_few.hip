@@ -478,8 +478,8 @@ constexpr int64_t kFewTokens = 4096;
 bool mm_few(int64_t rows, int64_t cols, int64_t m, bool forward)
 {
     if (m > kFewTokens) return false;
-    if (!forward) return m <= 16 || back_plan(rows, cols, m).us < mm_tiled_us(rows, cols, m);
-    return thin(m, false) || few_plan(rows, cols, m, false).us < mm_tiled_us(cols, rows, m);
+    if (!forward) return m <= 16 || back_plan(rows, cols, m).us < mm_tiled_us(rows, cols, m, false);
+    return thin(m, false) || few_plan(rows, cols, m, false).us < mm_tiled_us(cols, rows, m, true);
 }
 bool mm4_few(int64_t rows, int64_t cols, int64_t m)
 {
@@ -560,7 +560,7 @@ hipError_t launch_split_sum(const float* part, int splits, int64_t m, int64_t nc
 
 size_t matmul_ws(int64_t rows, int64_t cols, bool forward, int64_t m)
 {
-    if (!mm_few(rows, cols, m, forward)) return forward ? mm_tiled_ws(cols, rows, m) : mm_tiled_ws(rows, cols, m);
+    if (!mm_few(rows, cols, m, forward)) return forward ? mm_tiled_ws(cols, rows, m, true) : mm_tiled_ws(rows, cols, m, false);
     if (forward) return 0;
     const int parts = back_plan(rows, cols, m).parts;
     return parts > 1 ? size_t(parts) * size_t(m) * size_t(cols) * sizeof(float) : 0;

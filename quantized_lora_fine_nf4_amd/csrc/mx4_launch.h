@@ -24,8 +24,8 @@ hipError_t launch_matmul(int dtype, const uint8_t* codes, const uint8_t* scales,
 
 // Their tiled kernels (k_mx4_mm.hip), for all but few tokens; a function of the
 // reduction's length and the output's columns.
-size_t mm_tiled_ws(int64_t kred, int64_t ncol, int64_t m);
-double mm_tiled_us(int64_t kred, int64_t ncol, int64_t m);   // about how long they take
+size_t mm_tiled_ws(int64_t kred, int64_t ncol, int64_t m, bool forward);
+double mm_tiled_us(int64_t kred, int64_t ncol, int64_t m, bool forward);   // about how long they take
 hipError_t launch_mm_tiled(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                            bool forward, const void* x, int64_t m, void* out, int out_kind, float* part, hipStream_t s);
 

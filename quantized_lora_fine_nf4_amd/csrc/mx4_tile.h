@@ -26,8 +26,8 @@ struct TilePlan {
 constexpr int kCus = 256;
 
 // Measured on this card, in us: a step of the reduction, and what a tile costs
-// besides (its start and its stores), for large tiles (one on each compute unit), for
-// small ones with one on each compute unit and for small ones with two.
+// besides (its start and its stores), for a round of large tiles (one on each compute
+// unit), for one of small tiles with one on each, and for one with two.
 struct TileCosts {
     double big_step, big_tile, one_step, one_tile, two_step, two_tile;
 };
