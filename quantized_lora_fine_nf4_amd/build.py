@@ -1,4 +1,5 @@
-"""Compile the HIP library ``libnf4.so`` for gfx950, in-tree.
+"""Compile the HIP library ``libnf4.so`` for gfx950, in-tree, the host-CPU pass
+``libnf4cpu.so`` and the Python calls' plain case ``_calls.so`` beside it.
 
 hipcc cross-compiles without a GPU, one process per source (the matmul files
 take about a minute each).  Flags: no fast-math and no FMA

@@ -470,9 +470,9 @@ BackPlan back_plan(int64_t rows, int64_t cols, int64_t m)
 }
 
 // Whether these kernels take a product, or the tiled ones: by the estimates, up to as many tokens as their grids are
-// made for (both in 16 bits: 100 tokens through 1024 x 1024 4.0 us, tiled 10.1; 64 through 4096 x 4096 14.0 and 15.1,
-// through 13824 x 5120 32.1 and 28.3; backward 300 through 512 x 512 5.3 and 8.7, 64 through 4096 x 4096 18.8 and
-// 14.3).  The tiled kernel of two operands in codes takes rows of 256 at least.
+// made for (forward: 100 tokens through 1024 x 1024 4.0 us, tiled 11.0; 64 through 4096 x 4096 14.0 and 13.5,
+// through 13824 x 5120 32.1 and 24.4; backward 300 through 512 x 512 5.3 and 8.1, 64 through 4096 x 4096 17.5 and
+// 14.3; in codes 64 through 4096 x 4096 8.2 and 11.5, through 13824 x 5120 19.6 and 16.6).  The tiled kernel of two operands in codes takes rows of 256 at least.
 constexpr int64_t kFewTokens = 4096;
 
 bool mm_few(int64_t rows, int64_t cols, int64_t m, bool forward)

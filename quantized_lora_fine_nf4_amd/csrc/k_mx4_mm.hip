@@ -3,8 +3,8 @@
 //
 // v_mfma_f32_32x32x16; a 256 x 256 output tile by four waves of 128 x 128, one per
 // SIMD.  A step is 64 of the reduction: x's rows (128 bytes each) and the weight's
-// codes go straight into one of three LDS buffers (one multiplied, one complete,
-// one on its way).  The codes leave LDS as codes: each wave converts the fragments
+// codes go straight into one of three or four LDS buffers (one multiplied, one
+// complete, the others on their way).  The codes leave LDS as codes: each wave converts the fragments
 // it multiplies, two values an instruction, in the shadow of the matrix
 // instructions; the weight is never written anywhere in 16 bits.
 //
@@ -15,7 +15,10 @@
 // Forward: lane (r, h) reads row r's 16 bytes of block h of the step, one scale
 // under which its four dwords become the fragments of the four sub-steps
 // (reduction index 32 h + 8 f + j).  Weight row TN r + c of a wave's is row r of its
-// tile c, so that a lane ends with TN consecutive columns.
+// tile c, so that a lane ends with TN consecutive columns.  The scales of twelve or
+// sixteen steps are loaded at once and a round ahead, so that a step waits by count
+// for what it reads and for no more: 7% of the large product, a quarter where a tile
+// has the compute unit alone.
 //
 // Backward the reduction runs over the weight's rows, whose scales differ.  The
 // transposing read gives lane (r, h) the bytes (two columns) of rows 32 h + 8 f + j,
@@ -29,14 +32,11 @@
 // with a permutation by the index itself; the products, which other things bound,
 // take the same time.
 //
-// 4096 tokens through 13824 x 5120 in bf16 take 473 us forward and 457 backward (1.22
-// and 1.27 PF; the library's product alone, of a weight in 16 bits, 487 and 628), 8192 x
-// 8192 x 8192 808 and 777.  The matrix cores are busy two thirds of the time: one wave a
-// SIMD waits at each step's barrier and at a tile's ends (12 us a round).  With operands
-// of zeros 8192 x 8192 x 8192 takes 622 us: the rest is the clock that the power leaves.
-// Eight waves of 128 x 64 took 3% longer, codes fetched four steps at once through
-// registers 3% too.  x comes through a buffer descriptor that ends with it: rows
-// past its end, and pieces past a row's end (offset kFar), arrive as zeros.
+// 4096 tokens through 13824 x 5120 in bf16 take 445 us forward and 459 backward (1.30
+// and 1.26 PF; the library's product alone, of a weight in 16 bits, 487 and 628), 8192 x
+// 8192 x 8192 791 and 777.  What is left is one wave a SIMD that waits at each step's
+// barrier, a tile's ends (12 us a round), and power: with operands of zeros 8192 x 8192
+// x 8192 takes 575 of 743 us forward.  Eight waves of 128 x 64 took 3% longer.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -112,6 +112,27 @@ def test_matmul4_on_whole_tiles(m, ncol, kred):
         assert untouched(buf)
 
 
+@pytest.mark.parametrize("rows", [136, 1032, 4104])
+@pytest.mark.parametrize("cols", [32, 64, 96, 160, 224, 256, 288, 704, 768, 800, 960, 1024, 1056, 1504, 1568, 2080])
+def test_matmul_around_rounds_of_scales(rows, cols):
+    """Tiles that have a compute unit alone, that share it, and large ones, with reductions that end before, at and after
+    a round of scales and with rows shorter than what is loaded of them at once; one row of NaN scales, and nothing of a
+    neighbour's in another one."""
+    m = 4200
+    g = gen(rows + cols)
+    codes, scales = matrix(rows, cols, g)
+    bad = rows // 2 + 1
+    scales[bad] = 255
+    w = values(codes, scales).float().to(BF16).double()
+    ok = torch.arange(rows, device="cuda") != bad
+    print_case("rounds of scales", m, rows, cols)
+    x = torch.randn(m, cols, generator=g, device="cuda").to(BF16)
+    buf, out = guarded(m, rows, BF16)
+    matmul(codes, scales, x, out)
+    check(out[:, ok], x.double(), w[ok].t().contiguous(), "forward")
+    assert torch.isnan(out[:, bad]).all() and untouched(buf)
+
+
 @pytest.mark.parametrize("rows,cols", [(1032, 544), (4096, 4096), (520, 6176), (2048, 224)])
 def test_every_number_of_few_tokens(rows, cols):
     """All the token counts at which another kernel, tile or split may begin."""
