@@ -98,6 +98,12 @@ def test_matmul_arguments():
     assert call(x=FAKE + 2) == q.NF4_E_ALIGN
     assert call4(xc=None) == q.NF4_E_ARG and call4(xs=None) == q.NF4_E_ARG
     assert call4(xc=FAKE + 8) == q.NF4_E_ALIGN
+    # a side of 2^22 and more, and over 2^38 outputs (of the product or of its gradient)
+    for kw in ({"rows": 1 << 22, "cols": 32}, {"rows": 8, "cols": 1 << 22}, {"rows": 8, "cols": (1 << 13) + 32, "m": 1 << 25},
+               {"rows": (1 << 13) + 8, "cols": 32, "m": 1 << 25}):
+        assert call(**kw) == call(back=1, **kw) == call4(**kw) == q.NF4_E_ARG, kw
+        rows, cols, n = kw["rows"], kw["cols"], kw.get("m", 4)
+        assert q.mx4_matmul_workspace_bytes(rows, cols, False, n) == q.mx4_matmul4_workspace_bytes(rows, cols, n) == 0
     m = 4
     for back in (0, 1):
         if q.mx4_matmul_workspace_bytes(4096, 2048, back, m):
