@@ -408,9 +408,9 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
 
 // k_few's time in us: for each round of a workgroup on every compute unit 1.5, 0.15 for
 // each of a wave's tiles and 30 ns (22 with x in codes) for each load instruction of its
-// waves (64 lanes on 64 lines).  kRT x kMT tiles of 16 x 16 a wave,
-// the cheapest (4096 x 4096, 4 tokens: 1 x 1 5.7, 2 x 1 7.5; 13824 x 5120, 16
-// tokens: 4 x 1 16.1, 2 x 1 20.5, 1 x 1 29.6).
+// waves (64 lanes on 64 lines).  kRT x kMT tiles of 16 x 16 a wave, the cheapest (4096 x
+// 4096, 4 tokens: 1 x 1 5.7, 2 x 1 7.5; 13824 x 5120, 16 tokens: 4 x 1 16.1, 2 x 1 20.5,
+// 1 x 1 29.6).
 // Rows of one run need one wave, and many of those fit a compute unit at once.
 constexpr int64_t kOneWave = 512;
 
@@ -472,7 +472,8 @@ BackPlan back_plan(int64_t rows, int64_t cols, int64_t m)
 // Whether these kernels take a product, or the tiled ones: by the estimates, up to as many tokens as their grids are
 // made for (forward: 100 tokens through 1024 x 1024 4.0 us, tiled 11.0; 64 through 4096 x 4096 14.0 and 13.5,
 // through 13824 x 5120 32.1 and 24.4; backward 300 through 512 x 512 5.3 and 8.1, 64 through 4096 x 4096 17.5 and
-// 14.3; in codes 64 through 4096 x 4096 8.2 and 11.5, through 13824 x 5120 19.6 and 16.6).  The tiled kernel of two operands in codes takes rows of 256 at least.
+// 14.3; in codes 64 through 4096 x 4096 8.2 and 11.5, through 13824 x 5120 19.6 and 16.6).  The tiled kernel of two
+// operands in codes takes rows of 256 at least.
 constexpr int64_t kFewTokens = 4096;
 
 bool mm_few(int64_t rows, int64_t cols, int64_t m, bool forward)

@@ -120,8 +120,8 @@ constexpr int kVmcnt0 = 0x0f70;   // s_waitcnt: vector memory only, none outstan
 
 // READS LDS reads, VALU vector instructions and LOADS loads spread over N matrix
 // instructions, the reads over the first three quarters: the next sub-step begins
-// with what they bring.  Four waves share the LDS and the address unit, and what is bunched waits
-// there while the matrix cores are idle.
+// with what they bring.  Four waves share the LDS and the address unit, and what is
+// bunched waits there while the matrix cores are idle.
 template <int N, int READS, int VALU, int LOADS, int I = 0>
 __device__ __forceinline__ void spread()
 {
