@@ -269,6 +269,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
         }
     };
 
+    // Steps left over by the buffers' turns come after the loop (600 tokens through 4232 x 544, nine steps: 9.0 us, with
+    // twelve 10.2).  The large tile's sums leave no registers for a second way out of it (4096 tokens through 13824 x 5120
+    // 515 us for 451): there they are followed by steps of zeros.
+    constexpr bool kTail = TM < 4;
     Eights ls, ls0;
     load_scales(ls0, first);
     load_scales(ls, first + kQ);
@@ -301,7 +305,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
             load_scales(ls, base + 2 * kQ);
         }
         const int end = base + kQ < last ? base + kQ : last;
-        for (int step = base; step < end; step += NB) {
+        for (int step = base; step + (kTail ? NB - 1 : 0) < end; step += NB) {
             if constexpr (NB == 4) {
                 body(b0, b1, b3, step);
                 body(b1, b2, b0, step + 1);
@@ -311,6 +315,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
                 body(b0, b1, b2, step);
                 body(b1, b2, b0, step + 1);
                 body(b2, b0, b1, step + 2);
+            }
+        }
+    }
+    if constexpr (kTail) {
+        const int left = (last - first) % NB, step = last - left;
+        if (left > 0) {
+            body(b0, b1, NB == 4 ? b3 : b2, step);
+            if (left > 1) {
+                body(b1, b2, b0, step + 1);
+                if (NB == 4 && left > 2) body(b2, b3, b1, step + 2);
             }
         }
     }
@@ -496,10 +510,18 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm_back(MmArgs g)
     read_sub(b0, 0, 0);
     read_sub(b0, 1, 1);
     decode(0, 0);
-    for (int step = first; step < last; step += 3) {
+    constexpr bool kTail = TM < 4;   // as forward (333 tokens through 8192 x 2048 25.6 us for 26.5)
+    for (int step = first; step + (kTail ? 2 : 0) < last; step += 3) {
         body(b0, b1, b2, step);
         body(b1, b2, b0, step + 1);
         body(b2, b0, b1, step + 2);
+    }
+    if constexpr (kTail) {
+        const int left = (last - first) % 3, step = last - left;
+        if (left > 0) {
+            body(b0, b1, b2, step);
+            if (left > 1) body(b1, b2, b0, step + 1);
+        }
     }
     __builtin_amdgcn_s_waitcnt(kVmcnt0);   // nothing may come into LDS after the end
     store_tile<TM, TN, TN == 4>(acc, g.out, g.part, g.kind, g.grid, part, g.m, g.ncol, g.ldo, m0, n0, wm, wn, r, h);
@@ -523,7 +545,7 @@ hipError_t mm_go(int dtype, bool forward, const MmArgs& a, hipStream_t s)
 // Backward and forward.  Forward up to 256 small tiles have four buffers and a compute unit each, more of them three
 // and share it in pairs (128 tokens through 32768 x 4096 in 256 tiles 34.6 us, with three buffers 42.8; 256 in 512
 // tiles 61 in pairs, 66 one after another).  Backward the same gains nothing (333 tokens through 8192 x 2048 24.5 and
-// 26.5, but 300 through 5120 x 13824 72 and 64).
+// 25.6, but 300 through 5120 x 13824 72 and 64).
 constexpr TileCosts kCosts[2] = {{1.58, 12.0, 0.67, 3.2, 0.98, 7.0}, {1.44, 13.0, 0.45, 3.3, 0.85, 7.0}};
 
 TilePlan mm_plan(int64_t kred, int64_t ncol, int64_t m, bool forward, double* us = nullptr)

@@ -209,10 +209,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm4(Mm4Args g)
     begin(b0);
     fetch_scales(clamp(first + 1));
     fetch(b1, clamp(first + 1), Zero{}, Third{});
-    // pairs of steps: an odd one is followed by one under scales of 0
-    for (int step = first; step < last; step += 2) {
+    // Pairs of steps, and an odd one by itself (600 tokens through 4232 x 544 6.8 us, with a fourth step 7.5).  The large
+    // tile's sums leave no registers for another way out (4096 through 13824 x 5120 192 us for 186): there an odd one is
+    // followed by one under scales of 0.
+    constexpr bool kTail = TM < 4;
+    for (int step = first; step + kTail < last; step += 2) {
         body(b0, b1, step);
         body(b1, b0, step + 1);
+    }
+    if constexpr (kTail) {
+        if ((last - first) % 2) body(b0, b1, last - 1);
     }
     __builtin_amdgcn_s_waitcnt(kVmcnt0);   // nothing may come into LDS after the end
 #undef MX4_MULTIPLY

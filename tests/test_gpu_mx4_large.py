@@ -133,6 +133,38 @@ def test_matmul_around_rounds_of_scales(rows, cols):
     assert torch.isnan(out[:, bad]).all() and untouched(buf)
 
 
+@pytest.mark.parametrize("m", [600, 1500, 4200])
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 6, 7, 9, 11, 13])
+def test_every_end_of_the_buffers_turns(steps, m):
+    """Reductions of so many steps, and of so many whole ones and a part of one: forward and backward (steps of 64) and
+    of both operands in codes (256), with a NaN in every matrix's neighbourhood and not in it."""
+    g = gen(31 * steps + m)
+    for short in (0, 32):
+        k64, k256, n = 64 * steps - short, 256 * steps - 3 * short, 4232
+        print_case("ends", m, steps, short)
+        codes, scales = matrix(n, k64, g)
+        x = torch.full((m + 1, k64), float("nan"), dtype=BF16, device="cuda")[:m]
+        x.copy_(torch.randn(m, k64, generator=g, device="cuda"))
+        buf, out = guarded(m, n, BF16)
+        matmul(codes, scales, x, out)
+        check(out, x.double(), values(codes, scales).double().t().contiguous(), "forward")
+        assert untouched(buf)
+        # backward the reduction is the weight's rows, eights of them
+        n = 4224
+        codes, scales = matrix(k64, n, g)
+        buf, out = guarded(m, n, BF16)
+        matmul(codes, scales, x, out, back=True)
+        check(out, x.double(), values(codes, scales).double(), "backward")
+        assert untouched(buf)
+        n = 4232
+        codes, scales = matrix(n, k256, g)
+        xc, xs = matrix(m, k256, g)
+        buf, out = guarded(m, n, BF16)
+        matmul4(codes, scales, xc, xs, out)
+        check(out, values(xc, xs).double(), values(codes, scales).double().t().contiguous(), "codes")
+        assert untouched(buf)
+
+
 @pytest.mark.parametrize("rows,cols", [(1032, 544), (4096, 4096), (520, 6176), (2048, 224)])
 def test_every_number_of_few_tokens(rows, cols):
     """All the token counts at which another kernel, tile or split may begin."""
