@@ -43,8 +43,9 @@ extern "C" {
 nf4_status mx4_quantize(const void* x, int64_t rows, int64_t cols, int32_t dtype, uint8_t* codes,
                         uint8_t* scales, double* err, void* ws, size_t ws_bytes, hipStream_t stream);
 
-/* The values of codes and scales in dtype, each rounded once (fp16: infinity
- * beyond its range).  codes and out 16-byte aligned. */
+/* The values of codes and scales in dtype, each rounded once (infinity beyond its
+ * range: fp16's, and in bf16 4 and 6 under scale 2^126, 2 to 6 under 2^127).  codes
+ * and out 16-byte aligned. */
 nf4_status mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                           int32_t dtype, void* out, hipStream_t stream);
 
@@ -54,10 +55,10 @@ nf4_status mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t r
  * x row-major in dtype, W's values rounded to dtype (as mx4_dequantize), sums
  * fp32 on the matrix cores; out row-major, fp32 (out_fp32 = 1) or dtype rounded
  * once.  rows a multiple of 8 and cols of 32 (else NF4_E_UNSUPPORTED), each
- * below 2^22; 1 <= m <= 2^25; m times the larger side at most 2^38.  x, codes
- * and out 16-byte aligned; out must not overlap the operands.  ws:
- * mx4_matmul_workspace_bytes(rows, cols, backward, m), 256-byte aligned, may be
- * NULL where that is 0.  With few output tiles the reduction is split and the
+ * below 2^22 and their product below 2^40; 1 <= m <= 2^25; m times the larger side
+ * at most 2^38.  x, codes and out 16-byte aligned; out must not overlap the
+ * operands.  ws: mx4_matmul_workspace_bytes(rows, cols, backward, m), 256-byte
+ * aligned, may be NULL where that is 0.  With few output tiles the reduction is split and the
  * parts are added in a fixed order.  A value that is not finite acts as in fp32
  * arithmetic, in its own row and column of the result only. */
 nf4_status mx4_matmul(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
@@ -65,9 +66,12 @@ nf4_status mx4_matmul(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                       int32_t out_fp32, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* The forward product with both operands in this form: out[m x rows] = x W^T,
- * x [m x cols] as xcodes and xscales.  Products are exact and sums fp32 on the
- * matrix cores.  out: fp32 (out_fp32 = 1) or dtype rounded once.  Limits and
- * alignment as for mx4_matmul, xcodes 16-byte aligned too.  ws:
+ * x [m x cols] as xcodes and xscales.  Sums are fp32 on the matrix cores.  The
+ * product of two values, scales included, comes into them unrounded within fp32's
+ * range, subnormal numbers among it; what is far below the smallest of those counts
+ * as 0, what is past the largest number as an infinity.  A value past the range (6
+ * under scale 254) times 0 is 0.  out: fp32 (out_fp32 = 1) or dtype rounded once.
+ * Limits and alignment as for mx4_matmul, xcodes 16-byte aligned too.  ws:
  * mx4_matmul4_workspace_bytes(rows, cols, m). */
 nf4_status mx4_matmul4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                        const uint8_t* xcodes, const uint8_t* xscales, int64_t m, int32_t dtype,
