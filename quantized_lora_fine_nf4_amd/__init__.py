@@ -211,7 +211,8 @@ class _NoCalls:
 
 
 def _load_calls():
-    """The module that makes plain calls without Python's checks (csrc/py_calls.cpp), once."""
+    """The module that makes plain calls without Python's checks (csrc/py_calls.cpp), once.  Where it cannot be used
+    the first call says so."""
     global _plain
     import torch
     L = lib()
@@ -220,8 +221,11 @@ def _load_calls():
         at = [ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "nf4_layer_norm", "nf4_layer_norm_grad", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_matmul4")]
         native.setup(*at, torch._C._cuda_getCurrentRawStream)
-    except (ImportError, AttributeError):
+    except (ImportError, AttributeError) as e:
         native = _NoCalls
+        import warnings
+        warnings.warn(f"the compiled module of the plain calls cannot be used, small calls will be slower ({e}); "
+                      "python -m quantized_lora_fine_nf4_amd.build builds it", RuntimeWarning, stacklevel=3)
     _plain = native
     return native
 
