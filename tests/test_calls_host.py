@@ -6,6 +6,7 @@ import sys
 import pytest
 import torch
 
+import __graft_entry__
 import quantized_lora_fine_nf4_amd as q
 from quantized_lora_fine_nf4_amd import build
 
@@ -46,3 +47,29 @@ def test_a_loaded_module_says_nothing(monkeypatch, recwarn):
     monkeypatch.setattr(q, "_plain", None)
     quantise()
     assert not [w for w in recwarn if issubclass(w.category, RuntimeWarning)]
+
+
+@pytest.mark.parametrize("why", ["compiler fails", "no compiler", "no torch"])
+def test_a_build_goes_on_without_it(why, monkeypatch, tmp_path, capsys):
+    path = tmp_path / "_calls.so"
+    path.write_bytes(b"of an older source")
+    monkeypatch.setattr(build, "CALLS_PATH", str(path))
+    if why == "no torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    else:
+        monkeypatch.setattr(build, "calls_command", lambda out: ["false" if why == "compiler fails" else str(tmp_path / "none")])
+    assert build.build_calls_if_possible() is None
+    assert not path.exists() and "was not built" in capsys.readouterr().err
+
+
+def test_the_build_entry_point_goes_on_without_it(monkeypatch, tmp_path, capsys):
+    """With every other part's build taken as done."""
+    import oracle
+    import synth
+    monkeypatch.setattr(build, "CALLS_PATH", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(build, "calls_command", lambda out: ["false"])
+    for module, name in ((build, "build"), (build, "build_cpu"), (oracle, "build"), (synth, "build")):
+        monkeypatch.setattr(module, name, lambda **kw: None)
+    __graft_entry__.build()
+    said = capsys.readouterr()
+    assert "was not built" in said.err and "built" in said.out
