@@ -40,6 +40,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "mx4_format.h"
 #include "mx4_launch.h"
 #include "mx4_sum.h"
@@ -81,6 +83,8 @@ struct Buffer {
     u32x4 w[64 * TN * 2];       // codes: 64 TN rows of 32 bytes
 };
 
+struct NoBuffer {};             // in the fourth one's place
+
 // Scales come kQ steps at a time, through registers, while the steps before them are
 // multiplied: one load a step would have to be waited for with the step's own.
 template <int TN, int NB>
@@ -106,8 +110,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
 {
     typedef Buffer<TM, TN> Buf;
     typedef Scales<TN, NB> Sc;
-    __shared__ Buf b0, b1, b2, b3;   // objects of their own, so that reads of one need not wait for what comes into another
+    __shared__ Buf b0, b1, b2;   // objects of their own, so that reads of one need not wait for what comes into another
+    __shared__ std::conditional_t<NB == 4, Buf, NoBuffer> b3;
     __shared__ Sc sc;
+    static_assert(NB * sizeof(Buf) + sizeof(Sc) < 160 * 1024, "a compute unit's LDS");
     constexpr int kBM = 64 * TM, kBN = 64 * TN;
     constexpr int kA = 2 * TM, kW = TN / 2;   // 16-byte pieces per thread and step
     int tm, tn, part;
@@ -321,10 +327,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_mm(MmArgs g)
     if constexpr (kTail) {
         const int left = (last - first) % NB, step = last - left;
         if (left > 0) {
-            body(b0, b1, NB == 4 ? b3 : b2, step);
+            if constexpr (NB == 4) body(b0, b1, b3, step);
+            else body(b0, b1, b2, step);
             if (left > 1) {
                 body(b1, b2, b0, step + 1);
-                if (NB == 4 && left > 2) body(b2, b3, b1, step + 2);
+                if constexpr (NB == 4) {
+                    if (left > 2) body(b2, b3, b1, step + 2);
+                }
             }
         }
     }
