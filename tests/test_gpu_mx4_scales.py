@@ -19,9 +19,11 @@ from mx4_ref import TINY, U16, U32
 
 pytestmark = pytest.mark.gpu
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
-# tokens, weight rows: one, two and four weight rows by four tokens, 16 x 16 tiles, small tiles that have a compute
-# unit alone and that share one, large tiles with small ones beside them
-SIZES = [(1, 1032), (7, 1032), (7, 4232), (16, 264), (48, 264), (333, 1032), (1500, 4232), (4200, 4232)]
+# tokens, weight rows, columns: one, two and four weight rows by four tokens, 16 x 16 tiles, workgroups that share a
+# compute unit backward, small tiles that have one alone and that share one, large tiles with small ones beside them
+SIZES = [(1, 1032, 2080), (3, 4232, 2080), (7, 1032, 2080), (7, 4232, 2080), (8, 4232, 2048), (12, 4232, 2080),
+         (16, 264, 2080), (16, 4104, 8224), (30, 8200, 2080), (48, 264, 2080), (48, 4104, 8224), (333, 1032, 2080),
+         (1500, 4232, 2080), (4200, 4232, 2080)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -105,13 +107,12 @@ def draw16(m, shift, dtype, e, seed):
 
 
 @pytest.mark.parametrize("back", [False, True], ids=["fwd", "back"])
-@pytest.mark.parametrize("m,rows", SIZES)
-def test_matmul_under_every_scale(m, rows, back):
+@pytest.mark.parametrize("m,rows,cols", SIZES)
+def test_matmul_under_every_scale(m, rows, cols, back):
     """All 255 scales in bfloat16 (subnormal weights against large tokens, the largest against small ones), and in
     float16 those around its range, whose weights it rounds to subnormals and to zero."""
-    cols = 2080
     for dtype, base, top, e in ((BF16, 0, 63, 50), (BF16, 64, 63, 0), (BF16, 128, 63, -45), (FP16, 100, 20, 8)):
-        print_case("mx4_matmul scales", m, rows, back, dtype, base)
+        print_case("mx4_matmul scales", m, rows, cols, back, dtype, base)
         codes, scales, a, b = weight(rows, cols, base, top, m + rows + base)
         x = draw16(m, a if back else b.repeat_interleave(32), dtype, e, m)
         w = values(codes, scales).to(FP32).to(dtype).double()
@@ -126,12 +127,11 @@ def test_matmul_under_every_scale(m, rows, back):
         check(out, x.double(), w if back else w.t().contiguous(), (dtype, base))
 
 
-@pytest.mark.parametrize("m,rows", SIZES)
-def test_matmul4_under_every_scale(m, rows):
+@pytest.mark.parametrize("m,rows,cols", SIZES)
+def test_matmul4_under_every_scale(m, rows, cols):
     """Small scales of one operand against large ones of the other, both ways round."""
-    cols = 2080
     for base, xbase in ((0, 190), (64, 127), (128, 63)):
-        print_case("mx4_matmul4 scales", m, rows, base)
+        print_case("mx4_matmul4 scales", m, rows, cols, base)
         codes, scales, _, b = weight(rows, cols, base, 63, m + rows + base)
         xc = torch.randint(0, 256, (m, cols // 2), generator=gen(m), dtype=torch.uint8, device="cuda")
         xs = xbase + steps(m, 63 if m > 1 else 0)[:, None] - b[None, :]
@@ -141,7 +141,7 @@ def test_matmul4_under_every_scale(m, rows):
         check(out, values(xc, xs), values(codes, scales).t().contiguous(), base)
 
 
-@pytest.mark.parametrize("m,rows", SIZES)
+@pytest.mark.parametrize("m,rows", [s[:2] for s in SIZES])
 def test_products_at_the_ends_of_fp32(m, rows):
     """What is far below fp32's smallest number is 0, what is past its largest an infinity of its sign.  One group of 32 is
     not 0 in each row, so that an infinity meets no other."""
@@ -174,7 +174,7 @@ def test_products_at_the_ends_of_fp32(m, rows):
     assert torch.equal(matmul(codes, scales, x, FP32, False).double(), (sign * float("inf")).expand(m, rows))
 
 
-@pytest.mark.parametrize("m,rows", SIZES)
+@pytest.mark.parametrize("m,rows", [s[:2] for s in SIZES])
 def test_sums_below_the_normal_range_of_fp32(m, rows):
     """Subnormal sums keep fp32's step there: each addition of K is within one such step, toward zero or nearest."""
     cols = 544
