@@ -471,9 +471,10 @@ nf4_status nf4_lora_grad(const void* u, const void* x, int64_t m, int64_t n, int
  *   out = (h - mean) rstd weight + bias, rstd = 1 / sqrt(variance + eps)
  * with the variance the mean of (h - mean)^2.  x, residual, out, total device
  * [m x n] of dtype, weight and bias [n] of dtype; stats device fp32 [m x 2],
- * written with mean and rstd of every token.  Sums and statistics are fp32;
- * out is rounded once.  out may be x (or residual), and total may be either;
- * out and total are two buffers.  1 <= m <= 2^25, n < 2^26, 0 <= eps finite
+ * written with mean and rstd of every token.  Sums and statistics are fp32 (a
+ * token whose squared differences add up past fp32's range has rstd 0 and out =
+ * bias); out is rounded once.  out may be x (or residual), and total may be
+ * either; out and total are two buffers.  1 <= m <= 2^25, n < 2^26, 0 <= eps finite
  * (else NF4_E_ARG), n a multiple of 8 (else NF4_E_UNSUPPORTED); all 16-byte
  * aligned, stats 8.  A value that is not finite acts in its own token only. */
 nf4_status nf4_layer_norm(const void* x, const void* residual, const void* weight, const void* bias,

@@ -173,3 +173,25 @@ def test_column_sums_of_more_long_rows_than_a_grid():
     dw, db, dx = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty_like(x)
     q.nf4_layer_norm_grad(dy, x, weight, stats, dx, dw, db, workspace(q.nf4_layer_norm_grad_workspace_bytes(m, n)))
     check_grad(dy, x, weight, stats, None, dx, dw, db, BF16)
+
+
+@pytest.mark.parametrize("n", [64, 520, 5120, 8200, 24584])
+def test_a_variance_past_fp32(n):
+    """Differences of 2^70, whose squares fp32 does not hold: rstd is 0, out the bias, and the gradient what comes past
+    the norm; the tokens beside it are as without it."""
+    print_case("nf4_layer_norm, variance past fp32", n)
+    m = 5
+    x, w, b = draw((m, n), BF16, n), draw((n,), BF16, 1), draw((n,), BF16, 2)
+    out, stats = torch.empty_like(x), torch.empty(m, 2, device="cuda")
+    q.nf4_layer_norm(x, w, b, out, stats)
+    big = x.clone()
+    big[2] = 2.0 ** 70 * (1 - 2 * (torch.arange(n, device="cuda") % 2))   # mean 0
+    got, st = torch.empty_like(x), torch.empty(m, 2, device="cuda")
+    q.nf4_layer_norm(big, w, b, got, st)
+    assert st[2].tolist() == [0, 0] and torch.equal(got[2], b)
+    keep = torch.arange(m, device="cuda") != 2
+    assert torch.equal(got[keep], out[keep]) and torch.equal(st[keep], stats[keep])
+    dy, r = draw((m, n), BF16, 3), draw((m, n), BF16, 4)
+    dx, dw, db = torch.empty_like(x), torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    q.nf4_layer_norm_grad(dy, big, w, st, dx, dw, db, workspace(q.nf4_layer_norm_grad_workspace_bytes(m, n)), residual=r)
+    assert torch.equal(dx[2], r[2]) and torch.isfinite(dw).all()
