@@ -20,8 +20,9 @@
 // consecutive columns.
 //
 // One token through 13824 x 5120 in bf16 takes 9.0 us (4.2 TB/s of codes), backward
-// 19.4, where the conversion of each byte under its own row's scale counts and the
-// parts' sum takes 4.
+// 19.5 to 19.9: 16.6 the kernel and 4.5 the parts' sum.  320 workgroups come to 256
+// compute units there; on those that have two, 18,400 vector instructions (4,600 a
+// SIMD) take about 8 us, and half of a wave's time is waiting.
 // With small weights these kernels need no second launch where the tiled ones split
 // their reduction, and take many tokens too.
 #include <hip/hip_runtime.h>
@@ -470,9 +471,10 @@ BackPlan back_plan(int64_t rows, int64_t cols, int64_t m)
 }
 
 // Whether these kernels take a product, or the tiled ones: by the estimates, up to as many tokens as their grids are
-// made for (forward: 100 tokens through 1024 x 1024 4.0 us, tiled 11.0; 64 through 4096 x 4096 14.0 and 13.5,
-// through 13824 x 5120 32.1 and 24.4; backward 300 through 512 x 512 5.3 and 8.1, 64 through 4096 x 4096 17.5 and
-// 14.3; in codes 64 through 4096 x 4096 8.2 and 11.5, through 13824 x 5120 19.6 and 16.6).  The tiled kernel of two
+// made for (forward: 100 tokens through 1024 x 1024 4.6 us, tiled 10.4; 64 through 4096 x 4096 14.1 and 15.8, where
+// the estimates are level and take the tiled one, through 13824 x 5120 32.2 and 25.6; backward 300 through 512 x 512 5.3
+// and 7.0, 64 through 4096 x 4096 17.5 and 15.8; in codes 64 through 4096 x 4096 8.3 and 13.7, through 13824 x 5120 19.7
+// and 17.0).  The tiled kernel of two
 // operands in codes takes rows of 256 at least.
 constexpr int64_t kFewTokens = 4096;
 

@@ -4,9 +4,9 @@
 // v_mfma_f32_32x32x16; a 256 x 256 output tile by four waves of 128 x 128, one per
 // SIMD.  A step is 64 of the reduction: x's rows (128 bytes each) and the weight's
 // codes go straight into one of three or four LDS buffers (one multiplied, one
-// complete, the others on their way).  The codes leave LDS as codes: each wave converts the fragments
-// it multiplies, two values an instruction, in the shadow of the matrix
-// instructions; the weight is never written anywhere in 16 bits.
+// complete, the others on their way).  The codes leave LDS as codes: each wave
+// converts the fragments it multiplies, two values an instruction, in the shadow of
+// the matrix instructions; the weight is never written anywhere in 16 bits.
 //
 // A step has four sub-steps of 16.  While one is multiplied, the next one's weight
 // is converted, its x read, and the codes of the one after it.  The barrier stands
@@ -27,16 +27,19 @@
 // wave's 128 columns lane r = 8 q + i has 32 q + 2 i, + 1, + 16, + 17 (one scale
 // group); neighbours exchange a pair at the end and hold four in a row.
 //
-// 16-byte pieces lie permuted by half their row's index, so that a read's lanes
-// touch all 64 banks (two rows of 128 bytes).  Reads alone run 1.9 times as fast as
-// with a permutation by the index itself; the products, which other things bound,
-// take the same time.
+// x's 16-byte pieces lie permuted by half their row's index, so that a read's lanes
+// touch all 64 banks (two rows of 128 bytes), and forward the codes' by an eighth of
+// it.  Reads alone run 1.9 times as fast as with a permutation by the index itself;
+// the products, which other things bound, take the same time.  The transposing reads
+// of the codes backward are not free of conflicts: 0.17 of the cycles that LDS is
+// busy, where forward there are none.
 //
 // 4096 tokens through 13824 x 5120 in bf16 take 445 us forward and 459 backward (1.30
 // and 1.26 PF; the library's product alone, of a weight in 16 bits, 487 and 628), 8192 x
-// 8192 x 8192 791 and 777.  What is left is one wave a SIMD that waits at each step's
-// barrier, a tile's ends (12 us a round), and power: with operands of zeros 8192 x 8192
-// x 8192 takes 575 of 743 us forward.  Eight waves of 128 x 64 took 3% longer.
+// 8192 x 8192 780 to 790 each.  What is left is one wave a SIMD that waits at each
+// step's barrier, a tile's ends (12 us a round), and power: with operands of zeros 8192
+// x 8192 x 8192 takes 621 us of 781 forward, 641 of 788 backward.  Eight waves of 128 x
+// 64 took 3% longer.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -553,8 +556,9 @@ hipError_t mm_go(int dtype, bool forward, const MmArgs& a, hipStream_t s)
 
 // Backward and forward.  Forward up to 256 small tiles have four buffers and a compute unit each, more of them three
 // and share it in pairs (128 tokens through 32768 x 4096 in 256 tiles 34.6 us, with three buffers 42.8; 256 in 512
-// tiles 61 in pairs, 66 one after another).  Backward the same gains nothing (333 tokens through 8192 x 2048 24.5 and
-// 25.6, but 300 through 5120 x 13824 72 and 64).
+// tiles 61 in pairs, 66 one after another).  Backward there are three: the same change was measured while both forms filled
+// the steps left over by the buffers' turns up with zeros (333 tokens through 8192 x 2048 24.5 us for 26.5; 300 through
+// 5120 x 13824, which are more tiles than compute units, 72 for 64), and not since they no longer do (25.5 to 27.6 now).
 constexpr TileCosts kCosts[2] = {{1.58, 12.0, 0.67, 3.2, 0.98, 7.0}, {1.44, 13.0, 0.45, 3.3, 0.85, 7.0}};
 
 TilePlan mm_plan(int64_t kred, int64_t ncol, int64_t m, bool forward, double* us = nullptr)

@@ -8,11 +8,13 @@
 // accumulator registers each) reads 128 KB from LDS a step and 64 KB come into it, for
 // 2,048 matrix cycles.  Eight waves of 128 x 64 would read half as much again.
 //
-// 8192 x 8192 x 8192 takes 263 to 280 us (3.9 to 4.2 PF); with operands of zeros 205, so a
-// quarter of it is the clock that the power leaves.  A round of tiles through 5120
-// columns takes 47 us: 3.0 until the first step is there, 39 for the 20 steps, 3.5 for
-// the stores and 1.3 until the next tile.  Those ends are why 4096 tokens through
-// 13824 x 5120 (3.4 rounds, 183 us) reach 3.2 PF.
+// 8192 x 8192 x 8192 takes 263 to 288 us (3.8 to 4.2 PF), with operands of zeros 205 to
+// 257.  A round of tiles through 5120 columns takes 47 to 49 us (zeros 41): 3.0 until the
+// first step is there, 39 for the 20 steps, 3.5 for the stores and 1.3 until the next
+// tile.  The steps' matrix instructions are 17 of the 39 at 2.4 GHz: with two buffers a
+// wave waits at each step's barrier for all that it has asked for, and nothing else is
+// on its SIMD.  That first, then a tile's ends, and power last are why 4096 tokens
+// through 13824 x 5120 (3.4 rounds, 183 us) reach 3.2 PF.
 //
 // A step is 256 columns: 128 bytes of codes and 8 scales of each row.  The codes go
 // straight to one of two LDS buffers (global_load_lds) while the other one is
