@@ -20,8 +20,8 @@
 // consecutive columns.
 //
 // One token through 13824 x 5120 in bf16 takes 9.0 us (4.2 TB/s of codes), backward
-// 19.5 to 19.9: 16.6 the kernel and 4.5 the parts' sum.  320 workgroups come to 256
-// compute units there; on those that have two, 18,400 vector instructions (4,600 a
+// 19.5 to 19.9: 15.6 the kernel and 4.5 the parts' sum.  320 workgroups come to 256
+// compute units there; on those that have two, 18,000 vector instructions (4,500 a
 // SIMD) take about 8 us, and half of a wave's time is waiting.
 // With small weights these kernels need no second launch where the tiled ones split
 // their reduction, and take many tokens too.

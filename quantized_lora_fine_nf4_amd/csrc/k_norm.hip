@@ -14,7 +14,7 @@
 // a lane, over the lanes of a wave, over the waves in wave order.  Rows past what
 // registers hold are read again instead (k_norm_long, k_norm_grad_long).
 //
-// 8192 x 5120 in bf16 with a residual: 62 us, 5.4 TB/s; the gradient 65 us, 5.3 TB/s,
+// 8192 x 5120 in bf16 with a residual: 62 us, 5.4 TB/s; the gradient 65 us, 5.2 TB/s,
 // and 5 us for the sum of the 256 workgroups' column sums (a copy reaches 5.2 TB/s).
 // 17 x 5120 3.3 us, what any launch of this size takes.  Rows past the registers, 1024 x
 // 24584 with a residual: 52 us (3.8 TB/s of what has to be read and written), the
