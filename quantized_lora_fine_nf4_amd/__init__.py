@@ -222,7 +222,7 @@ def _load_calls():
             "nf4_layer_norm", "nf4_layer_norm_grad", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_matmul4")]
         native.setup(*at, torch._C._cuda_getCurrentRawStream)
     except (ImportError, AttributeError) as e:
-        native = _NoCalls
+        _plain = native = _NoCalls   # before the warning, which may be an error
         import warnings
         warnings.warn(f"the compiled module of the plain calls cannot be used, small calls will be slower ({e}); "
                       "python -m quantized_lora_fine_nf4_amd.build builds it", RuntimeWarning, stacklevel=3)

@@ -2,6 +2,7 @@
 go on without it and the first one says so, a build without it goes on and says so."""
 import os
 import sys
+import warnings
 
 import pytest
 import torch
@@ -32,6 +33,14 @@ def test_the_first_call_without_it_says_so(no_module, recwarn):
     assert said[0].filename == __file__   # the caller's line
     quantise()
     assert len([w for w in recwarn if issubclass(w.category, RuntimeWarning)]) == 1
+
+
+def test_warnings_as_errors_stop_the_first_call_alone(no_module):
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(RuntimeWarning):
+            quantise()
+        quantise()
 
 
 def test_a_torch_without_the_raw_stream_says_so(monkeypatch):
